@@ -327,6 +327,41 @@ moe_status_t moe_layer_region(moe_layer_t* layer, int32_t region, void** dptr, s
 /* The tactic chosen at create time. tactic: [host out]. */
 moe_status_t moe_layer_tactic(const moe_layer_t* layer, moe_tactic_t* tactic);
 
+/* Element types of the norm's residual stream and weight. */
+enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 };
+
+typedef struct {
+  int32_t hidden;         /* H, multiple of 128, <= 16384 */
+  float eps;              /* added to the mean square; finite, >= 0 */
+  int32_t residual_type;  /* MOE_TYPE_* of residual and residual_out */
+  int32_t weight_type;    /* MOE_TYPE_* of weight */
+} moe_norm_config_t;
+
+/* Residual addition, RMS norm and e4m3 quantisation of num_tokens rows:
+ *   s = x + residual,  y = s * rsqrt(mean(s^2) + eps) * weight,
+ *   scale = max|y| / 448 per 128 columns, code = e4m3 RNE_sat(y / scale).
+ * codes and scales are what moe_stage_inputs and moe_layer_decode take as
+ * prequantised rows.  Every output is rounded once, from FP32 values: the
+ * codes are those of y, not of the BF16 row.
+ *  x              device bfloat16 [T, H], rows x_stride elements apart.
+ *  residual       device [T, H] of residual_type, rows residual_stride
+ *                 elements apart; NULL: s = x.
+ *  weight         device [H] of weight_type.
+ *  codes, scales  device e4m3 [T, H] and float32 [T, H/128], contiguous;
+ *                 both NULL when only the BF16 rows are wanted.
+ *  y_bf16         device bfloat16 [T, H], contiguous, or NULL.
+ *  residual_out   device [T, H] of residual_type: s, or NULL.
+ * Strides are at least H and whole 16-byte pieces (of no account for one
+ * row); pointers are 16-byte aligned (codes 8, scales 4).  A row is read
+ * before any of it is written, so residual_out may be residual with the same
+ * stride, and y_bf16 may be x with stride H.  A block of y with a NaN or an
+ * infinity gets a NaN or infinite scale and NaN codes; an all-zero block
+ * scale 0 and zero codes.  num_tokens 0 launches nothing. */
+moe_status_t moe_rms_norm_quant(const moe_norm_config_t* cfg, const void* x, int64_t x_stride, const void* residual,
+                                int64_t residual_stride, const void* weight, int32_t num_tokens, uint8_t* codes,
+                                float* scales, void* y_bf16, void* residual_out, int64_t residual_out_stride,
+                                void* stream);
+
 /* Optional per-kernel timing with HIP events recorded around the launches
  * of the selected kernel classes on the launch stream.  kernel_mask: bit
  * (1 << MOE_KERNEL_*) per class to time, MOE_PROFILE_ALL for all of them,

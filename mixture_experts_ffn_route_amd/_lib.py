@@ -42,6 +42,8 @@ MOE_FLAG_PERSISTENT_FFN = 16
 MOE_FLAG_BF16_GATEUP = 32
 MOE_FLAG_NO_STREAM = 64
 MOE_FLAG_STREAM_FC1 = 128
+MOE_TYPE_BF16 = 0
+MOE_TYPE_F32 = 1
 MOE_DEV_BAD_EXPERT = 1
 MOE_DEV_DUPLICATE = 2
 MOE_DEV_NONFINITE = 4
@@ -61,7 +63,7 @@ EXPORTS = (
     "moe_workspace_query", "moe_layer_create", "moe_stage_inputs", "moe_layer_forward",
     "moe_layer_forward_noalloc", "moe_read_status", "moe_layer_region", "moe_layer_tactic", "moe_profile_enable",
     "moe_profile_read", "moe_layer_destroy", "moe_token_bucket", "moe_status_string",
-    "moe_last_error", "moe_debug_slot_timers",
+    "moe_last_error", "moe_debug_slot_timers", "moe_rms_norm_quant",
 )
 
 
@@ -88,6 +90,10 @@ class moe_tactic_t(Structure):
         ("grid_fc2", c_int32), ("row_cap", c_int32), ("max_m_tiles", c_int32), ("tile_order", c_int32),
         ("stream_depth_fc1", c_int32), ("stream_depth_fc2", c_int32),
     ]
+
+
+class moe_norm_config_t(Structure):
+    _fields_ = [("hidden", c_int32), ("eps", c_float), ("residual_type", c_int32), ("weight_type", c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -121,6 +127,8 @@ def _load() -> ctypes.CDLL:
         "moe_profile_read": (i32, [vp, POINTER(c_double), POINTER(c_int64)]),
         "moe_layer_destroy": (i32, [vp]),
         "moe_debug_slot_timers": (i32, [vp, i32]),
+        "moe_rms_norm_quant": (i32, [POINTER(moe_norm_config_t), vp, c_int64, vp, c_int64, vp, i32, vp, vp, vp, vp,
+                                     c_int64, vp]),
         "moe_token_bucket": (i32, [i32]),
         "moe_status_string": (c_char_p, [i32]),
         "moe_last_error": (c_char_p, []),
@@ -234,3 +242,12 @@ def moe_debug_slot_timers():
     buf = (ctypes.c_uint64 * MOE_SLOT_TIMER_WORDS)()
     _check(_lib.moe_debug_slot_timers(ctypes.cast(buf, c_void_p), MOE_SLOT_TIMER_WORDS))
     return list(buf)
+
+
+def moe_rms_norm_quant(hidden: int, eps: float, residual_type: int, weight_type: int, x: int, x_stride: int,
+                       residual: int, residual_stride: int, weight: int, num_tokens: int, codes: int, scales: int,
+                       y_bf16: int, residual_out: int, residual_out_stride: int, stream: int = 0) -> None:
+    cfg = moe_norm_config_t(hidden, eps, residual_type, weight_type)
+    _check(_lib.moe_rms_norm_quant(ctypes.byref(cfg), x, x_stride, residual or None, residual_stride, weight,
+                                   num_tokens, codes or None, scales or None, y_bf16 or None, residual_out or None,
+                                   residual_out_stride, stream))

@@ -37,6 +37,7 @@ SOURCES = [
     "moe_combine.hip",
     "moe_weights.hip",
     "moe_noalloc.hip",
+    "moe_norm.hip",
 ]
 
 # Packed FP32 VALU ops are disabled for all device code.

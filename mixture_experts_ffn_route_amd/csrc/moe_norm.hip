@@ -1,0 +1,276 @@
+// Residual addition, RMS norm and e4m3 quantisation of activation rows, in
+// one pass over them: what a decoder layer does between its attention and
+// this layer, with the output in the form moe_stage_inputs and
+// moe_layer_decode take.
+//
+//   s = x + residual                       (FP32)
+//   y = s * rsqrt(mean(s^2) + eps) * weight
+//   per 128 columns: scale = max|y| / 448, code = e4m3 RNE_sat(y / scale)
+//
+// Rounding happens once per output: the new residual is s, the BF16 row is y
+// and the codes are y / scale, each from the FP32 values (the codes are not
+// taken from the rounded BF16 row).  The sum of squares is kept in FP64, so
+// that no finite row overflows or vanishes in it; everything else is FP32.
+//
+// HBM bounds it.  One workgroup per row at a time; a thread owns C chunks of
+// 8 consecutive columns (16 bytes of BF16) and keeps s in registers between
+// the sum and the output, so every input is read once.  A 128-column block is
+// one chunk of 16 consecutive lanes, a DPP row, so the block maximum never
+// leaves the wave.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxWaves = 16;
+
+struct NormArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  const void* residual;  // null: none
+  int64_t residual_stride;
+  const void* weight;
+  int32_t tokens, hidden;
+  float eps;
+  uint8_t* codes;
+  float* scales;
+  uint16_t* y;         // null: not wanted
+  void* residual_out;  // null: not wanted
+  int64_t residual_out_stride;
+};
+
+// Maximum over a DPP row (16 consecutive lanes), in every lane of it.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // quad_perm: lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // quad_perm: lane ^ 2
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror: other quad
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // row_mirror: other half
+}
+
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, float v[8]) {
+  const u32x4 r = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_to_f32(r[i] & 0xffffu);
+    v[2 * i + 1] = bf16_to_f32(r[i] >> 16);
+  }
+}
+__device__ __forceinline__ void load8_f32(const float* p, float v[8]) {
+  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float v[8]) {
+  if constexpr (F32)
+    load8_f32(static_cast<const float*>(base) + at, v);
+  else
+    load8_bf16(static_cast<const uint16_t*>(base) + at, v);
+}
+__device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
+  return u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+}
+
+// e4m3 codes of 8 values of a block with scale s: those of the quotients
+// v / s.  A quotient is formed from a reciprocal and one correction step; a
+// scale below 2^-90, whose remainders could underflow, divides.  A block
+// that holds a NaN or an infinity has such a scale and NaN codes.
+__device__ __forceinline__ u32x2 quant8(const float v[8], float s) {
+  if (s == 0.0f) return u32x2{0u, 0u};
+  if (!isfinite(s)) return u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
+  float q[8];
+  if (s >= 0x1p-90f) {
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = v[i] * inv;
+      q[i] = copysignf(fmaf(fmaf(-q0, s, v[i]), inv, q0), v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
+  }
+  u32x2 w;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lo = cvt2_e4m3(q[4 * j], q[4 * j + 1], 0, false);
+    w[j] = (uint32_t)cvt2_e4m3(q[4 * j + 2], q[4 * j + 3], lo, true);
+  }
+  return w;
+}
+
+// R: 0 no residual, 1 BF16, 2 FP32.  WF32: FP32 weight.
+template <int C, int R, bool WF32>
+__global__ __launch_bounds__(1024) void rms_norm_quant_kernel(NormArgs a) {
+  __shared__ double part[2][kMaxWaves];
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int wave = tid >> 6, waves = nt >> 6;
+  const int chunks = a.hidden >> 3;
+  float w[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int j = c * nt + tid;
+    if (j < chunks) load8<WF32>(a.weight, (int64_t)j * 8, w[c]);
+  }
+  int parity = 0;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x, parity ^= 1) {
+    float s[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = c * nt + tid;
+      if (j < chunks) {
+        load8_bf16(a.x + t * a.x_stride + j * 8, s[c]);
+        if constexpr (R != 0) {
+          float r[8];
+          load8<R == 2>(a.residual, t * a.residual_stride + j * 8, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[c][i] += r[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[c][i] = 0.0f;
+      }
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fma((double)s[c][i], (double)s[c][i], sum);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
+    if ((tid & 63) == 0) part[parity][wave] = sum;
+    __syncthreads();  // the other parity's sums of the last row may still be read
+    sum = 0.0;
+    for (int i = 0; i < waves; ++i) sum += part[parity][i];
+    const float f = (float)(1.0 / sqrt(sum / a.hidden + (double)a.eps));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = c * nt + tid;
+      if (j >= chunks) continue;  // whole DPP rows: chunks and nt are multiples of 16
+      if constexpr (R != 0) {
+        if (a.residual_out) {
+          if constexpr (R == 2) {
+            f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.residual_out) + t * a.residual_out_stride + j * 8);
+            d[0] = f32x4{s[c][0], s[c][1], s[c][2], s[c][3]};
+            d[1] = f32x4{s[c][4], s[c][5], s[c][6], s[c][7]};
+          } else {
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.residual_out) + t * a.residual_out_stride + j * 8) =
+                pack8_bf16(s[c]);
+          }
+        }
+      }
+      float y[8];
+      uint32_t m = 0;  // maximum of |y| as bits: a NaN is larger than every number
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = s[c][i] * f * w[c][i];
+        m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+      }
+      if (a.y) *reinterpret_cast<u32x4*>(a.y + t * a.hidden + j * 8) = pack8_bf16(y);
+      if (a.codes) {
+        const float scale = __uint_as_float(row16_max(m)) / kE4m3Max;
+        *reinterpret_cast<u32x2*>(a.codes + t * a.hidden + j * 8) = quant8(y, scale);
+        if ((tid & 15) == 0) a.scales[t * (a.hidden >> 7) + (j >> 4)] = scale;
+      }
+    }
+  }
+}
+
+template <int C>
+int launch_c(const NormArgs& a, int r, bool wf32, dim3 grid, dim3 block, hipStream_t s) {
+#define MOE_NORM(R)                                                                             \
+  if (wf32)                                                                                     \
+    hipLaunchKernelGGL((rms_norm_quant_kernel<C, R, true>), grid, block, 0, s, a);              \
+  else                                                                                          \
+    hipLaunchKernelGGL((rms_norm_quant_kernel<C, R, false>), grid, block, 0, s, a)
+  if (r == 0) {
+    MOE_NORM(0);
+  } else if (r == 1) {
+    MOE_NORM(1);
+  } else {
+    MOE_NORM(2);
+  }
+#undef MOE_NORM
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+int launch_norm(const NormArgs& a, int r, bool wf32, hipStream_t s) {
+  const int chunks = a.hidden / 8;
+  // one chunk per thread up to 1024 of them (H = 8192), else two
+  const int c = chunks <= 1024 ? 1 : 2;
+  const int nt = ((chunks + c - 1) / c + 63) / 64 * 64;
+  const int grid = a.tokens < 65536 ? a.tokens : 65536;
+  return c == 1 ? launch_c<1>(a, r, wf32, dim3(grid), dim3(nt), s) : launch_c<2>(a, r, wf32, dim3(grid), dim3(nt), s);
+}
+
+bool valid_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_rms_norm_quant(const moe_norm_config_t* cfg, const void* x, int64_t x_stride,
+                                           const void* residual, int64_t residual_stride, const void* weight,
+                                           int32_t num_tokens, uint8_t* codes, float* scales, void* y_bf16,
+                                           void* residual_out, int64_t residual_out_stride, void* stream) {
+  moe::clear_error();
+  if (!cfg) return moe::fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  const int32_t H = cfg->hidden;
+  if (H <= 0) return moe::fail(MOE_ERR_INVALID_ARG, "hidden (%d) must be positive", H);
+  if (H % 128 || H > 16384)
+    return moe::fail(MOE_ERR_UNSUPPORTED, "hidden (%d) must be a multiple of 128, at most 16384", H);
+  if (!(cfg->eps >= 0.0f) || !isfinite(cfg->eps))
+    return moe::fail(MOE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!moe::valid_type(cfg->residual_type) || !moe::valid_type(cfg->weight_type))
+    return moe::fail(MOE_ERR_INVALID_ARG, "unknown residual_type %d or weight_type %d", cfg->residual_type,
+                     cfg->weight_type);
+  if (num_tokens < 0) return moe::fail(MOE_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_tokens == 0) return MOE_OK;  // tensors of no rows have no address
+  if (!codes != !scales) return moe::fail(MOE_ERR_INVALID_ARG, "codes and scales come together");
+  if (!codes && !y_bf16) return moe::fail(MOE_ERR_INVALID_ARG, "neither codes nor y_bf16 is wanted");
+  if (residual_out && !residual) return moe::fail(MOE_ERR_INVALID_ARG, "residual_out without a residual");
+  if (!x || !weight) return moe::fail(MOE_ERR_INVALID_ARG, "x and weight must be non-NULL");
+  if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)y_bf16 | (uintptr_t)residual_out) & 15)
+    return moe::fail(MOE_ERR_INVALID_ARG, "x, residual, weight, y and residual_out must be 16-byte aligned");
+  if (((uintptr_t)codes & 7) || ((uintptr_t)scales & 3))
+    return moe::fail(MOE_ERR_INVALID_ARG, "codes must be 8-byte and scales 4-byte aligned");
+  // rows of 16-byte pieces that do not overlap (a single row needs no stride)
+  const int per16 = cfg->residual_type == MOE_TYPE_F32 ? 4 : 8;
+  if (num_tokens > 1) {
+    if (x_stride < H || x_stride % 8) return moe::fail(MOE_ERR_INVALID_ARG, "x_stride %lld", (long long)x_stride);
+    if (residual && (residual_stride < H || residual_stride % per16))
+      return moe::fail(MOE_ERR_INVALID_ARG, "residual_stride %lld", (long long)residual_stride);
+    if (residual_out && (residual_out_stride < H || residual_out_stride % per16))
+      return moe::fail(MOE_ERR_INVALID_ARG, "residual_out_stride %lld", (long long)residual_out_stride);
+  }
+  moe::NormArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = x_stride;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.weight = weight;
+  a.tokens = num_tokens;
+  a.hidden = H;
+  a.eps = cfg->eps;
+  a.codes = codes;
+  a.scales = scales;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.residual_out = residual_out;
+  a.residual_out_stride = residual_out_stride;
+  const int r = !residual ? 0 : (cfg->residual_type == MOE_TYPE_F32 ? 2 : 1);
+  if (moe::launch_norm(a, r, cfg->weight_type == MOE_TYPE_F32, static_cast<hipStream_t>(stream)) != 0) {
+    const hipError_t e = hipGetLastError();
+    return moe::fail(MOE_ERR_HIP, "norm launch: %s", hipGetErrorString(e));
+  }
+  return MOE_OK;
+}
