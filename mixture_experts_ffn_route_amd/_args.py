@@ -1,0 +1,24 @@
+"""Argument checks shared by the torch wrappers."""
+
+from __future__ import annotations
+
+import torch
+
+# The current stream's handle of a device (torch.cuda.current_stream builds a
+# Stream object first, 2 us more a call).
+current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def check(t: torch.Tensor, name: str, shape, dtypes, device, strided: bool = False) -> None:
+    """Raises ValueError unless ``t`` has this shape, one of these types and
+    this device, and is contiguous (``strided``: along its last dimension)."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != device:
+        kinds = " or ".join(str(d) for d in dtypes)
+        raise ValueError(f"{name} must be {kinds} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    if not (t.is_contiguous() or (strided and t.stride(-1) == 1)):
+        raise ValueError(f"{name} must be contiguous" + (" along its last dimension" if strided else ""))
+
+
+def ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()

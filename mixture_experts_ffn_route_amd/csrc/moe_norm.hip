@@ -16,7 +16,11 @@
 // 8 consecutive columns (16 bytes of BF16) and keeps s in registers between
 // the sum and the output, so every input is read once.  A 128-column block is
 // one chunk of 16 consecutive lanes, a DPP row, so the block maximum never
-// leaves the wave.
+// leaves the wave.  The outputs are stored non-temporally: T=8192 H=2048 24.2
+// us against 30.8 with plain stores of codes and BF16 rows, T=4096 H=7168
+// 48.3 against 50.8.  At T=4096 H=7168 with a BF16 residual and every output
+// a call moves 265 MB in 48.3 us, 5.5 TB/s (a 2 GiB copy: 4.9); T=32768
+// without the BF16 rows 1652 MB in 295 us, 5.6 TB/s; T=1 takes 4.1 us.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -77,6 +81,10 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, float v[8]) 
     load8_f32(static_cast<const float*>(base) + at, v);
   else
     load8_bf16(static_cast<const uint16_t*>(base) + at, v);
+}
+template <typename T>
+__device__ __forceinline__ void store_nt(void* p, T v) {
+  __builtin_nontemporal_store(v, static_cast<T*>(p));
 }
 __device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
   return u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
@@ -161,12 +169,11 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(NormArgs a) {
       if constexpr (R != 0) {
         if (a.residual_out) {
           if constexpr (R == 2) {
-            f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.residual_out) + t * a.residual_out_stride + j * 8);
-            d[0] = f32x4{s[c][0], s[c][1], s[c][2], s[c][3]};
-            d[1] = f32x4{s[c][4], s[c][5], s[c][6], s[c][7]};
+            float* d = static_cast<float*>(a.residual_out) + t * a.residual_out_stride + j * 8;
+            store_nt(d, f32x4{s[c][0], s[c][1], s[c][2], s[c][3]});
+            store_nt(d + 4, f32x4{s[c][4], s[c][5], s[c][6], s[c][7]});
           } else {
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.residual_out) + t * a.residual_out_stride + j * 8) =
-                pack8_bf16(s[c]);
+            store_nt(static_cast<uint16_t*>(a.residual_out) + t * a.residual_out_stride + j * 8, pack8_bf16(s[c]));
           }
         }
       }
@@ -177,10 +184,10 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(NormArgs a) {
         y[i] = s[c][i] * f * w[c][i];
         m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
       }
-      if (a.y) *reinterpret_cast<u32x4*>(a.y + t * a.hidden + j * 8) = pack8_bf16(y);
+      if (a.y) store_nt(a.y + t * a.hidden + j * 8, pack8_bf16(y));
       if (a.codes) {
         const float scale = __uint_as_float(row16_max(m)) / kE4m3Max;
-        *reinterpret_cast<u32x2*>(a.codes + t * a.hidden + j * 8) = quant8(y, scale);
+        store_nt(a.codes + t * a.hidden + j * 8, quant8(y, scale));
         if ((tid & 15) == 0) a.scales[t * (a.hidden >> 7) + (j >> 4)] = scale;
       }
     }
@@ -207,8 +214,12 @@ int launch_c(const NormArgs& a, int r, bool wf32, dim3 grid, dim3 block, hipStre
 
 int launch_norm(const NormArgs& a, int r, bool wf32, hipStream_t s) {
   const int chunks = a.hidden / 8;
-  // one chunk per thread up to 1024 of them (H = 8192), else two
-  const int c = chunks <= 1024 ? 1 : 2;
+  // Chunks per thread: two from H = 4096 up, one below.  With one, a row of
+  // H = 7168 takes 14 waves, and two such workgroups leave a CU 4 wave slots
+  // idle (T=4096 57.8 us against 48.3; T=32768 399 against 295); with two, a
+  // row of H = 2048 has 2 waves (T=512 4.5 us against 4.0, T=8192 24.2
+  // against 24.6).  Four chunks were slower at both (51.2, 309; 5.4, 25.9).
+  const int c = chunks > 512 ? 2 : 1;
   const int nt = ((chunks + c - 1) / c + 63) / 64 * 64;
   const int grid = a.tokens < 65536 ? a.tokens : 65536;
   return c == 1 ? launch_c<1>(a, r, wf32, dim3(grid), dim3(nt), s) : launch_c<2>(a, r, wf32, dim3(grid), dim3(nt), s);

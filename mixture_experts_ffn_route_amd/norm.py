@@ -12,8 +12,10 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib as L
+from ._args import check, current_raw_stream, ptr
 
 _TYPES = {torch.bfloat16: L.MOE_TYPE_BF16, torch.float32: L.MOE_TYPE_F32}
+_BF16, _F32, _CODES = (torch.bfloat16,), (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
 
 
 class NormOutput(NamedTuple):
@@ -21,15 +23,6 @@ class NormOutput(NamedTuple):
     scale: Optional[torch.Tensor]     # float32 [T, H/128]
     y: Optional[torch.Tensor]         # bfloat16 [T, H]
     residual: Optional[torch.Tensor]  # [T, H], x + residual in the residual's type
-
-
-def _rows(t: torch.Tensor, name: str, shape, dtypes, device, strided: bool = False) -> torch.Tensor:
-    if t.shape != shape or t.dtype not in dtypes or t.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} of {dtypes} on {device}, got {tuple(t.shape)} {t.dtype} on "
-                         f"{t.device}")
-    if not (t.is_contiguous() or (strided and t.stride(-1) == 1)):
-        raise ValueError(f"{name} must be contiguous" + (" along its last dimension" if strided else ""))
-    return t
 
 
 def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -45,37 +38,43 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     """
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError("x must be a [T, H] device tensor")
-    T, H = x.shape
-    dev = x.device
-    if dev.index != torch.cuda.current_device():
+    shape, dev = x.shape, x.device
+    index = dev.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return rms_norm_quant(x, weight, residual, eps=eps, codes=codes, bf16=bf16, out=out)
-    _rows(x, "x", x.shape, (torch.bfloat16,), dev, True)
-    _rows(weight, "weight", (H,), _TYPES, dev)
+    T, H = shape
+    check(x, "x", shape, _BF16, dev, True)
+    check(weight, "weight", (H,), _TYPES, dev)
     if residual is not None:
-        _rows(residual, "residual", x.shape, _TYPES, dev, True)
+        check(residual, "residual", shape, _TYPES, dev, True)
     if out is None:
-        empty = torch.empty
-        out = NormOutput(empty((T, H), dtype=torch.uint8, device=dev) if codes else None,
-                         empty((T, H // 128), dtype=torch.float32, device=dev) if codes else None,
-                         empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
-                         None if residual is None else empty((T, H), dtype=residual.dtype, device=dev))
+        q = s = y = ro = None
+        if codes:
+            q = torch.empty(shape, dtype=torch.uint8, device=dev)
+            s = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+        if bf16:
+            y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if residual is not None:
+            ro = torch.empty(shape, dtype=residual.dtype, device=dev)
+        out = NormOutput(q, s, y, ro)
     else:
-        if out.codes is not None:
-            _rows(out.codes, "out.codes", x.shape, (torch.uint8, torch.float8_e4m3fn), dev)
-        if out.scale is not None:
-            _rows(out.scale, "out.scale", (T, H // 128), (torch.float32,), dev)
-        if out.y is not None:
-            _rows(out.y, "out.y", x.shape, (torch.bfloat16,), dev)
-        if out.residual is not None:
+        q, s, y, ro = out
+        if q is not None:
+            check(q, "out.codes", shape, _CODES, dev)
+        if s is not None:
+            check(s, "out.scale", (T, H // 128), _F32, dev)
+        if y is not None:
+            check(y, "out.y", shape, _BF16, dev)
+        if ro is not None:
             if residual is None:
                 raise ValueError("out.residual without a residual")
-            _rows(out.residual, "out.residual", x.shape, (residual.dtype,), dev, True)
-    r, ro = residual, out.residual
-    ptr = torch.Tensor.data_ptr
-    L.moe_rms_norm_quant(H, eps, _TYPES[r.dtype] if r is not None else 0, _TYPES[weight.dtype], ptr(x), x.stride(0),
-                         0 if r is None else ptr(r), 0 if r is None else r.stride(0), ptr(weight), T,
-                         0 if out.codes is None else ptr(out.codes), 0 if out.scale is None else ptr(out.scale),
-                         0 if out.y is None else ptr(out.y), 0 if ro is None else ptr(ro),
-                         0 if ro is None else ro.stride(0), torch.cuda.current_stream().cuda_stream)
+            check(ro, "out.residual", shape, (residual.dtype,), dev, True)
+    rtype = r = rs = ros = 0
+    if residual is not None:
+        rtype, r, rs = _TYPES[residual.dtype], residual.data_ptr(), residual.stride(0)
+        if ro is not None:
+            ros = ro.stride(0)
+    L.moe_rms_norm_quant(H, eps, rtype, _TYPES[weight.dtype], x.data_ptr(), x.stride(0), r, rs, weight.data_ptr(), T,
+                         ptr(q), ptr(s), ptr(y), ptr(ro), ros, current_raw_stream(index))
     return out
