@@ -362,6 +362,71 @@ moe_status_t moe_rms_norm_quant(const moe_norm_config_t* cfg, const void* x, int
                                 float* scales, void* y_bf16, void* residual_out, int64_t residual_out_stride,
                                 void* stream);
 
+/* Router scores. */
+enum {
+  MOE_SCORE_SOFTMAX = 0, /* softmax over all experts */
+  MOE_SCORE_SIGMOID = 1  /* a sigmoid per expert; the selection may add a bias */
+};
+
+typedef struct {
+  int32_t hidden;         /* H, multiple of 128, <= 16384 */
+  int32_t num_experts;    /* E of the whole model, 1..1024 */
+  int32_t top_k;          /* K, 1..8 (the layer takes 1, 2, 4, 6 and 8) */
+  int32_t score;          /* MOE_SCORE_* */
+  int32_t num_groups;     /* the experts form this many equal groups, 1..16 (1: no groups) */
+  int32_t top_groups;     /* groups whose experts can be chosen; they hold at least K experts */
+  int32_t renormalize;    /* 1: a token's K weights are divided by their sum */
+  float scale;            /* factor on the weights */
+  int32_t expert_base;    /* this GPU holds experts [expert_base, expert_base + local_experts) */
+  int32_t local_experts;
+} moe_router_config_t;
+
+typedef struct moe_router moe_router_t;
+
+/* Router: l = x W^T; score = softmax(l) or sigmoid(l); choice = score + bias
+ * (sigmoid), l (softmax, which orders as its scores do).  A group's value is
+ * the sum of its two largest choices (sigmoid) or its largest (softmax); the
+ * top_groups groups of the largest values stay, and the K largest choices
+ * among their experts are the token's, in descending order.  Ties go to the
+ * lowest group and expert; a NaN ranks below every number.  The weight of a
+ * chosen expert is its score, without the bias, divided by the K scores' sum
+ * with renormalize, times scale.
+ *
+ * The chosen experts are those of 64-bit arithmetic on the given x, W and
+ * bias, whatever the batch they come in: choices that lie within the FP32
+ * product's rounding errors of each other are computed again in FP64.  (Rows
+ * whose squared norm leaves float32's range go by their FP32 logits.)
+ *
+ * moe_router_workspace_query: device bytes for batches of up to max_rows
+ * tokens.  Host only. */
+moe_status_t moe_router_workspace_query(const moe_router_config_t* cfg, int32_t max_rows, size_t* ws_bytes);
+
+/* Bind the gate weights and the workspace.
+ *  weight     device bfloat16 [E, H]; copied into the workspace in the
+ *             kernels' order, and read in place where choices lie close: the
+ *             caller keeps it alive and unchanged while the handle exists.
+ *  bias       device float32 [E] or NULL, added to sigmoid scores for the
+ *             selection only; kept alive and unchanged too.
+ *  workspace  device, 256-byte aligned, ws_bytes >= the query's.
+ * The launches of one handle must not overlap on the device (its workspace
+ * holds the logits of the call in progress). */
+moe_status_t moe_router_create(const moe_router_config_t* cfg, int32_t max_rows, const void* weight,
+                               const float* bias, void* workspace, size_t ws_bytes, void* stream, moe_router_t** out);
+
+/* Route num_tokens rows (0 launches nothing).
+ *  x         device bfloat16 [T, H], rows x_stride elements apart (at least
+ *            H, whole 16-byte pieces), 16-byte aligned.
+ *  topk_idx  device int32 [T, K]: id - expert_base of this GPU's experts, -1
+ *            for the others -- what moe_stage_inputs and moe_layer_decode
+ *            take.
+ *  topk_w    device float32 [T, K].
+ *  ids       device int32 [T, K], or NULL: the ids in the whole model. */
+moe_status_t moe_router_forward(moe_router_t* router, const void* x, int64_t x_stride, int32_t num_tokens,
+                                int32_t* topk_idx, float* topk_w, int32_t* ids, void* stream);
+
+/* Release the handle (host memory only).  NULL is a no-op. */
+moe_status_t moe_router_destroy(moe_router_t* router);
+
 /* Optional per-kernel timing with HIP events recorded around the launches
  * of the selected kernel classes on the launch stream.  kernel_mask: bit
  * (1 << MOE_KERNEL_*) per class to time, MOE_PROFILE_ALL for all of them,

@@ -10,3 +10,4 @@ from . import _lib  # noqa: F401  (raises ImportError if the library is missing)
 from ._lib import MoEError  # noqa: F401
 from .layer import MoELayer  # noqa: F401
 from .norm import NormOutput, rms_norm_quant  # noqa: F401
+from .router import MoERouter  # noqa: F401

@@ -44,6 +44,8 @@ MOE_FLAG_NO_STREAM = 64
 MOE_FLAG_STREAM_FC1 = 128
 MOE_TYPE_BF16 = 0
 MOE_TYPE_F32 = 1
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 MOE_DEV_BAD_EXPERT = 1
 MOE_DEV_DUPLICATE = 2
 MOE_DEV_NONFINITE = 4
@@ -64,6 +66,7 @@ EXPORTS = (
     "moe_layer_forward_noalloc", "moe_read_status", "moe_layer_region", "moe_layer_tactic", "moe_profile_enable",
     "moe_profile_read", "moe_layer_destroy", "moe_token_bucket", "moe_status_string",
     "moe_last_error", "moe_debug_slot_timers", "moe_rms_norm_quant",
+    "moe_router_workspace_query", "moe_router_create", "moe_router_forward", "moe_router_destroy",
 )
 
 
@@ -94,6 +97,14 @@ class moe_tactic_t(Structure):
 
 class moe_norm_config_t(Structure):
     _fields_ = [("hidden", c_int32), ("eps", c_float), ("residual_type", c_int32), ("weight_type", c_int32)]
+
+
+class moe_router_config_t(Structure):
+    _fields_ = [
+        ("hidden", c_int32), ("num_experts", c_int32), ("top_k", c_int32), ("score", c_int32),
+        ("num_groups", c_int32), ("top_groups", c_int32), ("renormalize", c_int32), ("scale", c_float),
+        ("expert_base", c_int32), ("local_experts", c_int32),
+    ]
 
 
 def _load() -> ctypes.CDLL:
@@ -129,6 +140,10 @@ def _load() -> ctypes.CDLL:
         "moe_debug_slot_timers": (i32, [vp, i32]),
         "moe_rms_norm_quant": (i32, [POINTER(moe_norm_config_t), vp, c_int64, vp, c_int64, vp, i32, vp, vp, vp, vp,
                                      c_int64, vp]),
+        "moe_router_workspace_query": (i32, [POINTER(moe_router_config_t), i32, POINTER(c_size_t)]),
+        "moe_router_create": (i32, [POINTER(moe_router_config_t), i32, vp, vp, vp, c_size_t, vp, POINTER(vp)]),
+        "moe_router_forward": (i32, [vp, vp, c_int64, i32, vp, vp, vp, vp]),
+        "moe_router_destroy": (i32, [vp]),
         "moe_token_bucket": (i32, [i32]),
         "moe_status_string": (c_char_p, [i32]),
         "moe_last_error": (c_char_p, []),
@@ -251,3 +266,26 @@ def moe_rms_norm_quant(hidden: int, eps: float, residual_type: int, weight_type:
     _check(_lib.moe_rms_norm_quant(ctypes.byref(cfg), x, x_stride, residual or None, residual_stride, weight,
                                    num_tokens, codes or None, scales or None, y_bf16 or None, residual_out or None,
                                    residual_out_stride, stream))
+
+
+def moe_router_workspace_query(cfg: moe_router_config_t, max_rows: int) -> int:
+    n = c_size_t(0)
+    _check(_lib.moe_router_workspace_query(ctypes.byref(cfg), max_rows, ctypes.byref(n)))
+    return n.value
+
+
+def moe_router_create(cfg: moe_router_config_t, max_rows: int, weight: int, bias: int, workspace: int, ws_bytes: int,
+                      stream: int = 0) -> int:
+    h = c_void_p()
+    _check(_lib.moe_router_create(ctypes.byref(cfg), max_rows, weight, bias or None, workspace, ws_bytes, stream,
+                                  ctypes.byref(h)))
+    return h.value
+
+
+def moe_router_forward(router: int, x: int, x_stride: int, num_tokens: int, topk_idx: int, topk_w: int, ids: int = 0,
+                       stream: int = 0) -> None:
+    _check(_lib.moe_router_forward(router, x, x_stride, num_tokens, topk_idx, topk_w, ids or None, stream))
+
+
+def moe_router_destroy(router: int) -> None:
+    _check(_lib.moe_router_destroy(router))

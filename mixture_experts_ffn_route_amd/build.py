@@ -38,6 +38,7 @@ SOURCES = [
     "moe_weights.hip",
     "moe_noalloc.hip",
     "moe_norm.hip",
+    "moe_router.hip",
 ]
 
 # Packed FP32 VALU ops are disabled for all device code.
