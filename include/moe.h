@@ -373,7 +373,9 @@ typedef struct {
   int32_t num_experts;    /* E of the whole model, 1..1024 */
   int32_t top_k;          /* K, 1..8 (the layer takes 1, 2, 4, 6 and 8) */
   int32_t score;          /* MOE_SCORE_* */
-  int32_t num_groups;     /* the experts form this many equal groups, 1..16 (1: no groups) */
+  int32_t num_groups;     /* the experts form this many equal groups, 1..16 (1: no groups); more than 512
+                             experts in a number of groups that is no power of two: groups of at most
+                             64 (9..15 groups), 128 (5..7) or 256 (3) experts */
   int32_t top_groups;     /* groups whose experts can be chosen; they hold at least K experts */
   int32_t renormalize;    /* 1: a token's K weights are divided by their sum */
   float scale;            /* factor on the weights */

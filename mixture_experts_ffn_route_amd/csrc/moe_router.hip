@@ -35,6 +35,7 @@
 #include <string.h>
 
 #include <new>
+#include <type_traits>
 
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -52,11 +53,11 @@ constexpr int kGemmThreads = 512;
 constexpr int kGemmWaves = 8;
 constexpr int kKC = 128;            // K per chunk: one staged piece of the token rows
 constexpr int kPieces = kKC / 8;    // 16-byte pieces per row and chunk
-constexpr int kTileExperts = 256;   // experts per workgroup at most
 constexpr int kTargetGroups = 256;  // workgroups a split over K aims at
+constexpr int kMaxSplits = 8;
 constexpr int kMaxGroups = 16;
 constexpr int kMaxTopK = 8;
-constexpr float kLogitMargin = 0x1p-15f;
+constexpr float kLogitMargin = 0x1p-17f;
 
 struct RouterGemmArgs {
   const uint16_t* x;
@@ -80,6 +81,7 @@ struct RouterSelectArgs {
   const float* bias;  // null: none
   int32_t tokens, hidden, experts, row, splits;
   int32_t top_k, groups, group_size, top_groups;
+  int32_t lanes_per_group, per_lane;  // see router_select_kernel
   int32_t sigmoid, renormalize;
   float scale;
   int32_t expert_base, local_experts;
@@ -103,15 +105,14 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
   constexpr int TB = BT / 32;                       // token blocks
   constexpr int NP = BT * kPieces / kGemmThreads;   // staged pieces per thread
   static_assert(NP >= 1 && STEPS >= 1, "tile shape");
-  constexpr int kStage = 2 * BT * kPieces, kRed = WE * EW * 4 * 64;  // 16-byte pieces
+  constexpr int kStage = 3 * BT * kPieces, kRed = WE * EW * 4 * 64;  // 16-byte pieces
   __shared__ __attribute__((aligned(1024))) u32x4 lds[kStage > kRed ? kStage : kRed];
-  u32x4* const stage[2] = {lds, lds + BT * kPieces};
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int we = wave % WE, wk = wave / WE;
   const int t0 = blockIdx.x * BT;
-  const int eb0 = (int)blockIdx.y * (kTileExperts / 32) + we * EW;
+  const int eb0 = (int)blockIdx.y * (WE * EW) + we * EW;
   const int split = blockIdx.z;
   const int c0 = split * a.chunks_per_split;
   const int c1 = min(c0 + a.chunks_per_split, a.hidden / kKC);
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
   auto put_x = [&](const u32x4 (&r)[NP], int buf) {
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      stage[buf][piece_at(pr + j * (kGemmThreads / kPieces), pc)] = r[j];
+      lds[buf * (BT * kPieces) + piece_at(pr + j * (kGemmThreads / kPieces), pc)] = r[j];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf16x2 v = __builtin_bit_cast(bf16x2, r[j][i]);
@@ -168,43 +169,63 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
       }
     }
   };
-  auto compute = [&](int buf, int c) {
+  auto load_b = [&](bf16x8 (&r)[TB], int buf, int step) {
+    const int piece = (wk * STEPS + step) * 2 + (lane >> 5);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int piece = (wk * STEPS + s) * 2 + (lane >> 5);
-      bf16x8 bf[TB];
-#pragma unroll
-      for (int t = 0; t < TB; ++t)
-        bf[t] = __builtin_bit_cast(bf16x8, stage[buf][piece_at(t * 32 + (lane & 31), piece)]);
-#pragma unroll
-      for (int b = 0; b < EW; ++b)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-          acc[b][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, wr[s][b]), bf[t], acc[b][t],
-                                                              0, 0, 0);
-      load_w(s, c + 1);  // this step of the next chunk
-    }
+    for (int t = 0; t < TB; ++t)
+      r[t] = __builtin_bit_cast(bf16x8, lds[buf * (BT * kPieces) + piece_at(t * 32 + (lane & 31), piece)]);
   };
-
-  // Chunk c is staged while chunk c - 1 is computed; its rows were loaded two
-  // chunks before, its weights one.
+  // Chunk c's rows are put into LDS during chunk c - 2, loaded into registers
+  // two chunks before that; its weights are loaded during chunk c - 1.  With
+  // three buffers the fragments of a chunk's first step are read during the
+  // last step of the chunk before, so no wave stands still after the barrier.
+  // The scheduling barriers keep each step's weight loads in their step: left
+  // alone, the compiler issues them all at the end of the chunk, right before
+  // they are needed.
+  bf16x8 bf[2][TB];
   load_x(xr[0], c0);
   load_x(xr[1], c0 + 1);
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) load_w(s, c0);
   put_x(xr[0], 0);
   load_x(xr[0], c0 + 2);
+  if (c0 + 1 < c1) put_x(xr[1], 1);
+  load_x(xr[1], c0 + 3);
   __syncthreads();
+  load_b(bf[0], 0, 0);
+  int buf = 0;  // of chunk c
+  auto chunk = [&](u32x4 (&x)[NP], int c) {
+    const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      if (s + 1 < STEPS)
+        load_b(bf[(s + 1) & 1], buf, s + 1);
+      else
+        load_b(bf[(s + 1) & 1], next, 0);
+#pragma unroll
+      for (int b = 0; b < EW; ++b)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+          acc[b][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, wr[s][b]), bf[s & 1][t],
+                                                              acc[b][t], 0, 0, 0);
+      load_w(s, c + 1);  // this step of the next chunk
+      __builtin_amdgcn_sched_barrier(0);
+      if (s == (STEPS > 1 ? STEPS / 2 - 1 : 0)) {
+        if (c + 2 < c1) put_x(x, after);
+        load_x(x, c + 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if constexpr (STEPS & 1) {  // an odd number of steps leaves the next fragments in the other set
+#pragma unroll
+      for (int t = 0; t < TB; ++t) bf[0][t] = bf[1][t];
+    }
+    buf = next;
+    __syncthreads();
+  };
   for (int c = c0; c < c1; c += 2) {
-    if (c + 1 < c1) put_x(xr[1], 1);
-    load_x(xr[1], c + 3);
-    compute(0, c);
-    __syncthreads();
-    if (c + 1 >= c1) break;
-    if (c + 2 < c1) put_x(xr[0], 0);
-    load_x(xr[0], c + 4);
-    compute(1, c + 1);
-    __syncthreads();
+    chunk(xr[0], c);
+    if (c + 1 < c1) chunk(xr[1], c + 1);
   }
 
   // Sum of the wave groups, one 32-token block at a time: groups 1.. leave
@@ -277,7 +298,9 @@ template <int CTRL>
 __device__ __forceinline__ float dppf(float v) {
   return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
 }
-constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;  // quad_perm, quad_perm, ...
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e;              // quad_perm: lane ^ 1, lane ^ 2
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;    // lane ^ 7, lane ^ 15
+constexpr int kNext = 0x101;                           // row_shl:1, the lane after; 0 in the last
 
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, dpp<kXor1>(v));
@@ -308,331 +331,377 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return k < 2u ? -INFINITY : __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+// The rest of a choice as an ordered integer; it is a small number or 0.
+constexpr uint32_t kNoRest = 0x80000000u;
+__device__ __forceinline__ float unordered_rest(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
 __device__ __forceinline__ float sigmoid_fast(float l) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * l));
 }
 
-// Order of LDS accesses between the lanes of one wave (whose LDS operations
-// complete in order): a fence for the compiler only.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
-// One flagged token, by a whole wave: the choices that lie too close are
-// computed again in FP64.  All values are wave-uniform unless they carry a
-// lane.
-struct Exact {
-  double* logit;    // LDS [experts]: FP32 logits, FP64 where recomputed
-  double* choice;   // LDS [experts]
-  uint32_t* mark;   // LDS [32]: experts to recompute
-  const RouterSelectArgs& a;
-  int64_t t;
-  double margin;    // Bk: bound on a choice's error
-  uint32_t kept;    // groups that stay
-  int lane;
-
-  __device__ double choice_of(double l, int e) const {
-    double c = l;
-    if (a.sigmoid) c = 1.0 / (1.0 + exp(-l)) + (a.bias ? (double)a.bias[e] : 0.0);
-    return c != c ? -INFINITY : c;
-  }
-  __device__ bool candidate(int e) const { return a.groups == 1 || ((kept >> (e / a.group_size)) & 1u); }
-
-  // FP64 logits of the marked experts, then no marks.
-  __device__ void recompute() {
-    wave_fence();
-    for (int w = 0; w < (a.experts + 31) / 32; ++w) {
-      uint32_t bits = __builtin_amdgcn_readfirstlane(mark[w]);
-      while (bits) {
-        const int e = w * 32 + __builtin_ctz(bits);
-        bits &= bits - 1;
-        const uint16_t* x = a.x + t * a.x_stride;
-        const uint16_t* wr = a.w + (int64_t)e * a.hidden;
-        double s = 0.0;
-#pragma unroll 4
-        for (int i = lane * 8; i < a.hidden; i += 512) {
-          const u32x4 xv = *reinterpret_cast<const u32x4*>(x + i), wv = *reinterpret_cast<const u32x4*>(wr + i);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s = fma((double)bf16_to_f32(xv[k] & 0xffffu), (double)bf16_to_f32(wv[k] & 0xffffu), s);
-            s = fma((double)bf16_to_f32(xv[k] >> 16), (double)bf16_to_f32(wv[k] >> 16), s);
-          }
-        }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-        if (lane == 0) {
-          logit[e] = s;
-          choice[e] = choice_of(s, e);
-        }
-      }
-    }
-    wave_fence();
-    if (lane < 32) mark[lane] = 0u;
-    wave_fence();
-  }
-
-  // Largest candidate after (c, e) in descending order of choice, lowest
-  // expert first; e < 0 when there is none.
-  __device__ void next(double& c, int& e) const {
-    double best = 0.0;
-    int at = 0x7fffffff;
-    for (int i = lane; i < a.experts; i += 64) {
-      const double v = choice[i];
-      if (!candidate(i) || !(e < 0 || v < c || (v == c && i > e))) continue;
-      if (at == 0x7fffffff || v > best) {
-        best = v;
-        at = i;
-      }
-    }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double ov = __shfl_xor(best, m, 64);
-      const int oe = __shfl_xor(at, m, 64);
-      if (oe != 0x7fffffff && (at == 0x7fffffff || ov > best || (ov == best && oe < at))) {
-        best = ov;
-        at = oe;
-      }
-    }
-    c = best;
-    e = __builtin_amdgcn_readfirstlane(at == 0x7fffffff ? -1 : at);
-  }
-
-  // Group values (lane g holds group g's) and the groups that stay.  With
-  // `mark_close` the members that decide a border closer than the margins
-  // are marked; returns whether there is such a border.
-  __device__ bool pick_groups(bool mark_close) {
-    const int n = a.group_size;
-    double k1 = -INFINITY, k2 = -INFINITY;
-    if (lane < a.groups)
-      for (int i = lane * n; i < lane * n + n; ++i) {
-        const double v = choice[i];
-        if (v > k1) {
-          k2 = k1;
-          k1 = v;
-        } else if (v > k2) {
-          k2 = v;
-        }
-      }
-    const bool two = a.sigmoid && n > 1;
-    const double gv = two ? k1 + k2 : k1;
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double o = __shfl(gv, g, 64);
-      rank += (o > gv || (o == gv && g < lane)) ? 1 : 0;
-    }
-    const bool in = lane < a.groups && rank < a.top_groups;
-    kept = (uint32_t)__ballot(in);
-    double lo = in ? gv : INFINITY;                           // smallest value that stays
-    double hi = (lane < a.groups && !in) ? gv : -INFINITY;    // largest that does not
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      lo = fmin(lo, __shfl_xor(lo, m, 64));
-      hi = fmax(hi, __shfl_xor(hi, m, 64));
-    }
-    const double g4 = 4.0 * margin;
-    if (!mark_close || !(lo - hi <= g4)) return false;
-    if (lane < a.groups && (fabs(gv - lo) <= g4 || fabs(gv - hi) <= g4)) {
-      const double from = (two ? k2 : k1) - 2.0 * margin;
-      for (int i = lane * n; i < lane * n + n; ++i)
-        if (choice[i] >= from) atomicOr(&mark[i >> 5], 1u << (i & 31));
-    }
-    return true;
-  }
-
-  // The ids of the K largest, ids[k] in lane k.
-  __device__ int select() {
-    if (lane < 32) mark[lane] = 0u;
-    wave_fence();
-    if (a.groups > 1 && pick_groups(true)) {
-      recompute();
-      pick_groups(false);
-    }
-    // neighbours in the order of the choices that lie closer than the margins
-    double c = 0.0, pc = 0.0, border = 0.0;
-    int e = -1, pe = -1;
-    bool any = false;
-    for (int k = 0;; ++k) {
-      next(c, e);
-      if (e < 0) break;
-      if (k > 0 && pc - c <= 2.0 * margin) {
-        any = true;
-        if (lane == 0) {
-          atomicOr(&mark[e >> 5], 1u << (e & 31));
-          atomicOr(&mark[pe >> 5], 1u << (pe & 31));
-        }
-      }
-      if (k == a.top_k - 1) border = c;
-      if (k >= a.top_k && c < border - 2.0 * margin) break;
-      pc = c;
-      pe = e;
-    }
-    if (any) recompute();
-    int mine = -1;
-    c = 0.0;
-    e = -1;
-    for (int k = 0; k < a.top_k; ++k) {
-      next(c, e);
-      if (lane == k) mine = e;
-    }
-    return mine;
-  }
-};
-
-// EPL experts per lane: lane q of a token's 16 holds experts [q EPL, +EPL).
-template <int EPL>
-__global__ __launch_bounds__(256) void router_select_kernel(RouterSelectArgs a) {
-  __shared__ double lds_logit[4][16 * EPL];
-  __shared__ double lds_choice[4][16 * EPL];
-  __shared__ uint32_t lds_mark[4][32];
-  const int tid = threadIdx.x, lane = tid & 63, q = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t tw = ((int64_t)blockIdx.x * 4 + wave) * 4;  // first token of the wave
-  if (tw >= a.tokens) return;
+// Where the experts of a token sit: lane q of its 16 belongs to group
+// q / lanes and holds `per_lane` experts of it from (q % lanes) * per_lane on,
+// at most EPL (one group: 16 lanes).  An expert's slot, q EPL + j, rises with
+// its number.
+//
+// A choice known in FP64 is kept as a pair of floats, its value rounded and
+// the rest: key (ordered) then rest.  The rest is 0 for choices known in FP32.
+template <int EPL, bool SPLIT>
+__global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
+  constexpr uint32_t kSlots = 16 * EPL;    // a power of two
+  constexpr uint32_t kSlotMask = kSlots - 1;
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // SPLIT: [4][row]
+  const int lane = threadIdx.x, q = lane & 15, row0 = lane & 48;
+  const int64_t tw = (int64_t)blockIdx.x * 4;  // first of the wave's four tokens
   const int64_t t = tw + (lane >> 4);
   const bool live = t < a.tokens;
   const int64_t tt = live ? t : a.tokens - 1;
+  // this lane's experts
+  const int grp = q / a.lanes_per_group, sub = q - grp * a.lanes_per_group;
+  const int e0 = grp * a.group_size + sub * a.per_lane;
+  const int count = grp < a.groups ? max(0, min(a.per_lane, a.group_size - sub * a.per_lane)) : 0;
 
+  // Its logits.  Slots past the count read the lane's first expert (the
+  // row's first, if it has none).
   float l[EPL];
+  const float* src;
+  if constexpr (SPLIT) {
+    // the K parts of the wave's tokens, summed in order
+    const int n4 = (int)min((int64_t)4, a.tokens - tw) * (a.row / 4);
+    const f32x4* p = reinterpret_cast<const f32x4*>(a.part + tw * a.row);
+    const int64_t step = (int64_t)a.tokens * a.row / 4;
+    for (int i = lane; i < n4; i += 64) {
+      f32x4 part[kMaxSplits];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) l[j] = 0.0f;
-  float n2 = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float* p = a.part + ((int64_t)s * a.tokens + tt) * a.row + q * EPL;
-    if constexpr (EPL >= 4) {
+      for (int s = 0; s < kMaxSplits; ++s) part[s] = p[min(s, a.splits - 1) * step + i];
+      f32x4 v = part[0];
 #pragma unroll
-      for (int j = 0; j < EPL; j += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p + j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) l[j + k] += v[k];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) l[j] += p[j];
+      for (int s = 1; s < kMaxSplits; ++s)
+        if (s < a.splits) v += part[s];
+      reinterpret_cast<f32x4*>(sums)[i] = v;
     }
-    n2 += a.norm2[(int64_t)s * a.tokens + tt];
+    __syncthreads();
+    src = sums + (tt - tw) * a.row + e0;
+  } else {
+    src = a.part + tt * a.row + e0;
   }
+  if (EPL >= 4 && (a.per_lane | a.group_size) % 4 == 0) {  // whole 16-byte pieces
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(src + (j < count ? j : (count ? 0 : -e0)));
+#pragma unroll
+      for (int k = 0; k < 4 && j + k < EPL; ++k) l[j + k] = v[k];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = src[j < count ? j : (count ? 0 : -e0)];
+  }
+  float n2 = 0.0f;
+  for (int s = q; s < a.splits; s += 16) n2 += a.norm2[(int64_t)s * a.tokens + tt];
+  n2 = row_sum(n2);
 
-  // choices as ordered integers, and the margin of a choice
+  auto choice = [&](float logit, int e) {
+    return a.sigmoid ? sigmoid_fast(logit) + (a.bias ? a.bias[e] : 0.0f) : logit;
+  };
   uint32_t key[EPL];
   float largest = 0.0f;
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = q * EPL + j;
-    const bool in = e < a.experts;
-    float c = l[j];
-    if (a.sigmoid) c = sigmoid_fast(l[j]) + (a.bias && in ? a.bias[e] : 0.0f);
-    key[j] = in ? ordered(c) : 0u;
-    if (in) {
-      largest = fmaxf(largest, fabsf(l[j]));
-      top = fmaxf(top, l[j]);
-    }
+    const bool in = j < count;
+    key[j] = in ? ordered(choice(l[j], in ? e0 + j : 0)) : 0u;
+    largest = fmaxf(largest, in ? fabsf(l[j]) : 0.0f);
+    top = fmaxf(top, in ? l[j] : -INFINITY);
   }
   largest = __uint_as_float(row_max(__float_as_uint(largest)));  // not negative
-  float margin = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
-  // a sigmoid's slope is at most 1/4; evaluating it and adding the bias costs
-  // less than 2^-20 of their size
-  if (a.sigmoid) margin = 0.25f * margin + 0x1p-20f * (1.0f + a.limits[1]);
-  const bool guard = margin < INFINITY;  // not for rows with a NaN or an overflow
-  bool close = false;
+  const float logit_margin = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
+  // Margin of a choice: a sigmoid's slope is s (1 - s), 1/4 at most, and
+  // evaluating it and adding the bias costs less than 2^-20 of their size.
+  const float eval = a.sigmoid ? 0x1p-20f * (1.0f + a.limits[1]) : 0.0f;
+  const float margin = a.sigmoid ? fmaf(0.25f, logit_margin, eval) : logit_margin;
+  auto margin_of = [&](float logit) {
+    const float s = sigmoid_fast(logit);
+    return a.sigmoid ? fmaf(1.01f * s * (1.0f - s), logit_margin, eval) : logit_margin;
+  };
+  // not for rows with a NaN or an overflow, nor for zero rows, whose logits
+  // are exact
+  const bool guard = live && margin < INFINITY && n2 > 0.0f;
+
+  // FP64 logit of expert e for the token of row `from`, in every lane.
+  auto dot = [&](int from, int e) -> double {
+    const uint16_t* xr = a.x + (tw + (from >> 4)) * a.x_stride;
+    const uint16_t* wr = a.w + (int64_t)e * a.hidden;
+    double d = 0.0;
+#pragma unroll 7
+    for (int i = lane * 8; i < a.hidden; i += 512) {
+      const u32x4 xv = *reinterpret_cast<const u32x4*>(xr + i), wv = *reinterpret_cast<const u32x4*>(wr + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        d = fma((double)bf16_to_f32(xv[k] & 0xffffu), (double)bf16_to_f32(wv[k] & 0xffffu), d);
+        d = fma((double)bf16_to_f32(xv[k] >> 16), (double)bf16_to_f32(wv[k] >> 16), d);
+      }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m, 64);
+    return d;
+  };
+  auto choice64 = [&](double logit, int e) -> double {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (a.bias ? (double)a.bias[e] : 0.0) : logit;
+  };
+
+  // Choices of marked slots (bits of the lanes' `need`) in FP64.
+  uint32_t rest[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) rest[j] = kNoRest;
+  auto recompute = [&](uint64_t need) {
+    for (uint64_t lanes = __ballot(need != 0); lanes; lanes = __ballot(need != 0)) {
+      const int from = __builtin_ctzll(lanes);
+      const uint64_t bits = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(need >> 32), from) << 32) |
+                            (uint32_t)__builtin_amdgcn_readlane((int)need, from);
+      const int j0 = __builtin_ctzll(bits);
+      const int e = __builtin_amdgcn_readlane(e0, from) + j0;
+      const double d = dot(from, e), c = choice64(d, e);
+      const uint32_t hi = ordered((float)c), lo = ordered((float)(c - (double)(float)c));
+      if (lane == from) {
+        need &= need - 1;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (j == j0) {
+            l[j] = (float)d;
+            key[j] = hi;
+            rest[j] = lo;
+          }
+      }
+    }
+  };
 
   if (a.groups > 1) {
-    const int n = a.group_size;
-    const bool two = a.sigmoid && n > 1;
-    float gv = -INFINITY;
-    for (int g = 0; g < a.groups; ++g) {
-      uint32_t k1 = 0, k2 = 0;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const uint32_t v = (uint32_t)(q * EPL + j - g * n) < (uint32_t)n ? key[j] : 0u;
-        k2 = max(k2, min(k1, v));
-        k1 = max(k1, v);
-      }
-      auto merge = [&](uint32_t o1, uint32_t o2) {
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
-      };
-      merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
-      merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
-      merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
-      merge(dpp<kMirror>(k1), dpp<kMirror>(k2));
-      if (q == g) gv = two ? unordered(k1) + unordered(k2) : unordered(k1);
-    }
-    // groups ahead of this lane's, by rotating the row
-    int rank = 0;
-    auto ahead = [&](float o, int lane_from) { rank += (o > gv || (o == gv && lane_from < q)) ? 1 : 0; };
-#define MOE_ROT(N) ahead(dppf<0x120 + N>(gv), (q - N) & 15)
-    MOE_ROT(1); MOE_ROT(2); MOE_ROT(3); MOE_ROT(4); MOE_ROT(5); MOE_ROT(6); MOE_ROT(7); MOE_ROT(8);
-    MOE_ROT(9); MOE_ROT(10); MOE_ROT(11); MOE_ROT(12); MOE_ROT(13); MOE_ROT(14); MOE_ROT(15);
-#undef MOE_ROT
-    const bool in = q < a.groups && rank < a.top_groups;
-    const uint32_t kept = (uint32_t)(__ballot(in) >> (lane & 48)) & 0xffffu;
-    const uint32_t lo = row_min(in ? ordered(gv) : 0xffffffffu);
-    const uint32_t hi = row_max(q < a.groups && !in ? ordered(gv) : 0u);
-    close = hi > 1u && unordered(lo) - unordered(hi) <= 4.0f * margin;
-    const uint32_t magic = ((1u << 20) + n - 1) / n;  // e / n for e and n up to 1024
+    const bool two = a.sigmoid && a.group_size > 1;
+    // the group's two largest choices, in all its lanes
+    uint32_t k1 = 0, k2 = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const uint32_t g = ((uint32_t)(q * EPL + j) * magic) >> 20;
-      if (!((kept >> g) & 1u)) key[j] = 0u;
+      k2 = max(k2, min(k1, key[j]));
+      k1 = max(k1, key[j]);
     }
+    auto merge = [&](uint32_t o1, uint32_t o2) {
+      k2 = max(min(k1, o1), max(k2, o2));
+      k1 = max(k1, o1);
+    };
+    if (a.lanes_per_group > 1) merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
+    if (a.lanes_per_group > 2) merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
+    if (a.lanes_per_group > 4) merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
+    const float v = two ? unordered(k1) + unordered(k2) : unordered(k1);
+    const bool valid = grp < a.groups;
+    // lanes of groups ahead of this one, by rotating the row
+    const uint32_t vk = valid ? ordered(v) : 0u;
+    int ahead = 0;
+#define MOE_ROT(N)                                                                      \
+  {                                                                                     \
+    const uint32_t o = dpp<0x120 + N>(vk);                                              \
+    ahead += (o > vk || (o == vk && ((q - N) & 15) / a.lanes_per_group < grp)) ? 1 : 0; \
   }
-
-  // the K largest in order, lane k of the row keeping the k-th, and one more
-  // to see whether it lies close
-  int id = -1;
-  float mine = 0.0f;
-  float before = INFINITY;
-  for (int k = 0; k <= a.top_k; ++k) {
-    uint32_t bk = 0;
-    int bj = 0;
-    float bl = 0.0f;
+    MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
+    MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
+#undef MOE_ROT
+    bool in = valid && ahead < a.top_groups * a.lanes_per_group;
+    // smallest value that stays, largest that does not
+    const float lo = unordered(row_min(in ? vk : 0xffffffffu));
+    const float hi = unordered(row_max(valid && !in ? vk : 0u));
+    const float g4 = 4.0f * margin;
+    const bool close = guard && lo - hi <= g4;
+    if (__ballot(close)) {
+      // FP64 for the members that can make the values of groups at the border
+      const bool at = close && valid && (fabsf(v - lo) <= g4 || fabsf(v - hi) <= g4);
+      const float from = unordered(two ? k2 : k1) - 2.0f * margin;
+      uint64_t need = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (key[j] > bk) {
-        bk = key[j];
-        bj = j;
-        bl = l[j];
+      for (int j = 0; j < EPL; ++j)
+        if (at && key[j] > 1u && unordered(key[j]) >= from) need |= 1ull << j;
+      recompute(need);
+      double c1 = -INFINITY, c2 = -INFINITY;
+      auto put = [&](double c) {
+        c2 = fmax(c2, fmin(c1, c));
+        c1 = fmax(c1, c);
+      };
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        put(key[j] > 1u ? (double)unordered(key[j]) + (double)unordered_rest(rest[j]) : -INFINITY);
+      for (int m = 1; m < a.lanes_per_group; m <<= 1) {
+        const double o1 = __shfl_xor(c1, m, 64), o2 = __shfl_xor(c2, m, 64);
+        put(o1);
+        put(o2);
       }
-    const uint32_t m = row_max(bk);
-    if (m > 1u) {
-      const float c = unordered(m);
-      close |= before - c <= 2.0f * margin;
-      before = c;
+      const double gv = two ? c1 + c2 : c1;
+      int rank = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const double o = __shfl(gv, row0 + g * a.lanes_per_group, 64);
+        rank += (o > gv || (o == gv && g < grp)) ? 1 : 0;
+      }
+      in = valid && rank < a.top_groups;
     }
-    if (k == a.top_k) break;
-    const uint32_t e = row_min(bk == m ? (uint32_t)(q * EPL + bj) : 0xffffffffu);
-    const float el = __shfl(bl, (lane & 48) + (int)(e / EPL), 64);
-    if (q == k) {
-      id = (int)e;
-      mine = el;
-    }
+    if (!in) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if ((uint32_t)(q * EPL + j) == e) key[j] = 0u;
+      for (int j = 0; j < EPL; ++j) key[j] = 0u;
+    }
   }
 
-  // tokens with choices too close to call
-  uint64_t todo = __ballot(close && guard && live && q == 0);
-  while (todo) {
-    const int from = __builtin_ctzll(todo);  // first lane of the token's row
-    todo &= todo - 1;
-    Exact x{lds_logit[wave], lds_choice[wave], lds_mark[wave], a, tw + (from >> 4), 0.0, 0xffffu, lane};
-    x.margin = (double)__shfl(margin, from, 64);
-    if ((lane & 48) == from) {
+  // The K + 1 largest, by keys whose low bits give way to the slot (the lowest
+  // slot the largest): one maximum finds value and expert, lane k of the row
+  // keeping the k-th.
+  uint32_t pk[EPL];
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) x.logit[q * EPL + j] = (double)l[j];
+  for (int j = 0; j < EPL; ++j)
+    pk[j] = key[j] ? (max(key[j], kSlots) & ~kSlotMask) | (kSlotMask - (uint32_t)(q * EPL + j)) : 0u;
+  uint32_t mk = 0;     // lane k: the k-th packed key
+  float ml = 0.0f;     //   its logit
+  auto take = [&](int k) -> uint32_t {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) m = max(m, pk[j]);
+    m = row_max(m);
+    float sl = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const bool hit = pk[j] == m;
+      sl = hit ? l[j] : sl;
+      pk[j] = hit ? 0u : pk[j];
     }
-    wave_fence();
-    for (int e = lane; e < a.experts; e += 64) x.choice[e] = x.choice_of(x.logit[e], e);
-    wave_fence();
-    const int got = __shfl(x.select(), q, 64);  // lane k of the wave holds the k-th
-    if ((lane & 48) == from && q < a.top_k) {
-      id = got;
-      mine = (float)x.logit[got];
+    const int owner = row0 + (int)((kSlotMask - (m & kSlotMask)) / EPL);
+    const float ol = __shfl(sl, owner, 64);
+    if (q == k) {
+      mk = m;
+      ml = ol;
     }
-    wave_fence();
+    return m;
+  };
+  for (int k = 0; k <= a.top_k; ++k) (void)take(k);
+  auto expert_of = [&](uint32_t m) -> int {
+    const int slot = (int)(kSlotMask - (m & kSlotMask));
+    const int qs = slot / EPL, gs = qs / a.lanes_per_group;
+    return gs * a.group_size + (qs - gs * a.lanes_per_group) * a.per_lane + slot % EPL;
+  };
+  // largest choice that a packed key can stand for
+  auto upper = [&](uint32_t m) { return m >= 2 * kSlots ? unordered(m | kSlotMask) : -INFINITY; };
+  int id = mk ? expert_of(mk) : 0;
+  float c = mk ? choice(ml, id) : -INFINITY;
+  float mine = ml;
+  // Too close: neighbours among the K within the largest of their margins,
+  // or the last of them and what follows within its margin and any.
+  const uint32_t after = dpp<kNext>(mk);
+  const float among = unordered(row_max(q < a.top_k ? ordered(margin_of(ml)) : 0u));
+  const bool tight = guard && q < a.top_k && c - upper(after) <= among + (q + 1 < a.top_k ? among : margin);
+  if (__ballot(tight)) {
+    // Some token of the wave has neighbours too close to call.  Its list goes
+    // on while choices may belong to the K after all.
+    const bool mineclose = ((__ballot(tight) >> row0) & 0xffffu) != 0;
+    const float border = unordered(row_min(q < a.top_k ? ordered(c) : 0xffffffffu)) - (among + margin);
+    int n = a.top_k + 1;
+    bool more = true;
+    for (; n < 16 && more; ++n) {
+      const uint32_t m = take(n);
+      more = __ballot(mineclose && upper(m) >= border) != 0;
+    }
+    if (!more) {
+      id = mk ? expert_of(mk) : 0;
+      c = mk ? choice(ml, id) : -INFINITY;
+      mine = ml;
+      // those within the margins of another, in FP64
+      bool redo = false;
+      const float mm = margin_of(ml);
+#define MOE_ROT(N)                                                     \
+  {                                                                    \
+    const float o = dppf<0x120 + N>(c);                                \
+    redo |= fabsf(c - o) <= mm + dppf<0x120 + N>(mm);                  \
+  }
+      MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
+      MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
+#undef MOE_ROT
+      double exact = c;
+      for (uint64_t todo = __ballot(redo && mineclose && mk != 0); todo; todo &= todo - 1) {
+        const int from = __builtin_ctzll(todo);
+        const int e = __builtin_amdgcn_readlane(id, from);
+        const double d = dot(from, e), f = choice64(d, e);
+        if (lane == from) {
+          exact = f;
+          mine = (float)d;
+        }
+      }
+      // their order, ties to the lowest expert; lane k takes the k-th
+      if (!mk) exact = -INFINITY;
+      int rank = 0;
+      for (int i = 0; i < 16; ++i) {
+        const double o = __shfl(exact, row0 + i, 64);
+        const int oe = __shfl(id, row0 + i, 64);
+        const bool there = __shfl((int)(mk != 0), row0 + i, 64) != 0;
+        rank += there && (!mk || o > exact || (o == exact && oe < id)) ? 1 : 0;
+      }
+      int at = row0;
+      for (int i = 0; i < 16; ++i)
+        if (__shfl(mk ? rank : 16, row0 + i, 64) == q) at = row0 + i;
+      const int nid = __shfl(id, at, 64);
+      const float nl = __shfl(mine, at, 64);
+      if (mineclose) {
+        id = nid;
+        mine = nl;
+      }
+    } else {
+      // Too many for the list: every choice within the margin of its
+      // neighbour, among all experts.
+      auto extract = [&](auto exact) -> uint64_t {
+        constexpr bool kExact = decltype(exact)::value;
+        uint64_t taken = 0, need = 0;
+        float before = INFINITY, last = -INFINITY;
+        uint32_t ps = 0;
+        for (int k = 0;; ++k) {
+          uint32_t bk = 0, br = 0, bs = 0;
+          float bl = 0.0f;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) {
+            const uint32_t kj = (taken >> j) & 1u ? 0u : key[j];
+            if (kExact ? (kj > bk || (kj == bk && kj != 0u && rest[j] > br)) : kj > bk) {
+              bk = kj;
+              br = rest[j];
+              bs = (uint32_t)(q * EPL + j);
+              bl = l[j];
+            }
+          }
+          const uint32_t m = row_max(bk);
+          bool best = bk == m;
+          if constexpr (kExact) {
+            const uint32_t r = row_max(best ? br : 0u);
+            best = best && br == r;
+          }
+          const uint32_t s = row_min(best ? bs : 0xffffffffu) & kSlotMask;
+          const bool own = s / EPL == (uint32_t)q;
+          if constexpr (!kExact) {
+            const float ck = unordered(m);
+            const bool number = m > 1u;
+            if (number && guard && before - ck <= 2.0f * margin) {
+              if (own) need |= 1ull << (s % EPL);
+              if (ps / EPL == (uint32_t)q) need |= 1ull << (ps % EPL);
+            }
+            if (k == a.top_k - 1) last = ck;
+            if (!__ballot(k < a.top_k || (number && guard && ck >= last - 2.0f * margin))) break;
+            before = number ? ck : INFINITY;
+            ps = s;
+          } else {
+            const float el = __shfl(bl, row0 + (int)(s / EPL), 64);
+            if (q == k && mineclose) {
+              id = expert_of(kSlotMask - s);
+              mine = el;
+            }
+            if (k == a.top_k - 1) break;
+          }
+          if (own) taken |= 1ull << (s % EPL);
+        }
+        return need;
+      };
+      recompute(extract(std::false_type{}));
+      extract(std::true_type{});
+    }
   }
 
   // routing weights
@@ -648,7 +717,7 @@ __global__ __launch_bounds__(256) void router_select_kernel(RouterSelectArgs a) 
     float z = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (q * EPL + j < a.experts) z += expf(l[j] - m);
+      if (j < count) z += expf(l[j] - m);
     z = row_sum(z);
     w = slot ? expf(mine - m) / z : 0.0f;
   }
@@ -705,26 +774,42 @@ __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, co
 
 // Token tile and K split of a batch.
 struct Plan {
-  int bt;
+  int bt, be;  // tokens and 32-expert blocks per workgroup
   int splits, chunks_per_split;
 };
 
+// Few tokens take narrow expert tiles, so that the K split, whose parts the
+// selection reads back, stays at most kMaxSplits; many take wide tiles, which
+// read the token rows once.
 Plan plan_for(const moe_router_config_t& c, int64_t tokens) {
   Plan p;
-  p.bt = tokens <= 1024 ? 32 : (tokens <= 8192 ? 64 : 128);
-  const int64_t tiles = (tokens + p.bt - 1) / p.bt * ((c.num_experts + kTileExperts - 1) / kTileExperts);
+  p.bt = tokens <= 512 ? 32 : (tokens <= 4096 ? 64 : 128);
+  const int blocks = (c.num_experts + 31) / 32;
+  p.be = tokens <= 32 ? 1 : (tokens <= 256 ? 2 : (tokens <= 8192 ? 4 : 8));
+  while (p.be / 2 >= blocks) p.be /= 2;
+  const int64_t tiles = (tokens + p.bt - 1) / p.bt * ((blocks + p.be - 1) / p.be);
   const int chunks = c.hidden / kKC;
   int64_t want = kTargetGroups / tiles;
-  want = want < 1 ? 1 : (want > chunks ? chunks : want);
+  want = want < 1 ? 1 : (want > kMaxSplits ? kMaxSplits : want);
+  if (want > chunks) want = chunks;
   p.chunks_per_split = (int)((chunks + want - 1) / want);
   p.splits = (chunks + p.chunks_per_split - 1) / p.chunks_per_split;
   return p;
 }
 
-// Floats per logit row: 16 lanes x a power of two.
-int row_of(int experts) {
-  int r = 32;
-  while (r < experts) r <<= 1;
+// Floats per logit row: whole blocks of 32 experts.
+int row_of(int experts) { return (experts + 31) / 32 * 32; }
+
+// Lanes of a token's 16 per group, a power of two, and experts per lane.
+struct Lanes {
+  int groups, lanes, per_lane;
+};
+Lanes lanes_for(const moe_router_config_t& c) {
+  Lanes r;
+  r.groups = c.top_groups == c.num_groups ? 1 : c.num_groups;  // every group stays: none to pick
+  r.lanes = 16;
+  while (r.lanes * r.groups > 16) r.lanes >>= 1;
+  r.per_lane = (c.num_experts / r.groups + r.lanes - 1) / r.lanes;
   return r;
 }
 
@@ -736,17 +821,11 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 RouterLayout router_layout(const moe_router_config_t& c, int64_t max_rows) {
   RouterLayout L;
-  // largest splits x tokens of any batch: within a token tile size the split
-  // falls as the tokens grow, so the tile count times the split is bounded
-  int64_t rows = max_rows;
-  const int64_t edges[3] = {1024, 8192, max_rows};
-  for (int64_t e : edges) {
-    const int64_t t = e < max_rows ? e : max_rows;
-    const Plan p = plan_for(c, t);
-    const int64_t bound = (int64_t)kTargetGroups * p.bt, all = (int64_t)(c.hidden / kKC) * t;
-    const int64_t r = bound < all ? bound : all;
-    rows = r > rows ? r : rows;
-  }
+  // splits x tokens of any batch: at most kMaxSplits parts, and no more token
+  // tiles than kTargetGroups where there are several
+  const int64_t split_rows = (int64_t)kTargetGroups * 128;
+  int64_t rows = max_rows * kMaxSplits;
+  if (rows > split_rows) rows = max_rows > split_rows ? max_rows : split_rows;
   L.w = 0;
   L.limits = L.w + align256((size_t)((c.num_experts + 31) / 32) * 32 * c.hidden * 2);
   L.part = L.limits + 256;
@@ -776,6 +855,10 @@ moe_status_t validate(const moe_router_config_t* c, int32_t max_rows) {
     return fail(MOE_ERR_INVALID_ARG, "top_groups %d outside [1, %d]", c->top_groups, c->num_groups);
   if (c->num_experts / c->num_groups * c->top_groups < c->top_k)
     return fail(MOE_ERR_INVALID_ARG, "top_groups %d hold fewer than top_k %d experts", c->top_groups, c->top_k);
+  const Lanes n = lanes_for(*c);
+  if (n.per_lane > 64)
+    return fail(MOE_ERR_UNSUPPORTED, "groups of %d experts: %d groups take at most %d each",
+                c->num_experts / c->num_groups, c->num_groups, 64 * n.lanes);
   if (c->renormalize != 0 && c->renormalize != 1)
     return fail(MOE_ERR_INVALID_ARG, "renormalize must be 0 or 1");
   if (!isfinite(c->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
@@ -789,16 +872,25 @@ moe_status_t validate(const moe_router_config_t* c, int32_t max_rows) {
 }
 
 template <int BT>
-void launch_gemm(const RouterGemmArgs& g, dim3 grid, hipStream_t s) {
+void launch_gemm(const RouterGemmArgs& g, int be, dim3 grid, hipStream_t s) {
   const dim3 block(kGemmThreads);
-  if (g.blocks > 4)
+  if (be == 8)
     hipLaunchKernelGGL((router_gemm_kernel<BT, 4, 2>), grid, block, 0, s, g);
-  else if (g.blocks > 2)
+  else if (be == 4)
     hipLaunchKernelGGL((router_gemm_kernel<BT, 4, 1>), grid, block, 0, s, g);
-  else if (g.blocks > 1)
+  else if (be == 2)
     hipLaunchKernelGGL((router_gemm_kernel<BT, 2, 1>), grid, block, 0, s, g);
   else
     hipLaunchKernelGGL((router_gemm_kernel<BT, 1, 1>), grid, block, 0, s, g);
+}
+
+template <int EPL>
+void launch_select(const RouterSelectArgs& a, hipStream_t s) {
+  const dim3 grid((a.tokens + 3) / 4), block(64);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((router_select_kernel<EPL, true>), grid, block, 4 * a.row * sizeof(float), s, a);
+  else
+    hipLaunchKernelGGL((router_select_kernel<EPL, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -903,14 +995,13 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   g.chunks_per_split = p.chunks_per_split;
   g.part = reinterpret_cast<float*>(r->ws + r->L.part);
   g.norm2 = reinterpret_cast<float*>(r->ws + r->L.norm2);
-  const dim3 grid((num_tokens + p.bt - 1) / p.bt, (c.num_experts + moe::kTileExperts - 1) / moe::kTileExperts,
-                  p.splits);
+  const dim3 grid((num_tokens + p.bt - 1) / p.bt, (g.blocks + p.be - 1) / p.be, p.splits);
   if (p.bt == 32)
-    moe::launch_gemm<32>(g, grid, s);
+    moe::launch_gemm<32>(g, p.be, grid, s);
   else if (p.bt == 64)
-    moe::launch_gemm<64>(g, grid, s);
+    moe::launch_gemm<64>(g, p.be, grid, s);
   else
-    moe::launch_gemm<128>(g, grid, s);
+    moe::launch_gemm<128>(g, p.be, grid, s);
   moe::RouterSelectArgs a;
   a.part = g.part;
   a.norm2 = g.norm2;
@@ -925,8 +1016,11 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.row = g.row;
   a.splits = p.splits;
   a.top_k = c.top_k;
-  a.groups = c.top_groups == c.num_groups ? 1 : c.num_groups;  // every group stays
-  a.group_size = c.num_experts / c.num_groups;
+  const moe::Lanes n = moe::lanes_for(c);
+  a.groups = n.groups;
+  a.group_size = c.num_experts / n.groups;
+  a.lanes_per_group = n.lanes;
+  a.per_lane = n.per_lane;
   a.top_groups = c.top_groups;
   a.sigmoid = c.score == MOE_SCORE_SIGMOID;
   a.renormalize = c.renormalize;
@@ -936,15 +1030,18 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.idx = topk_idx;
   a.out_w = topk_w;
   a.ids = ids;
-  const dim3 sg((num_tokens + 15) / 16), sb(256);
-  switch (g.row) {
-    case 32: hipLaunchKernelGGL(moe::router_select_kernel<2>, sg, sb, 0, s, a); break;
-    case 64: hipLaunchKernelGGL(moe::router_select_kernel<4>, sg, sb, 0, s, a); break;
-    case 128: hipLaunchKernelGGL(moe::router_select_kernel<8>, sg, sb, 0, s, a); break;
-    case 256: hipLaunchKernelGGL(moe::router_select_kernel<16>, sg, sb, 0, s, a); break;
-    case 512: hipLaunchKernelGGL(moe::router_select_kernel<32>, sg, sb, 0, s, a); break;
-    default: hipLaunchKernelGGL(moe::router_select_kernel<64>, sg, sb, 0, s, a); break;
-  }
+  if (n.per_lane <= 2)
+    moe::launch_select<2>(a, s);
+  else if (n.per_lane <= 4)
+    moe::launch_select<4>(a, s);
+  else if (n.per_lane <= 8)
+    moe::launch_select<8>(a, s);
+  else if (n.per_lane <= 16)
+    moe::launch_select<16>(a, s);
+  else if (n.per_lane <= 32)
+    moe::launch_select<32>(a, s);
+  else
+    moe::launch_select<64>(a, s);
   if (hipGetLastError() != hipSuccess) return moe::fail(MOE_ERR_HIP, "router launch failed");
   return MOE_OK;
 }

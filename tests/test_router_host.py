@@ -29,6 +29,7 @@ def _cfg(**kw):
     (dict(top_groups=0), L.MOE_ERR_INVALID_ARG),
     (dict(top_groups=9), L.MOE_ERR_INVALID_ARG),
     (dict(num_experts=32, num_groups=16, top_groups=2, local_experts=32), L.MOE_ERR_INVALID_ARG),  # 4 experts, K = 8
+    (dict(num_experts=1000, num_groups=10, top_groups=4, local_experts=1000), L.MOE_ERR_UNSUPPORTED),  # 100 a lane
     (dict(renormalize=2), L.MOE_ERR_INVALID_ARG),
     (dict(scale=float("nan")), L.MOE_ERR_INVALID_ARG),
     (dict(expert_base=-1), L.MOE_ERR_INVALID_ARG),
