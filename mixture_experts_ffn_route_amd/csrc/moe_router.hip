@@ -78,7 +78,7 @@ struct RouterSelectArgs {
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* w;  // [E, H] as the caller holds it
-  const float* bias;  // null: none
+  const float* bias;    // [row]: zeros where there is none
   int32_t tokens, hidden, experts, row, splits;
   int32_t top_k, groups, group_size, top_groups;
   int32_t lanes_per_group, per_lane;  // see router_select_kernel
@@ -363,10 +363,23 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const int e0 = grp * a.group_size + sub * a.per_lane;
   const int count = grp < a.groups ? max(0, min(a.per_lane, a.group_size - sub * a.per_lane)) : 0;
 
-  // Its logits.  Slots past the count read the lane's first expert (the
-  // row's first, if it has none).
-  float l[EPL];
-  const float* src;
+  // Its logits and biases.  Slots past the count read the lane's first
+  // expert (the row's first, if it has none).
+  float l[EPL], bias[EPL];
+  auto load_row = [&](const float* src, float (&v)[EPL]) {
+    if (EPL >= 4 && (a.per_lane | a.group_size) % 4 == 0) {  // whole 16-byte pieces
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) {
+        const f32x4 p = *reinterpret_cast<const f32x4*>(src + (j < count ? e0 + j : (count ? e0 : 0)));
+#pragma unroll
+        for (int k = 0; k < 4 && j + k < EPL; ++k) v[j + k] = p[k];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) v[j] = src[j < count ? e0 + j : (count ? e0 : 0)];
+    }
+  };
+  load_row(a.bias, bias);
   if constexpr (SPLIT) {
     // the K parts of the wave's tokens, summed in order
     const int n4 = (int)min((int64_t)4, a.tokens - tw) * (a.row / 4);
@@ -383,35 +396,22 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       reinterpret_cast<f32x4*>(sums)[i] = v;
     }
     __syncthreads();
-    src = sums + (tt - tw) * a.row + e0;
+    load_row(sums + (tt - tw) * a.row, l);
   } else {
-    src = a.part + tt * a.row + e0;
-  }
-  if (EPL >= 4 && (a.per_lane | a.group_size) % 4 == 0) {  // whole 16-byte pieces
-#pragma unroll
-    for (int j = 0; j < EPL; j += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(src + (j < count ? j : (count ? 0 : -e0)));
-#pragma unroll
-      for (int k = 0; k < 4 && j + k < EPL; ++k) l[j + k] = v[k];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) l[j] = src[j < count ? j : (count ? 0 : -e0)];
+    load_row(a.part + tt * a.row, l);
   }
   float n2 = 0.0f;
   for (int s = q; s < a.splits; s += 16) n2 += a.norm2[(int64_t)s * a.tokens + tt];
   n2 = row_sum(n2);
 
-  auto choice = [&](float logit, int e) {
-    return a.sigmoid ? sigmoid_fast(logit) + (a.bias ? a.bias[e] : 0.0f) : logit;
-  };
+  auto choice = [&](float logit, float bias) { return a.sigmoid ? sigmoid_fast(logit) + bias : logit; };
   uint32_t key[EPL];
   float largest = 0.0f;
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const bool in = j < count;
-    key[j] = in ? ordered(choice(l[j], in ? e0 + j : 0)) : 0u;
+    key[j] = in ? ordered(choice(l[j], bias[j])) : 0u;
     largest = fmaxf(largest, in ? fabsf(l[j]) : 0.0f);
     top = fmaxf(top, in ? l[j] : -INFINITY);
   }
@@ -433,22 +433,33 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   auto dot = [&](int from, int e) -> double {
     const uint16_t* xr = a.x + (tw + (from >> 4)) * a.x_stride;
     const uint16_t* wr = a.w + (int64_t)e * a.hidden;
-    double d = 0.0;
-#pragma unroll 7
-    for (int i = lane * 8; i < a.hidden; i += 512) {
-      const u32x4 xv = *reinterpret_cast<const u32x4*>(xr + i), wv = *reinterpret_cast<const u32x4*>(wr + i);
+    constexpr int kBatch = 7;  // loads in flight per row
+    double d0 = 0.0, d1 = 0.0;
+    for (int base = lane * 8; base - lane * 8 < a.hidden; base += kBatch * 512) {
+      u32x4 xv[kBatch], wv[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        d = fma((double)bf16_to_f32(xv[k] & 0xffffu), (double)bf16_to_f32(wv[k] & 0xffffu), d);
-        d = fma((double)bf16_to_f32(xv[k] >> 16), (double)bf16_to_f32(wv[k] >> 16), d);
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = base + k * 512 < a.hidden ? base + k * 512 : 0;
+        xv[k] = *reinterpret_cast<const u32x4*>(xr + i);
+        wv[k] = *reinterpret_cast<const u32x4*>(wr + i);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (base + k * 512 >= a.hidden) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d0 = fma((double)bf16_to_f32(xv[k][i] & 0xffffu), (double)bf16_to_f32(wv[k][i] & 0xffffu), d0);
+          d1 = fma((double)bf16_to_f32(xv[k][i] >> 16), (double)bf16_to_f32(wv[k][i] >> 16), d1);
+        }
       }
     }
+    double d = d0 + d1;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m, 64);
     return d;
   };
   auto choice64 = [&](double logit, int e) -> double {
-    return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (a.bias ? (double)a.bias[e] : 0.0) : logit;
+    return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (double)a.bias[e] : logit;
   };
 
   // Choices of marked slots (bits of the lanes' `need`) in FP64.
@@ -586,7 +597,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   // largest choice that a packed key can stand for
   auto upper = [&](uint32_t m) { return m >= 2 * kSlots ? unordered(m | kSlotMask) : -INFINITY; };
   int id = mk ? expert_of(mk) : 0;
-  float c = mk ? choice(ml, id) : -INFINITY;
+  float c = mk ? choice(ml, a.bias[id]) : -INFINITY;
   float mine = ml;
   // Too close: neighbours among the K within the largest of their margins,
   // or the last of them and what follows within its margin and any.
@@ -606,7 +617,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     }
     if (!more) {
       id = mk ? expert_of(mk) : 0;
-      c = mk ? choice(ml, id) : -INFINITY;
+      c = mk ? choice(ml, a.bias[id]) : -INFINITY;
       mine = ml;
       // those within the margins of another, in FP64
       bool redo = false;
@@ -753,12 +764,16 @@ __global__ __launch_bounds__(256) void router_tile_kernel(const uint16_t* w, u32
   dst[c] = v;
 }
 
-// limits[0] = max_e |w_e|, limits[1] = max_e |bias_e|; one wave per expert.
-// A maximum does not depend on the order of the atomics; as bits, a NaN is
-// larger than every number.
-__global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, const float* bias, int hidden,
-                                                           uint32_t* limits) {
+// limits[0] = max_e |w_e|, limits[1] = max_e |bias_e|, and the padded copy of
+// the biases; one wave per expert slot of a logit row.  A maximum does not
+// depend on the order of the atomics; as bits, a NaN is larger than every
+// number.
+__global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, const float* bias, int experts,
+                                                           int hidden, uint32_t* limits, float* bias_copy) {
   const int e = blockIdx.x;
+  const float b = bias && e < experts ? bias[e] : 0.0f;
+  if (threadIdx.x == 0) bias_copy[e] = b;
+  if (e >= experts) return;
   float s = 0.0f;
   for (int i = threadIdx.x; i < hidden; i += 64) {
     const float v = bf16_to_f32(w[(int64_t)e * hidden + i]);
@@ -768,7 +783,7 @@ __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, co
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
   if (threadIdx.x == 0) {
     atomicMax(&limits[0], __float_as_uint(sqrtf(s)) & 0x7fffffffu);
-    if (bias) atomicMax(&limits[1], __float_as_uint(bias[e]) & 0x7fffffffu);
+    atomicMax(&limits[1], __float_as_uint(b) & 0x7fffffffu);
   }
 }
 
@@ -814,7 +829,7 @@ Lanes lanes_for(const moe_router_config_t& c) {
 }
 
 struct RouterLayout {
-  size_t w, limits, part, norm2, total;
+  size_t w, limits, bias, part, norm2, total;
 };
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -828,7 +843,8 @@ RouterLayout router_layout(const moe_router_config_t& c, int64_t max_rows) {
   if (rows > split_rows) rows = max_rows > split_rows ? max_rows : split_rows;
   L.w = 0;
   L.limits = L.w + align256((size_t)((c.num_experts + 31) / 32) * 32 * c.hidden * 2);
-  L.part = L.limits + 256;
+  L.bias = L.limits + 256;
+  L.part = L.bias + align256((size_t)row_of(c.num_experts) * 4);
   L.norm2 = L.part + align256((size_t)rows * row_of(c.num_experts) * 4);
   L.total = L.norm2 + align256((size_t)rows * 4);
   return L;
@@ -899,7 +915,6 @@ void launch_select(const RouterSelectArgs& a, hipStream_t s) {
 struct moe_router {
   moe_router_config_t cfg;
   const uint16_t* w;
-  const float* bias;
   uint8_t* ws;
   moe::RouterLayout L;
   int32_t max_rows;
@@ -943,7 +958,6 @@ extern "C" moe_status_t moe_router_create(const moe_router_config_t* cfg, int32_
   if (!r) return moe::fail(MOE_ERR_INVALID_ARG, "out of host memory");
   r->cfg = *cfg;
   r->w = static_cast<const uint16_t*>(weight);
-  r->bias = bias;
   r->ws = static_cast<uint8_t*>(workspace);
   r->L = L;
   r->max_rows = max_rows;
@@ -954,8 +968,8 @@ extern "C" moe_status_t moe_router_create(const moe_router_config_t* cfg, int32_
   if (ok) {
     hipLaunchKernelGGL(moe::router_tile_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, r->w,
                        reinterpret_cast<moe::u32x4*>(r->ws + L.w), pieces, cfg->num_experts, cfg->hidden);
-    hipLaunchKernelGGL(moe::router_limits_kernel, dim3(cfg->num_experts), dim3(64), 0, s, r->w, bias, cfg->hidden,
-                       limits);
+    hipLaunchKernelGGL(moe::router_limits_kernel, dim3(moe::row_of(cfg->num_experts)), dim3(64), 0, s, r->w, bias,
+                       cfg->num_experts, cfg->hidden, limits, reinterpret_cast<float*>(r->ws + L.bias));
     ok = hipGetLastError() == hipSuccess;
   }
   if (!ok) {
@@ -1009,7 +1023,7 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.x = g.x;
   a.x_stride = x_stride;
   a.w = r->w;
-  a.bias = r->bias;
+  a.bias = reinterpret_cast<const float*>(r->ws + r->L.bias);
   a.tokens = num_tokens;
   a.hidden = c.hidden;
   a.experts = c.num_experts;

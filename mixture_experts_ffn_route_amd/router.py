@@ -22,9 +22,9 @@ class MoERouter:
     """``weight``: bfloat16 [E, H], the gate of the whole model; ``bias``:
     float32 [E], added to sigmoid scores for the selection.  The experts
     [expert_base, expert_base + local_experts) are this GPU's (all of them by
-    default); routes to others come out as -1.  Weight and bias are read in
-    place while the router exists; one router's calls must not overlap on the
-    device."""
+    default); routes to others come out as -1.  The weight is read in place
+    while the router exists, the bias is copied; one router's calls must not
+    overlap on the device."""
 
     def __init__(self, weight: torch.Tensor, top_k: int, *, max_rows: int, score: str = "softmax",
                  bias: Optional[torch.Tensor] = None, num_groups: int = 1, top_groups: int = 1,
@@ -50,7 +50,7 @@ class MoERouter:
         elif workspace.numel() * workspace.element_size() < self.ws_bytes or workspace.device != self.device:
             raise ValueError("workspace too small, or on another device")
         self.workspace = workspace
-        self._keep = (weight, bias)
+        self._keep = (weight, bias)  # the handle reads the weight in place; the bias until its copy is made
         with torch.cuda.device(self.device):
             self.handle = L.moe_router_create(self.cfg, max_rows, ptr(weight), ptr(bias), ptr(workspace),
                                               self.ws_bytes, current_raw_stream(self.device.index))
