@@ -317,6 +317,23 @@ moe_status_t moe_layer_forward_noalloc(moe_layer_t* layer, const void* x, const 
                                        const int32_t* topk_idx, const float* topk_w, int32_t num_tokens,
                                        void* out_bf16, uint32_t* status_bits, void* stream);
 
+/* The whole layer for a few tokens (at most 16, and at most max_rows) in two
+ * launches: same arguments, route checks and arithmetic as
+ * moe_layer_forward_noalloc, on the layer's weight tiles, but made for
+ * streaming the chosen experts' weights: no staged rows, no compaction, no
+ * y rows.  It differs from stage + forward by one rounding: the experts' rows
+ * are added in FP32 and never rounded to bfloat16 on the way.  Every route is
+ * held (capacity_factor does not drop any).
+ *  status_bits  device uint32, may be NULL: receives the call's MOE_DEV_*
+ *               bits (moe_read_status does not see them).
+ * E4M3_BLOCK128 weights only.  The handle's staged batch is left as it was;
+ * the call uses regions of the workspace of its own, so calls on one handle
+ * must not overlap each other on the device.  num_tokens 0 only clears
+ * status_bits. */
+moe_status_t moe_layer_decode(moe_layer_t* layer, const void* x, const float* x_scale, const int32_t* topk_idx,
+                              const float* topk_w, int32_t num_tokens, void* out_bf16, uint32_t* status_bits,
+                              void* stream);
+
 /* Synchronise `stream` and return the device status bits (MOE_DEV_*)
  * accumulated since the last moe_stage_inputs.  bits: [host out]. */
 moe_status_t moe_read_status(moe_layer_t* layer, void* stream, uint32_t* bits);

@@ -19,6 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 SLOT_TIMERS = os.environ.get("MOE_SLOT_TIMERS", "0") == "1"
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x_slot_timers.so" if SLOT_TIMERS else "libmoe_mi355x.so")
 MOE_SLOT_TIMER_WORDS = 32
+DECODE_TOKENS = 16  # most tokens moe_layer_decode takes
 
 # moe_status_t
 MOE_OK = 0
@@ -66,7 +67,7 @@ EXPORTS = (
     "moe_layer_forward_noalloc", "moe_read_status", "moe_layer_region", "moe_layer_tactic", "moe_profile_enable",
     "moe_profile_read", "moe_layer_destroy", "moe_token_bucket", "moe_status_string",
     "moe_last_error", "moe_debug_slot_timers", "moe_rms_norm_quant",
-    "moe_router_workspace_query", "moe_router_create", "moe_router_forward", "moe_router_destroy",
+    "moe_layer_decode", "moe_router_workspace_query", "moe_router_create", "moe_router_forward", "moe_router_destroy",
 )
 
 
@@ -131,6 +132,7 @@ def _load() -> ctypes.CDLL:
         "moe_stage_inputs": (i32, [vp, vp, vp, vp, vp, i32, vp, vp]),
         "moe_layer_forward": (i32, [vp, vp]),
         "moe_layer_forward_noalloc": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, vp]),
+        "moe_layer_decode": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, vp]),
         "moe_read_status": (i32, [vp, vp, POINTER(c_uint32)]),
         "moe_layer_region": (i32, [vp, i32, POINTER(vp), POINTER(c_size_t)]),
         "moe_layer_tactic": (i32, [vp, POINTER(moe_tactic_t)]),
@@ -210,6 +212,12 @@ def moe_layer_forward_noalloc(layer: int, x: int, x_scale: int, topk_idx: int, t
                               out_bf16: int, status_bits: int = 0, stream: int = 0) -> None:
     _check(_lib.moe_layer_forward_noalloc(layer, x, x_scale or None, topk_idx, topk_w, num_tokens, out_bf16,
                                           status_bits or None, stream))
+
+
+def moe_layer_decode(layer: int, x: int, x_scale: int, topk_idx: int, topk_w: int, num_tokens: int, out_bf16: int,
+                     status_bits: int = 0, stream: int = 0) -> None:
+    _check(_lib.moe_layer_decode(layer, x, x_scale or None, topk_idx, topk_w, num_tokens, out_bf16,
+                                 status_bits or None, stream))
 
 
 def moe_read_status(layer: int, stream: int = 0) -> int:

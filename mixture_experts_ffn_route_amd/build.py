@@ -37,6 +37,7 @@ SOURCES = [
     "moe_combine.hip",
     "moe_weights.hip",
     "moe_noalloc.hip",
+    "moe_decode.hip",
     "moe_norm.hip",
     "moe_router.hip",
 ]

@@ -231,6 +231,10 @@ extern "C" moe_status_t moe_layer_create(const moe_config_t* cfg, int32_t expect
   if (ok)
     ok = moe::launch_fill_zero(reinterpret_cast<uint32_t*>(l->ws + L.off[moe::kRegionBlkBase]),
                                (int64_t)(L.size[moe::kRegionBlkBase] / 4), stream) == 0;
+  // so do the few-token layer's (each call leaves them so)
+  if (ok)
+    ok = moe::launch_fill_zero(reinterpret_cast<uint32_t*>(l->ws + L.off[moe::kRegionDecodeArrive]),
+                               (int64_t)(L.size[moe::kRegionDecodeArrive] / 4), stream) == 0;
   // arrival counters of the fused combine start at zero (each forward leaves them so)
   if (ok && (cfg->flags & MOE_FLAG_FUSED_COMBINE))
     ok = moe::launch_fill_zero(reinterpret_cast<uint32_t*>(l->ws + L.off[MOE_REGION_ARRIVE]),
@@ -512,6 +516,58 @@ extern "C" moe_status_t moe_layer_forward_noalloc(moe_layer_t* l, const void* x,
   l->compacted = compacted;
   l->out = out;
   return st;
+}
+
+extern "C" moe_status_t moe_layer_decode(moe_layer_t* l, const void* x, const float* x_scale,
+                                         const int32_t* topk_idx, const float* topk_w, int32_t num_tokens,
+                                         void* out_bf16, uint32_t* status_bits, void* stream) {
+  moe::clear_error();
+  if (!l) return moe::fail(MOE_ERR_INVALID_ARG, "layer is NULL");
+  if (num_tokens < 0) return moe::fail(MOE_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_tokens > l->max_rows || num_tokens > moe::kDecodeTokens)
+    return moe::fail(MOE_ERR_CAPACITY, "num_tokens %d exceeds max_rows %d or the few-token layer's %d", num_tokens,
+                     l->max_rows, moe::kDecodeTokens);
+  const moe_config_t& c = l->cfg;
+  if (moe::is_mx(c.weight_format))
+    return moe::fail(MOE_ERR_UNSUPPORTED, "the few-token layer takes E4M3_BLOCK128 weights");
+  if ((uintptr_t)status_bits & 3) return moe::fail(MOE_ERR_INVALID_ARG, "status_bits must be 4-byte aligned");
+  if (num_tokens > 0) {
+    if (!x || !topk_idx || !topk_w || !out_bf16)
+      return moe::fail(MOE_ERR_INVALID_ARG, "x, topk_idx, topk_w and out must be non-NULL");
+    if (((uintptr_t)x | (uintptr_t)out_bf16) & 15)
+      return moe::fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+    if (((uintptr_t)topk_idx | (uintptr_t)topk_w | (uintptr_t)x_scale) & 3)
+      return moe::fail(MOE_ERR_INVALID_ARG, "topk_idx, topk_w and x_scale must be 4-byte aligned");
+  }
+  if (num_tokens == 0) {
+    if (status_bits && moe::launch_fill_zero(status_bits, 1, stream) != 0) return hip_fail("status clear");
+    return MOE_OK;
+  }
+  moe::DecodeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.x_scale = x_scale;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.tokens = num_tokens;
+  a.hidden = c.hidden;
+  a.inter = c.intermediate;
+  a.num_experts = c.num_experts;
+  a.top_k = c.top_k;
+  a.flags = c.flags;
+  a.w13 = region<uint8_t>(l, MOE_REGION_W13T);
+  a.w2 = region<uint8_t>(l, MOE_REGION_W2T);
+  a.w13_scale = static_cast<const float*>(l->w.w13_scale);
+  a.w2_scale = static_cast<const float*>(l->w.w2_scale);
+  const int64_t slots = (int64_t)(l->max_rows < moe::kDecodeTokens ? l->max_rows : moe::kDecodeTokens) * c.top_k;
+  a.hf = region<float>(l, moe::kRegionDecode);
+  a.hs = a.hf + slots * c.intermediate;
+  a.hq = reinterpret_cast<uint8_t*>(a.hs + slots * (c.intermediate / 128));
+  a.arrive = region<int32_t>(l, moe::kRegionDecodeArrive);
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.status = status_bits;
+  if (moe::launch_decode(a, stream) != 0) return hip_fail("decode launch");
+  return MOE_OK;
 }
 
 extern "C" moe_status_t moe_read_status(moe_layer_t* l, void* stream, uint32_t* bits) {

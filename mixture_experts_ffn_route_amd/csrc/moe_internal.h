@@ -13,8 +13,10 @@ constexpr int kMaxExperts = 1024;
 constexpr int kCompactChunk = 4096;        // bound on the routes per compaction workgroup (256 lanes x 16)
 constexpr int kCompactOneRoutes = 2048;    // batches up to this many routes compact in one workgroup
 constexpr int kCompactBlockRoutes = 1024;  // beyond that, about this many routes per workgroup
-constexpr int kNumRegions = 21;
+constexpr int kNumRegions = 23;
 constexpr int kRegionBlkBase = 20;   // internal: per-(compaction block, expert) bases
+constexpr int kRegionDecode = 21;    // internal: h of the few-token layer (moe_layer_decode)
+constexpr int kRegionDecodeArrive = 22;  // internal: its arrival counters
 
 // Words of the device header (MOE_REGION_STATUS).
 enum HeaderWord : int {
@@ -219,6 +221,28 @@ struct CombineArgs {
 int launch_combine(const CombineArgs& a, void* stream);
 // Zero-fill of 32-bit words (the arrival counters at create).
 int launch_fill_zero(uint32_t* p, int64_t words, void* stream);
+
+// The layer for at most kDecodeTokens tokens in two launches (moe_decode.hip).
+constexpr int kDecodeTokens = 16;
+struct DecodeArgs {
+  const void* x;            // bf16 [T, H], or e4m3 [T, H] with x_scale
+  const float* x_scale;     // [T, H/128] or null
+  const int32_t* topk_idx;  // [T, K]
+  const float* topk_w;
+  int32_t tokens, hidden, inter, num_experts, top_k;
+  uint32_t flags;
+  const uint8_t* w13;       // weight tiles, as the GEMMs'
+  const uint8_t* w2;
+  const float* w13_scale;   // [E, 2I/128, H/128]
+  const float* w2_scale;    // [E, H/128, I/128]
+  float* hf;                // [T * K, I] FP32 h
+  uint8_t* hq;              // [T * K, I] e4m3 h
+  float* hs;                // [T * K, I/128]
+  int32_t* arrive;          // [T * K, I/128], zero between calls: FC1 workgroups done with a block of h
+  uint16_t* out;            // bf16 [T, H]
+  uint32_t* status;         // MOE_DEV_* bits of the call, or null
+};
+int launch_decode(const DecodeArgs& a, void* stream);
 
 // MXFP8 weight formats (either element type, E8M0 scales per 32).
 inline bool is_mx(int weight_format) {

@@ -26,12 +26,12 @@
 
 #include "moe_device.h"
 #include "moe_internal.h"
+#include "moe_quant_dev.h"
 
 namespace moe {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxWaves = 16;
@@ -50,14 +50,6 @@ struct NormArgs {
   void* residual_out;  // null: not wanted
   int64_t residual_out_stride;
 };
-
-// Maximum over a DPP row (16 consecutive lanes), in every lane of it.
-__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // quad_perm: lane ^ 1
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // quad_perm: lane ^ 2
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror: other quad
-  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // row_mirror: other half
-}
 
 __device__ __forceinline__ void load8_bf16(const uint16_t* p, float v[8]) {
   const u32x4 r = *reinterpret_cast<const u32x4*>(p);
@@ -88,34 +80,6 @@ __device__ __forceinline__ void store_nt(void* p, T v) {
 }
 __device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
   return u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
-}
-
-// e4m3 codes of 8 values of a block with scale s: those of the quotients
-// v / s.  A quotient is formed from a reciprocal and one correction step; a
-// scale below 2^-90, whose remainders could underflow, divides.  A block
-// that holds a NaN or an infinity has such a scale and NaN codes.
-__device__ __forceinline__ u32x2 quant8(const float v[8], float s) {
-  if (s == 0.0f) return u32x2{0u, 0u};
-  if (!isfinite(s)) return u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
-  float q[8];
-  if (s >= 0x1p-90f) {
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q0 = v[i] * inv;
-      q[i] = copysignf(fmaf(fmaf(-q0, s, v[i]), inv, q0), v[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
-  }
-  u32x2 w;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int lo = cvt2_e4m3(q[4 * j], q[4 * j + 1], 0, false);
-    w[j] = (uint32_t)cvt2_e4m3(q[4 * j + 2], q[4 * j + 3], lo, true);
-  }
-  return w;
 }
 
 // R: 0 no residual, 1 BF16, 2 FP32.  WF32: FP32 weight.

@@ -13,7 +13,10 @@ from typing import Optional
 import torch
 
 from . import _lib as L
+from ._args import check, current_raw_stream, ptr
 
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
@@ -73,6 +76,34 @@ class MoELayer:
                 raise ValueError("inputs must be contiguous")
         L.moe_layer_forward_noalloc(self.handle, _ptr(x), _ptr(x_scale), _ptr(topk_idx), _ptr(topk_w), x.shape[0],
                                     _ptr(out), _ptr(status), self._stream())
+
+    def decode(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+               x_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The whole layer for at most 16 tokens in two launches
+        (moe_layer_decode): x bfloat16 [T, H], or e4m3 codes with x_scale.
+        The optional int32 ``status`` word receives the call's MOE_DEV_*
+        bits."""
+        dev = self.workspace.device
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.decode(x, topk_idx, topk_w, x_scale, out, status)
+        T = x.shape[0]
+        shape, routes = (T, self.hidden), (T, self.top_k)
+        check(x, "x", shape, _BF16 if x_scale is None else _CODES, dev)
+        if x_scale is not None:
+            check(x_scale, "x_scale", (T, self.hidden // 128), _F32, dev)
+        check(topk_idx, "topk_idx", routes, _I32, dev)
+        check(topk_w, "topk_w", routes, _F32, dev)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            check(out, "out", shape, _BF16, dev)
+        if status is not None:
+            check(status, "status", (1,), _I32, dev)
+        L.moe_layer_decode(self.handle, x.data_ptr(), ptr(x_scale), topk_idx.data_ptr(), topk_w.data_ptr(), T,
+                           out.data_ptr(), ptr(status), current_raw_stream(dev.index))
+        return out
 
     def status(self) -> int:
         return L.moe_read_status(self.handle, self._stream())
