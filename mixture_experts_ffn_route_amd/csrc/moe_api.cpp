@@ -30,6 +30,7 @@ struct moe_layer {
   int32_t staged_tokens;
   bool compacted;  // the staging launch also scattered the routes (one compaction workgroup)
   void* out;
+  int32_t cus;
   int32_t grid_fc1, grid_fc2;
   int32_t stream_fc1, stream_fc2;  // register-ring depth of the streaming kernel per GEMM (0: LDS-ring kernel)
   int32_t grid_persist;  // MOE_FLAG_PERSISTENT_FFN: cooperative grid of the FC1->FC2 launch
@@ -187,6 +188,7 @@ extern "C" moe_status_t moe_layer_create(const moe_config_t* cfg, int32_t expect
   l->staged_tokens = -1;
   l->compacted = false;
   l->out = nullptr;
+  l->cus = cus;
   const bool mx = moe::is_mx(cfg->weight_format);
   // the streaming kernel serves the plain two-launch FP8 path (the variants
   // with a gate/up output, the fused combine or one persistent launch run the
@@ -561,8 +563,10 @@ extern "C" moe_status_t moe_layer_decode(moe_layer_t* l, const void* x, const fl
   a.w2_scale = static_cast<const float*>(l->w.w2_scale);
   const int64_t slots = (int64_t)(l->max_rows < moe::kDecodeTokens ? l->max_rows : moe::kDecodeTokens) * c.top_k;
   a.hf = region<float>(l, moe::kRegionDecode);
-  a.hs = a.hf + slots * c.intermediate;
-  a.hq = reinterpret_cast<uint8_t*>(a.hs + slots * (c.intermediate / 128));
+  a.hq = reinterpret_cast<uint8_t*>(a.hf + slots * c.intermediate);
+  a.hs = reinterpret_cast<float*>(a.hq + slots * c.intermediate);
+  a.plan = reinterpret_cast<moe::DecodePlan*>(a.hs + slots * (c.intermediate / 128));
+  a.grid = l->cus;
   a.arrive = region<int32_t>(l, moe::kRegionDecodeArrive);
   a.out = static_cast<uint16_t*>(out_bf16);
   a.status = status_bits;

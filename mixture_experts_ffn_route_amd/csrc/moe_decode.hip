@@ -37,8 +37,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = 8;
-constexpr int kCols = 16;                // tokens at most: MFMA columns
-constexpr int kSlots = kCols * 8;        // routes at most
+constexpr int kCols = kDecodeTokens;     // MFMA columns
+constexpr int kSlots = kDecodeSlots;
 constexpr int kTileBytes = 32 * 1024;    // a 256 x 128 weight tile
 constexpr int kFragBytes = 2 * 1024;     // its 16 x 128 fragments
 
@@ -83,35 +83,41 @@ __device__ __forceinline__ uint32_t col_max(uint32_t v) {
   return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// The routes of the call, staged by every workgroup for itself: checked ids
-// (-1 masked) and weights in LDS, with moe_stage_inputs' rules.
+// Checked routes of the call in LDS: ids (-1 masked) and weights, with
+// moe_stage_inputs' rules, and the experts they reach.
 struct Routes {
+  int32_t raw[kSlots];
   int32_t id[kSlots];
   float w[kSlots];
+  int32_t first[kMaxExperts];  // lowest slot of an expert
   uint32_t status;
 };
-__device__ __forceinline__ void stage_routes(const DecodeArgs& a, Routes& r, int32_t* raw) {
-  const int n = a.tokens * a.top_k, i = threadIdx.x;
+
+// Fills r and the plan: the experts in the order of their first routes, and
+// per expert and token the route (the lowest, -1 for none) and its weight.  A
+// repeated id, which only stays without route checks, adds up in the weight.
+__device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, DecodePlan& plan) {
+  const int n = a.tokens * a.top_k, i = threadIdx.x, lane = i & 63;
   int id = -1;
   float w = 0.0f;
   if (i < n) {
     id = a.topk_idx[i];
     w = a.topk_w[i];
   }
+  for (int e = i; e < a.num_experts; e += kThreads) r.first[e] = kSlots;
   if (i == 0) r.status = 0u;
   uint32_t bits = 0;
   if (id < -1 || id >= a.num_experts) {
     bits = MOE_DEV_BAD_EXPERT;
     id = -1;
   }
-  if (i < kSlots) raw[i] = id;
+  if (i < kSlots) r.raw[i] = id;
   __syncthreads();
   if (i < kSlots) {
     if ((a.flags & MOE_FLAG_CHECK_ROUTES) && id >= 0) {
       // the lowest slot of an id stays, whatever its weight
-      const int first = i - i % a.top_k;
       bool again = false;
-      for (int j = first; j < i; ++j) again |= raw[j] == id;
+      for (int j = i - i % a.top_k; j < i; ++j) again |= r.raw[j] == id;
       if (again) {
         bits |= MOE_DEV_DUPLICATE;
         id = -1;
@@ -122,194 +128,235 @@ __device__ __forceinline__ void stage_routes(const DecodeArgs& a, Routes& r, int
     }
     r.id[i] = id;
     r.w[i] = id >= 0 ? w : 0.0f;
+    if (id >= 0) atomicMin(&r.first[id], i);
     if (bits) atomicOr(&r.status, bits);
   }
   __syncthreads();
-}
-
-// Slot of expert e's first route, from the ballots over a wave's two halves
-// of the slots.
-__device__ __forceinline__ int first_slot(const Routes& r, int e, int lane) {
-  const uint64_t lo = __ballot(r.id[lane] == e), hi = __ballot(r.id[64 + lane] == e);
-  return lo ? __builtin_ctzll(lo) : (hi ? 64 + __builtin_ctzll(hi) : kSlots);
+  if (i < 64) {
+    const int a0 = r.id[lane], a1 = r.id[64 + lane];
+    const bool f0 = a0 >= 0 && r.first[a0] == lane, f1 = a1 >= 0 && r.first[a1] == 64 + lane;
+    const uint64_t b0 = __ballot(f0), b1 = __ballot(f1), below = (1ull << lane) - 1;
+    if (f0) plan.expert[__popcll(b0 & below)] = a0;
+    if (f1) plan.expert[__popcll(b0) + __popcll(b1 & below)] = a1;
+    if (lane == 0) plan.experts = __popcll(b0) + __popcll(b1);
+  }
+  __syncthreads();
+  const int ne = plan.experts;
+  for (int j = i; j < ne * kCols; j += kThreads) {
+    const int t = j & 15, e = plan.expert[j >> 4];
+    int slot = -1;
+    float sum = 0.0f;
+    if (t < a.tokens)
+      for (int k = 0; k < a.top_k; ++k)
+        if (r.id[t * a.top_k + k] == e) {
+          if (slot < 0) slot = t * a.top_k + k;
+          sum += r.w[t * a.top_k + k];
+        }
+    plan.row[j] = slot;
+    plan.weight[j] = sum;
+  }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // FC1
 // ---------------------------------------------------------------------------
 
-// Workgroup (tile, slot): 16 F columns of h of the expert of route `slot`, if
-// that is its first route.  Wave w takes K-blocks [w kbs / 8, (w + 1) kbs / 8).
-template <int F, bool BF16, int D>
-__global__ __launch_bounds__(kThreads) void decode_fc1_kernel(DecodeArgs a) {
+// One workgroup per CU walks over tasks of 16 columns of h of one expert.
+// Wave w takes K-blocks [w kbs / 8, (w + 1) kbs / 8), at most NK, of every
+// task: it keeps its part of the token rows, quantised, in registers for all
+// tasks, and has D K-blocks of weights in flight, running on into the next
+// task.  The waves' sums of a task meet in LDS; one wave, another one each
+// task, finishes it while the others stream on.
+template <int NK, int D>
+__global__ __launch_bounds__(kThreads, 1) void decode_fc1_kernel(DecodeArgs a) {
+  static_assert(NK % D == 0, "a K-block's ring slot is the same in every task");
   __shared__ Routes routes;
-  __shared__ int32_t raw[kSlots];
-  __shared__ v4f red[kWaves][2 * F][64];
-  __shared__ int32_t col_slot[kCols];  // route of each column's token, -1 past the last
-  __shared__ int32_t last;
+  __shared__ DecodePlan plan;
+  __shared__ v4f red[2][kWaves][2][64];  // [task parity][wave][gate, up][lane]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slot = blockIdx.y, tile = blockIdx.x;
-  stage_routes(a, routes, raw);
-  if (a.status && slot == 0 && tile == 0 && tid == 0) *a.status = routes.status;
-  const int e = __builtin_amdgcn_readfirstlane(routes.id[slot]);
-  if (e < 0 || first_slot(routes, e, lane) != slot) return;
-
-  // the expert's tokens, in order, one per column
-  if (tid < kCols) col_slot[tid] = -1;
-  __syncthreads();
-  if (wave == 0) {
-    int mine = -1;
-    if (lane < a.tokens)
-      for (int k = a.top_k - 1; k >= 0; --k)
-        if (routes.id[lane * a.top_k + k] == e) mine = lane * a.top_k + k;
-    const uint64_t has = __ballot(mine >= 0);
-    if (mine >= 0) col_slot[__popcll(has & ((1ull << lane) - 1))] = mine;
-  }
-  __syncthreads();
   const int col = lane & 15, grp = lane >> 4;
-  const int my_slot = col_slot[col] >= 0 ? col_slot[col] : slot;  // spare columns repeat the first
-  const int64_t t = my_slot / a.top_k;
+  const int kbs = a.hidden / 128, nb = a.inter / 128;
+  const int kb0 = wave * kbs / kWaves, nk = (wave + 1) * kbs / kWaves - kb0;
 
-  const int kbs = a.hidden / 128;
-  const int kb0 = wave * kbs / kWaves, kb1 = (wave + 1) * kbs / kWaves;
-  constexpr int kPer128 = 8 / F;  // tiles per 128 columns
-  const int blk = tile / kPer128, sub = tile % kPer128;
-  const uint8_t* wbase =
-      a.w13 + ((int64_t)e * (a.inter / 128) + blk) * kbs * (int64_t)kTileBytes + sub * F * kFragBytes + lane * 16;
-  const uint8_t* x8 = static_cast<const uint8_t*>(a.x) + t * a.hidden + grp * 32;
-  const uint16_t* x16 = static_cast<const uint16_t*>(a.x) + t * a.hidden + grp * 32;
-  // the wave's weight scales: gate in lanes 0.., up in lanes 32..
-  const int nb = a.inter / 128;
-  float wsc = 0.0f;
+  // the wave's token operands: columns past the last token repeat it
+  v8i xb[NK];
+  float sx[NK];
   {
-    const int j = kb0 + (lane & 31);
-    if (j < kb1) wsc = a.w13_scale[((int64_t)e * 2 * nb + (lane < 32 ? blk : nb + blk)) * kbs + j];
+    const int64_t t = min(col, a.tokens - 1);
+    if (a.x_scale) {
+      const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const int at = k < nk ? k : 0;  // a wave without K-blocks reads the row's first
+        const u32x4* q = reinterpret_cast<const u32x4*>(nk ? x + at * 128 : static_cast<const uint8_t*>(a.x));
+        xb[k] = operand(Frag{q[0], q[1]});
+        sx[k] = a.x_scale[t * kbs + (nk ? kb0 + at : 0)];
+      }
+    } else {
+      const uint16_t* x = static_cast<const uint16_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const u32x4* q = reinterpret_cast<const u32x4*>(nk ? x + (k < nk ? k : 0) * 128
+                                                           : static_cast<const uint16_t*>(a.x));
+        u32x4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = q[i];
+        float v[32];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t w = r[i / 4][i % 4];
+          v[2 * i] = bf16_to_f32(w & 0xffffu);
+          v[2 * i + 1] = bf16_to_f32(w >> 16);
+          m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
+        }
+        sx[k] = __uint_as_float(col_max(m)) / kE4m3Max;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const q_u32x2 c = quant8(v + 8 * i, sx[k]);
+          xb[k][2 * i] = (int)c[0];
+          xb[k][2 * i + 1] = (int)c[1];
+        }
+      }
+    }
   }
+
+  plan_routes(a, routes, plan);
+  if (blockIdx.x == 0) {  // FC2 takes the plan from here
+    if (tid == 0 && a.status) *a.status = routes.status;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(&plan);
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.plan);
+    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kThreads) to[i] = from[i];
+  }
+  const int per_expert = a.inter / 16;
+  const int tasks = __builtin_amdgcn_readfirstlane(plan.experts) * per_expert;
 
   struct Stage {
-    Frag g[F], u[F];
-    u32x4 x[BF16 ? 4 : 2];
-    float sx;
+    Frag g, u;
   };
   Stage st[D];
-  auto load = [&](Stage& s, int kb) {
-    const uint8_t* p = wbase + (int64_t)kb * kTileBytes;
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      s.g[f] = load_frag_nt(p + f * kFragBytes);
-      s.u[f] = load_frag_nt(p + (8 + f) * kFragBytes);
-    }
-    if constexpr (BF16) {
-      const u32x4* q = reinterpret_cast<const u32x4*>(x16 + kb * 128);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s.x[i] = q[i];
-    } else {
-      const u32x4* q = reinterpret_cast<const u32x4*>(x8 + kb * 128);
-      s.x[0] = q[0];
-      s.x[1] = q[1];
-      s.sx = a.x_scale[t * kbs + kb];
-    }
+  float wsc = 0.0f, wsc_next = 0.0f;
+  // weights of a task's column tile; a task past the last repeats the last
+  auto task_at = [&](int task, int& n, int& blk, int& sub) {
+    n = task / per_expert;
+    const int c = task - n * per_expert;
+    blk = c >> 3;
+    sub = c & 7;
   };
-  v4f accg[F], accu[F];
-#pragma unroll
-  for (int f = 0; f < F; ++f) accg[f] = accu[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto base_of = [&](int task) -> const uint8_t* {
+    int n, blk, sub;
+    task_at(min(task, tasks - 1), n, blk, sub);
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
+    return a.w13 + (((int64_t)e * nb + blk) * kbs + kb0) * kTileBytes + sub * kFragBytes + lane * 16;
+  };
+  // weight scales of the wave's K-blocks: gate in lanes 0.., up in lanes 32..
+  auto scales_of = [&](int task) -> float {
+    int n, blk, sub;
+    task_at(min(task, tasks - 1), n, blk, sub);
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
+    const int j = min(lane & 31, nk - 1);
+    return a.w13_scale[((int64_t)e * 2 * nb + (lane < 32 ? blk : nb + blk)) * kbs + kb0 + j];
+  };
+  auto load = [&](Stage& s, const uint8_t* base, int k) {
+    const uint8_t* p = base + (int64_t)k * kTileBytes;
+    s.g = load_frag_nt(p);
+    s.u = load_frag_nt(p + 8 * kFragBytes);
+  };
 
-  auto compute = [&](Stage& s, int kb) {
-    v8i b;
-    float sx;
-    if constexpr (BF16) {
-      float v[32];
+  const int stride = gridDim.x;
+  int task = blockIdx.x;
+  const uint8_t* base = nullptr;
+  if (task < tasks && nk > 0) {
+    base = base_of(task);
+    wsc = scales_of(task);
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+      if (k < nk) load(st[k], base, k);
+  }
+  for (int turn = 0; task < tasks; task += stride, ++turn) {
+    v4f accg = {0.0f, 0.0f, 0.0f, 0.0f}, accu = accg;
+    if (nk > 0) {
+      const uint8_t* next = base_of(task + stride);
+      wsc_next = scales_of(task + stride);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        if (k < nk) {
+          Stage& s = st[k % D];
+          const float sg = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), k));
+          const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), 32 + k));
+          accg = add_scaled(accg, mfma_e4m3(s.g, xb[k]), sx[k], sg);
+          accu = add_scaled(accu, mfma_e4m3(s.u, xb[k]), sx[k], su);
+        }
+        // the K-block D ahead, in this task or the next
+        if (k + D < NK) {
+          if (k + D < nk) load(st[k % D], base, k + D);
+        } else if (k + D - NK < nk) {
+          load(st[k % D], next, k + D - NK);
+        }
+      }
+      base = next;
+      wsc = wsc_next;
+    }
+    const int par = turn & 1;
+    red[par][wave][0][lane] = accg;
+    red[par][wave][1][lane] = accu;
+    __syncthreads();  // the only one per task: the wave that reads red gets here before it is written again
+    if (wave != (turn & (kWaves - 1))) continue;
+
+    int n, blk, sub;
+    task_at(task, n, blk, sub);
+    v4f g = red[par][0][0][lane], u = red[par][0][1][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      g += red[par][w][0][lane];
+      u += red[par][w][1][lane];
+    }
+    // lane l: columns 4 (l / 16) + 0..3 of the tile, token l % 16
+    const int slot = plan.row[n * kCols + col];
+    if (slot >= 0) {
+      uint64_t* dst = reinterpret_cast<uint64_t*>(a.hf + (int64_t)slot * a.inter + blk * 128 + sub * 16 + grp * 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __float_as_uint(swiglu(g[2 * i], u[2 * i]));
+        const uint32_t hi = __float_as_uint(swiglu(g[2 * i + 1], u[2 * i + 1]));
+        __hip_atomic_store(dst + i, (uint64_t)lo | ((uint64_t)hi << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    // The stores are write-through (agent scope) and complete before the
+    // arrival; the eighth to arrive at a 128-column block reads it with
+    // agent-scope loads, so no cache has to be flushed.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int old = 0;
+    if (lane == 0) {
+      int32_t* ctr = a.arrive + n * nb + blk;
+      old = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (old == 7) __hip_atomic_store(ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+    }
+    if (__builtin_amdgcn_readfirstlane(old) != 7) continue;
+    for (int t0 = 0; t0 < a.tokens; t0 += 4) {  // 16 lanes per row, 8 columns each
+      const int t = t0 + grp;
+      const int to = t < kCols ? plan.row[n * kCols + t] : -1;
+      if (to < 0) continue;
+      const int c = blk * 128 + col * 8;
+      const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + c);
+      uint64_t p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = __hip_atomic_load(src + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      float h[8];
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t w = s.x[i / 4][i % 4];
-        v[2 * i] = bf16_to_f32(w & 0xffffu);
-        v[2 * i + 1] = bf16_to_f32(w >> 16);
-        m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
-      }
-      sx = __uint_as_float(col_max(m)) / kE4m3Max;
-#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const q_u32x2 c = quant8(v + 8 * i, sx);
-        b[2 * i] = (int)c[0];
-        b[2 * i + 1] = (int)c[1];
+        h[2 * i] = __uint_as_float((uint32_t)p[i]);
+        h[2 * i + 1] = __uint_as_float((uint32_t)(p[i] >> 32));
+        m = max(m, max((uint32_t)p[i] & 0x7fffffffu, (uint32_t)(p[i] >> 32) & 0x7fffffffu));
       }
-    } else {
-      b = operand(Frag{s.x[0], s.x[1]});
-      sx = s.sx;
-    }
-    const int j = kb - kb0;
-    const float sg = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), j));
-    const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), 32 + j));
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      accg[f] = add_scaled(accg[f], mfma_e4m3(s.g[f], b), sx, sg);
-      accu[f] = add_scaled(accu[f], mfma_e4m3(s.u[f], b), sx, su);
-    }
-  };
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (kb0 + d < kb1) load(st[d], kb0 + d);
-  for (int kb = kb0; kb < kb1; kb += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (kb + d >= kb1) break;
-      compute(st[d], kb + d);
-      if (kb + d + D < kb1) load(st[d], kb + d + D);
+      const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
+      *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)to * a.inter + c) = quant8(h, s);
+      if (col == 0) a.hs[(int64_t)to * nb + blk] = s;
     }
   }
-#pragma unroll
-  for (int f = 0; f < F; ++f) {
-    red[wave][f][lane] = accg[f];
-    red[wave][F + f][lane] = accu[f];
-  }
-  __syncthreads();
-
-  // h of the tile: value i of MFMA lane l is column 16 f + 4 (l / 16) + i of
-  // token column l % 16
-  const int c128 = blk * 128;
-  for (int v = tid; v < F * 256; v += kThreads) {
-    const int f = v >> 8, l = (v >> 2) & 63, i = v & 3;
-    const int to = col_slot[l & 15];
-    if (to < 0) continue;
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      g += red[w][f][l][i];
-      u += red[w][F + f][l][i];
-    }
-    __hip_atomic_store(a.hf + (int64_t)to * a.inter + c128 + (sub * F + f) * 16 + 4 * (l >> 4) + i, swiglu(g, u),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  // The stores are write-through (agent scope) and complete before the
-  // arrival; the workgroup that arrives last reads the whole block with
-  // agent-scope loads, so no cache has to be flushed.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  int32_t* ctr = a.arrive + (int64_t)slot * nb + blk;
-  if (tid == 0) {
-    last = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == kPer128 - 1;
-    if (last) __hip_atomic_store(ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
-  }
-  __syncthreads();
-  if (!last) return;
-  const int to = (tid >> 4) < kCols ? col_slot[tid >> 4] : -1;
-  if (to < 0) return;  // whole groups of 16 lanes
-  const int c = c128 + (tid & 15) * 8;
-  float h[8];
-  uint32_t m = 0;
-  const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + c);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t p = __hip_atomic_load(src + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    h[2 * i] = __uint_as_float((uint32_t)p);
-    h[2 * i + 1] = __uint_as_float((uint32_t)(p >> 32));
-    m = max(m, max((uint32_t)p & 0x7fffffffu, (uint32_t)(p >> 32) & 0x7fffffffu));
-  }
-  const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
-  *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)to * a.inter + c) = quant8(h, s);
-  if ((tid & 15) == 0) a.hs[(int64_t)to * nb + blk] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -320,41 +367,17 @@ __global__ __launch_bounds__(kThreads) void decode_fc1_kernel(DecodeArgs a) {
 // K-block) pairs of the call are split evenly over the waves in order.
 template <int F, int D>
 __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
-  __shared__ Routes routes;
-  __shared__ int32_t raw[kSlots];
-  __shared__ int32_t expert[kSlots];          // the call's experts, by first route
-  __shared__ int16_t row[kSlots][kCols];      // route of (expert, token), -1 none
-  __shared__ int32_t n_experts;
+  __shared__ DecodePlan plan;
   __shared__ v4f red[kWaves][F][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  stage_routes(a, routes, raw);
-  const int n = a.tokens * a.top_k;
-  if (wave == 0) {
-    // first routes of the lane's two slots
-    bool f0 = routes.id[lane] >= 0, f1 = routes.id[64 + lane] >= 0;
-    for (int j = 0; j < n; ++j) {
-      const int o = routes.id[j];
-      if (j < lane && o == routes.id[lane]) f0 = false;
-      if (j < 64 + lane && o == routes.id[64 + lane]) f1 = false;
-    }
-    const uint64_t b0 = __ballot(f0), b1 = __ballot(f1), below = (1ull << lane) - 1;
-    if (f0) expert[__popcll(b0 & below)] = routes.id[lane];
-    if (f1) expert[__popcll(b0) + __popcll(b1 & below)] = routes.id[64 + lane];
-    if (lane == 0) n_experts = __popcll(b0) + __popcll(b1);
+  {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(a.plan);
+    uint32_t* to = reinterpret_cast<uint32_t*>(&plan);
+    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kThreads) to[i] = from[i];
   }
   __syncthreads();
-  const int ne = __builtin_amdgcn_readfirstlane(n_experts);
-  for (int i = tid; i < ne * kCols; i += kThreads) {
-    const int t = i & 15, e = expert[i >> 4];
-    int r = -1;
-    if (t < a.tokens)
-      for (int k = a.top_k - 1; k >= 0; --k)
-        if (routes.id[t * a.top_k + k] == e) r = t * a.top_k + k;
-    row[i >> 4][t] = (int16_t)r;
-  }
-  __syncthreads();
-
+  const int ne = __builtin_amdgcn_readfirstlane(plan.experts);
   const int col = lane & 15, grp = lane >> 4;
   const int nb = a.inter / 128, n_tiles = (a.hidden + 255) / 256;
   const int tile = blockIdx.x;
@@ -370,26 +393,19 @@ __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
   Stage st[D];
   int ln = p0 / nb, lk = p0 - ln * nb;  // pair of the next load
   auto load = [&](Stage& s) {
-    const int e = __builtin_amdgcn_readfirstlane(expert[ln]);
-    const int r = row[ln][col];
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert[ln]);
+    const int r = plan.row[ln * kCols + col];
     const uint8_t* p =
         a.w2 + (((int64_t)e * n_tiles + nt) * nb + lk) * (int64_t)kTileBytes + rb * kFragBytes + lane * 16;
 #pragma unroll
     for (int f = 0; f < F; ++f) s.w[f] = load_frag_nt(p + f * kFragBytes);
-    const int64_t hr = r >= 0 ? r : 0;
+    const int64_t hr = r >= 0 ? r : 0;  // some row; the column does not count
     const u32x4* q = reinterpret_cast<const u32x4*>(a.hq + hr * a.inter + lk * 128 + grp * 32);
     s.h[0] = q[0];
     s.h[1] = q[1];
     s.sh = a.hs[hr * nb + lk];
     s.sw = a.w2_scale[((int64_t)e * (a.hidden / 128) + tile * F / 8) * nb + lk];
-    // the weights of a repeated id add up (only without route checks)
-    float rw = 0.0f;
-    if (r >= 0) {
-      rw = routes.w[r];
-      for (int k = r + 1; k < (r / a.top_k + 1) * a.top_k; ++k)
-        if (routes.id[k] == e) rw += routes.w[k];
-    }
-    s.rw = r >= 0 ? rw : 0.0f;
+    s.rw = plan.weight[ln * kCols + col];
     if (r < 0) s.sh = -1.0f;  // a scale is not negative: the column has no such route
     if (++lk == nb) {
       lk = 0;
@@ -439,17 +455,33 @@ __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
   }
 }
 
+template <int NK, int D>
+void launch_fc1(const DecodeArgs& a, hipStream_t s) {
+  // a task at least per workgroup, at most one workgroup per CU
+  const int64_t tasks = (int64_t)(a.tokens * a.top_k) * (a.inter / 16);
+  const unsigned grid = (unsigned)(tasks < a.grid ? tasks : a.grid);
+  hipLaunchKernelGGL((decode_fc1_kernel<NK, D>), dim3(grid), dim3(kThreads), 0, s, a);
+}
+
 }  // namespace
 
 int launch_decode(const DecodeArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  constexpr int F1 = 2, F2 = 1;
-  const dim3 g1(a.inter / (16 * F1), a.tokens * a.top_k), g2(a.hidden / (16 * F2)), block(kThreads);
-  if (a.x_scale)
-    hipLaunchKernelGGL((decode_fc1_kernel<F1, false, 3>), g1, block, 0, s, a);
+  constexpr int F2 = 1;
+  const int per_wave = (a.hidden / 128 + kWaves - 1) / kWaves;  // K-blocks of FC1
+  if (per_wave <= 1)
+    launch_fc1<1, 1>(a, s);
+  else if (per_wave <= 2)
+    launch_fc1<2, 2>(a, s);
+  else if (per_wave <= 4)
+    launch_fc1<4, 4>(a, s);
+  else if (per_wave <= 7)
+    launch_fc1<7, 7>(a, s);
+  else if (per_wave <= 10)
+    launch_fc1<10, 5>(a, s);
   else
-    hipLaunchKernelGGL((decode_fc1_kernel<F1, true, 2>), g1, block, 0, s, a);
-  hipLaunchKernelGGL((decode_fc2_kernel<F2, 4>), g2, block, 0, s, a);
+    launch_fc1<16, 2>(a, s);
+  hipLaunchKernelGGL((decode_fc2_kernel<F2, 4>), dim3(a.hidden / (16 * F2)), dim3(kThreads), 0, s, a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

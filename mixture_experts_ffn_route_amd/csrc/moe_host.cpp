@@ -167,10 +167,10 @@ static Layout layout_for(const moe_config_t& cfg, const Tactic& t, int32_t max_r
   L.size[MOE_REGION_ARRIVE] = (cfg.flags & MOE_FLAG_FUSED_COMBINE) ? (int64_t)max_rows * ((H + 255) / 256) * 4 : 0;
   // compaction: per-(workgroup, expert) bases, per-workgroup status bits, the arrival counter
   L.size[kRegionBlkBase] = (L.compact_blocks * (E + 1) + 1) * 4;
-  // the few-token layer: FP32 h, its codes and scales, and arrival counters
+  // the few-token layer: FP32 h, its codes and scales, the plan, and arrival counters
   if (weights) {
     const int64_t slots = (int64_t)(max_rows < kDecodeTokens ? max_rows : kDecodeTokens) * K;
-    L.size[kRegionDecode] = slots * I * 5 + slots * (I / 128) * 4;
+    L.size[kRegionDecode] = slots * I * 5 + slots * (I / 128) * 4 + sizeof(DecodePlan);
     L.size[kRegionDecodeArrive] = slots * (I / 128) * 4;
   }
   size_t off = 0;

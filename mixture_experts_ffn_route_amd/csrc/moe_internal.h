@@ -224,6 +224,14 @@ int launch_fill_zero(uint32_t* p, int64_t words, void* stream);
 
 // The layer for at most kDecodeTokens tokens in two launches (moe_decode.hip).
 constexpr int kDecodeTokens = 16;
+constexpr int kDecodeSlots = kDecodeTokens * 8;  // routes at most
+// What FC1 makes of the call's routes, for FC2.
+struct DecodePlan {
+  int32_t experts;                               // experts with a route
+  int32_t expert[kDecodeSlots];                  // in the order of their first routes
+  int32_t row[kDecodeSlots * kDecodeTokens];     // [expert][token]: route, -1 none
+  float weight[kDecodeSlots * kDecodeTokens];    // its weight
+};
 struct DecodeArgs {
   const void* x;            // bf16 [T, H], or e4m3 [T, H] with x_scale
   const float* x_scale;     // [T, H/128] or null
@@ -238,7 +246,9 @@ struct DecodeArgs {
   float* hf;                // [T * K, I] FP32 h
   uint8_t* hq;              // [T * K, I] e4m3 h
   float* hs;                // [T * K, I/128]
-  int32_t* arrive;          // [T * K, I/128], zero between calls: FC1 workgroups done with a block of h
+  int32_t* arrive;          // [T * K, I/128], zero between calls: FC1 tasks done of an expert's block of h
+  DecodePlan* plan;
+  int32_t grid;             // FC1 workgroups at most (one per CU)
   uint16_t* out;            // bf16 [T, H]
   uint32_t* status;         // MOE_DEV_* bits of the call, or null
 };
