@@ -36,7 +36,9 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
-constexpr int kWaves = 8;
+constexpr int kWaves = 8;                // waves that stream weights
+constexpr int kRing = 4;                 // FC1: finishing waves, and sums between them and the streaming ones
+constexpr int kFc1Threads = (kWaves + kRing) * 64;
 constexpr int kCols = kDecodeTokens;     // MFMA columns
 constexpr int kSlots = kDecodeSlots;
 constexpr int kTileBytes = 32 * 1024;    // a 256 x 128 weight tile
@@ -104,7 +106,7 @@ __device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, Deco
     id = a.topk_idx[i];
     w = a.topk_w[i];
   }
-  for (int e = i; e < a.num_experts; e += kThreads) r.first[e] = kSlots;
+  for (int e = i; e < a.num_experts; e += blockDim.x) r.first[e] = kSlots;
   if (i == 0) r.status = 0u;
   uint32_t bits = 0;
   if (id < -1 || id >= a.num_experts) {
@@ -142,7 +144,7 @@ __device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, Deco
   }
   __syncthreads();
   const int ne = plan.experts;
-  for (int j = i; j < ne * kCols; j += kThreads) {
+  for (int j = i; j < ne * kCols; j += blockDim.x) {
     const int t = j & 15, e = plan.expert[j >> 4];
     int slot = -1;
     float sum = 0.0f;
@@ -163,23 +165,146 @@ __device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, Deco
 // ---------------------------------------------------------------------------
 
 // One workgroup per CU walks over tasks of 16 columns of h of one expert.
-// Wave w takes K-blocks [w kbs / 8, (w + 1) kbs / 8), at most NK, of every
-// task: it keeps its part of the token rows, quantised, in registers for all
-// tasks, and has D K-blocks of weights in flight, running on into the next
-// task.  The waves' sums of a task meet in LDS; one wave, another one each
-// task, finishes it while the others stream on.
+// Eight waves stream: wave w takes K-blocks [w kbs / 8, (w + 1) kbs / 8), at
+// most NK, of every task; it keeps its part of the token rows, quantised, in
+// registers for all tasks, and has D K-blocks of weights in flight, running on
+// into the next task.  Four more waves take turns at finishing tasks: sum of
+// the eight parts, SwiGLU, the stores of h, and the quantisation of a
+// 128-column block that is complete.  They wait for memory several times a
+// task, which a streaming wave could only do by letting its loads run dry.
+// The two kinds meet in a ring of kRing sums in LDS with counters, not
+// barriers, so no wave waits for the others' memory.
 template <int NK, int D>
-__global__ __launch_bounds__(kThreads, 1) void decode_fc1_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a) {
   static_assert(NK % D == 0, "a K-block's ring slot is the same in every task");
   __shared__ Routes routes;
   __shared__ DecodePlan plan;
-  __shared__ v4f red[2][kWaves][2][64];  // [task parity][wave][gate, up][lane]
+  __shared__ v4f red[kRing][kWaves][2][64];  // [task % kRing][wave][gate, up][lane]
+  __shared__ int32_t filled[kRing];           // streaming waves that have put their sums, over all tasks
+  __shared__ int32_t emptied[kRing];          // tasks finished
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, grp = lane >> 4;
   const int kbs = a.hidden / 128, nb = a.inter / 128;
-  const int kb0 = wave * kbs / kWaves, nk = (wave + 1) * kbs / kWaves - kb0;
 
+  if (tid < kRing) filled[tid] = emptied[tid] = 0;
+  plan_routes(a, routes, plan);  // ends with a barrier
+  if (blockIdx.x == 0) {  // FC2 takes the plan from here
+    if (tid == 0 && a.status) *a.status = routes.status;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(&plan);
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.plan);
+    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kFc1Threads) to[i] = from[i];
+  }
+  const int per_expert = a.inter / 16;
+  const int tasks = __builtin_amdgcn_readfirstlane(plan.experts) * per_expert;
+
+  const int stride = gridDim.x;
+  const auto task_at = [&](int task, int& n, int& blk, int& sub) {
+    n = task / per_expert;
+    const int c = task - n * per_expert;
+    blk = c >> 3;
+    sub = c & 7;
+  };
+
+  if (wave >= kWaves) {
+    // ---- finishing waves: turns wave - kWaves, + kRing, ... ----
+    int turn = wave - kWaves;
+    for (int task = blockIdx.x + turn * stride; task < tasks; task += kRing * stride, turn += kRing) {
+      const int buf = turn % kRing, round = turn / kRing;
+      while (__hip_atomic_load(&filled[buf], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < kWaves * (round + 1))
+        __builtin_amdgcn_s_sleep(1);
+      v4f g = red[buf][0][0][lane], u = red[buf][0][1][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) {
+        g += red[buf][w][0][lane];
+        u += red[buf][w][1][lane];
+      }
+      if (lane == 0) __hip_atomic_store(&emptied[buf], round + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+      int n, blk, sub;
+      task_at(task, n, blk, sub);
+      // lane l: columns 4 (l / 16) + 0..3 of the tile, token l % 16
+      const int slot = plan.row[n * kCols + col];
+      if (slot >= 0) {
+        uint64_t* dst = reinterpret_cast<uint64_t*>(a.hf + (int64_t)slot * a.inter + blk * 128 + sub * 16 + grp * 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t lo = __float_as_uint(swiglu(g[2 * i], u[2 * i]));
+          const uint32_t hi = __float_as_uint(swiglu(g[2 * i + 1], u[2 * i + 1]));
+          __hip_atomic_store(dst + i, (uint64_t)lo | ((uint64_t)hi << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+      // The stores are write-through (agent scope) and complete before the
+      // arrival; the eighth to arrive at a 128-column block reads it with
+      // agent-scope loads, so no cache has to be flushed.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      int old = 0;
+      if (lane == 0) {
+        int32_t* ctr = a.arrive + n * nb + blk;
+        old = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (old == 7) __hip_atomic_store(ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+      }
+      if (__builtin_amdgcn_readfirstlane(old) != 7) continue;
+      for (int t0 = 0; t0 < a.tokens; t0 += 4) {  // 16 lanes per row, 8 columns each
+        const int to = plan.row[n * kCols + t0 + grp];
+        if (to < 0) continue;
+        const int c = blk * 128 + col * 8;
+        const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + c);
+        uint64_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = __hip_atomic_load(src + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        float h[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[2 * i] = __uint_as_float((uint32_t)p[i]);
+          h[2 * i + 1] = __uint_as_float((uint32_t)(p[i] >> 32));
+          m = max(m, max((uint32_t)p[i] & 0x7fffffffu, (uint32_t)(p[i] >> 32) & 0x7fffffffu));
+        }
+        const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
+        *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)to * a.inter + c) = quant8(h, s);
+        if (col == 0) a.hs[(int64_t)to * nb + blk] = s;
+      }
+    }
+    return;
+  }
+
+  // ---- streaming waves ----
+  const int kb0 = wave * kbs / kWaves, nk = (wave + 1) * kbs / kWaves - kb0;
+  struct Stage {
+    Frag g, u;
+  };
+  Stage st[D];
+  // weights of a task's column tile; a task past the last repeats the last
+  auto base_of = [&](int task) -> const uint8_t* {
+    int n, blk, sub;
+    task_at(min(task, tasks - 1), n, blk, sub);
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
+    return a.w13 + (((int64_t)e * nb + blk) * kbs + kb0) * kTileBytes + sub * kFragBytes + lane * 16;
+  };
+  // weight scales of the wave's K-blocks: gate in lanes 0.., up in lanes 32..
+  auto scales_of = [&](int task) -> float {
+    int n, blk, sub;
+    task_at(min(task, tasks - 1), n, blk, sub);
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
+    const int j = min(lane & 31, nk - 1);
+    return a.w13_scale[((int64_t)e * 2 * nb + (lane < 32 ? blk : nb + blk)) * kbs + kb0 + j];
+  };
+  auto load = [&](Stage& s, const uint8_t* base, int k) {
+    const uint8_t* p = base + (int64_t)k * kTileBytes;
+    s.g = load_frag_nt(p);
+    s.u = load_frag_nt(p + 8 * kFragBytes);
+  };
+  int task = blockIdx.x;
+  if (task >= tasks) return;
+  const uint8_t* base = nullptr;
+  float wsc = 0.0f;
+  if (nk > 0) {
+    base = base_of(task);
+    wsc = scales_of(task);
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+      if (k < nk) load(st[k], base, k);
+  }
   // the wave's token operands: columns past the last token repeat it
   v8i xb[NK];
   float sx[NK];
@@ -223,63 +348,11 @@ __global__ __launch_bounds__(kThreads, 1) void decode_fc1_kernel(DecodeArgs a) {
     }
   }
 
-  plan_routes(a, routes, plan);
-  if (blockIdx.x == 0) {  // FC2 takes the plan from here
-    if (tid == 0 && a.status) *a.status = routes.status;
-    const uint32_t* from = reinterpret_cast<const uint32_t*>(&plan);
-    uint32_t* to = reinterpret_cast<uint32_t*>(a.plan);
-    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kThreads) to[i] = from[i];
-  }
-  const int per_expert = a.inter / 16;
-  const int tasks = __builtin_amdgcn_readfirstlane(plan.experts) * per_expert;
-
-  struct Stage {
-    Frag g, u;
-  };
-  Stage st[D];
-  float wsc = 0.0f, wsc_next = 0.0f;
-  // weights of a task's column tile; a task past the last repeats the last
-  auto task_at = [&](int task, int& n, int& blk, int& sub) {
-    n = task / per_expert;
-    const int c = task - n * per_expert;
-    blk = c >> 3;
-    sub = c & 7;
-  };
-  auto base_of = [&](int task) -> const uint8_t* {
-    int n, blk, sub;
-    task_at(min(task, tasks - 1), n, blk, sub);
-    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
-    return a.w13 + (((int64_t)e * nb + blk) * kbs + kb0) * kTileBytes + sub * kFragBytes + lane * 16;
-  };
-  // weight scales of the wave's K-blocks: gate in lanes 0.., up in lanes 32..
-  auto scales_of = [&](int task) -> float {
-    int n, blk, sub;
-    task_at(min(task, tasks - 1), n, blk, sub);
-    const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
-    const int j = min(lane & 31, nk - 1);
-    return a.w13_scale[((int64_t)e * 2 * nb + (lane < 32 ? blk : nb + blk)) * kbs + kb0 + j];
-  };
-  auto load = [&](Stage& s, const uint8_t* base, int k) {
-    const uint8_t* p = base + (int64_t)k * kTileBytes;
-    s.g = load_frag_nt(p);
-    s.u = load_frag_nt(p + 8 * kFragBytes);
-  };
-
-  const int stride = gridDim.x;
-  int task = blockIdx.x;
-  const uint8_t* base = nullptr;
-  if (task < tasks && nk > 0) {
-    base = base_of(task);
-    wsc = scales_of(task);
-#pragma unroll
-    for (int k = 0; k < D; ++k)
-      if (k < nk) load(st[k], base, k);
-  }
   for (int turn = 0; task < tasks; task += stride, ++turn) {
     v4f accg = {0.0f, 0.0f, 0.0f, 0.0f}, accu = accg;
     if (nk > 0) {
       const uint8_t* next = base_of(task + stride);
-      wsc_next = scales_of(task + stride);
+      const float wsc_next = scales_of(task + stride);
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         if (k < nk) {
@@ -299,63 +372,13 @@ __global__ __launch_bounds__(kThreads, 1) void decode_fc1_kernel(DecodeArgs a) {
       base = next;
       wsc = wsc_next;
     }
-    const int par = turn & 1;
-    red[par][wave][0][lane] = accg;
-    red[par][wave][1][lane] = accu;
-    __syncthreads();  // the only one per task: the wave that reads red gets here before it is written again
-    if (wave != (turn & (kWaves - 1))) continue;
-
-    int n, blk, sub;
-    task_at(task, n, blk, sub);
-    v4f g = red[par][0][0][lane], u = red[par][0][1][lane];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      g += red[par][w][0][lane];
-      u += red[par][w][1][lane];
-    }
-    // lane l: columns 4 (l / 16) + 0..3 of the tile, token l % 16
-    const int slot = plan.row[n * kCols + col];
-    if (slot >= 0) {
-      uint64_t* dst = reinterpret_cast<uint64_t*>(a.hf + (int64_t)slot * a.inter + blk * 128 + sub * 16 + grp * 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __float_as_uint(swiglu(g[2 * i], u[2 * i]));
-        const uint32_t hi = __float_as_uint(swiglu(g[2 * i + 1], u[2 * i + 1]));
-        __hip_atomic_store(dst + i, (uint64_t)lo | ((uint64_t)hi << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
-    // The stores are write-through (agent scope) and complete before the
-    // arrival; the eighth to arrive at a 128-column block reads it with
-    // agent-scope loads, so no cache has to be flushed.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    int old = 0;
-    if (lane == 0) {
-      int32_t* ctr = a.arrive + n * nb + blk;
-      old = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (old == 7) __hip_atomic_store(ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
-    }
-    if (__builtin_amdgcn_readfirstlane(old) != 7) continue;
-    for (int t0 = 0; t0 < a.tokens; t0 += 4) {  // 16 lanes per row, 8 columns each
-      const int t = t0 + grp;
-      const int to = t < kCols ? plan.row[n * kCols + t] : -1;
-      if (to < 0) continue;
-      const int c = blk * 128 + col * 8;
-      const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + c);
-      uint64_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = __hip_atomic_load(src + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      float h[8];
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[2 * i] = __uint_as_float((uint32_t)p[i]);
-        h[2 * i + 1] = __uint_as_float((uint32_t)(p[i] >> 32));
-        m = max(m, max((uint32_t)p[i] & 0x7fffffffu, (uint32_t)(p[i] >> 32) & 0x7fffffffu));
-      }
-      const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
-      *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)to * a.inter + c) = quant8(h, s);
-      if (col == 0) a.hs[(int64_t)to * nb + blk] = s;
-    }
+    const int buf = turn % kRing, round = turn / kRing;
+    while (__hip_atomic_load(&emptied[buf], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < round)
+      __builtin_amdgcn_s_sleep(1);
+    red[buf][wave][0][lane] = accg;
+    red[buf][wave][1][lane] = accu;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (lane == 0) __hip_atomic_fetch_add(&filled[buf], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
   }
 }
 
@@ -460,7 +483,7 @@ void launch_fc1(const DecodeArgs& a, hipStream_t s) {
   // a task at least per workgroup, at most one workgroup per CU
   const int64_t tasks = (int64_t)(a.tokens * a.top_k) * (a.inter / 16);
   const unsigned grid = (unsigned)(tasks < a.grid ? tasks : a.grid);
-  hipLaunchKernelGGL((decode_fc1_kernel<NK, D>), dim3(grid), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((decode_fc1_kernel<NK, D>), dim3(grid), dim3(kFc1Threads), 0, s, a);
 }
 
 }  // namespace
@@ -469,16 +492,12 @@ int launch_decode(const DecodeArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   constexpr int F2 = 1;
   const int per_wave = (a.hidden / 128 + kWaves - 1) / kWaves;  // K-blocks of FC1
-  if (per_wave <= 1)
-    launch_fc1<1, 1>(a, s);
-  else if (per_wave <= 2)
+  if (per_wave <= 2)
     launch_fc1<2, 2>(a, s);
   else if (per_wave <= 4)
-    launch_fc1<4, 4>(a, s);
-  else if (per_wave <= 7)
-    launch_fc1<7, 7>(a, s);
-  else if (per_wave <= 10)
-    launch_fc1<10, 5>(a, s);
+    launch_fc1<4, 2>(a, s);
+  else if (per_wave <= 8)
+    launch_fc1<8, 2>(a, s);
   else
     launch_fc1<16, 2>(a, s);
   hipLaunchKernelGGL((decode_fc2_kernel<F2, 4>), dim3(a.hidden / (16 * F2)), dim3(kThreads), 0, s, a);
