@@ -77,74 +77,81 @@ __device__ __forceinline__ v4f add_scaled(v4f acc, const v4f& p, float sx, float
   return acc;
 }
 
-// Maximum over the four lanes that share a token (l, l ^ 16, l ^ 32, l ^ 48).
-__device__ __forceinline__ uint32_t col_max(uint32_t v) {
-  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  v = max((uint32_t)a[0], (uint32_t)a[1]);
-  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  return max((uint32_t)b[0], (uint32_t)b[1]);
-}
-
 // Checked routes of the call in LDS: ids (-1 masked) and weights, with
-// moe_stage_inputs' rules, and the experts they reach.
+// moe_stage_inputs' rules.
 struct Routes {
   int32_t raw[kSlots];
   int32_t id[kSlots];
   float w[kSlots];
-  int32_t first[kMaxExperts];  // lowest slot of an expert
-  uint32_t status;
 };
 
-// Fills r and the plan: the experts in the order of their first routes, and
-// per expert and token the route (the lowest, -1 for none) and its weight.  A
-// repeated id, which only stays without route checks, adds up in the weight.
-__device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, DecodePlan& plan) {
-  const int n = a.tokens * a.top_k, i = threadIdx.x, lane = i & 63;
-  int id = -1;
-  float w = 0.0f;
-  if (i < n) {
-    id = a.topk_idx[i];
-    w = a.topk_w[i];
-  }
-  for (int e = i; e < a.num_experts; e += blockDim.x) r.first[e] = kSlots;
-  if (i == 0) r.status = 0u;
+// Order of LDS accesses between the lanes of one wave, whose LDS operations
+// complete in order: a fence for the compiler.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// By one wave: checks the routes and lists the experts they reach in the
+// order of their first routes.  Returns the MOE_DEV_* bits.
+__device__ __forceinline__ uint32_t check_routes(const DecodeArgs& a, Routes& r, DecodePlan& plan, int lane) {
+  const int n = a.tokens * a.top_k;
+  int id[2];
+  float w[2];
   uint32_t bits = 0;
-  if (id < -1 || id >= a.num_experts) {
-    bits = MOE_DEV_BAD_EXPERT;
-    id = -1;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = h * 64 + lane;
+    id[h] = i < n ? a.topk_idx[i] : -1;
+    w[h] = i < n ? a.topk_w[i] : 0.0f;
   }
-  if (i < kSlots) r.raw[i] = id;
-  __syncthreads();
-  if (i < kSlots) {
-    if ((a.flags & MOE_FLAG_CHECK_ROUTES) && id >= 0) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (id[h] < -1 || id[h] >= a.num_experts) {
+      bits |= MOE_DEV_BAD_EXPERT;
+      id[h] = -1;
+    }
+    r.raw[h * 64 + lane] = id[h];
+  }
+  wave_fence();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = h * 64 + lane;
+    if ((a.flags & MOE_FLAG_CHECK_ROUTES) && id[h] >= 0) {
       // the lowest slot of an id stays, whatever its weight
       bool again = false;
-      for (int j = i - i % a.top_k; j < i; ++j) again |= r.raw[j] == id;
+      for (int j = i - i % a.top_k; j < i; ++j) again |= r.raw[j] == id[h];
       if (again) {
         bits |= MOE_DEV_DUPLICATE;
-        id = -1;
-      } else if (!isfinite(w)) {
+        id[h] = -1;
+      } else if (!isfinite(w[h])) {
         bits |= MOE_DEV_NONFINITE;
-        id = -1;
+        id[h] = -1;
       }
     }
-    r.id[i] = id;
-    r.w[i] = id >= 0 ? w : 0.0f;
-    if (id >= 0) atomicMin(&r.first[id], i);
-    if (bits) atomicOr(&r.status, bits);
+    r.id[i] = id[h];
+    r.w[i] = id[h] >= 0 ? w[h] : 0.0f;
   }
-  __syncthreads();
-  if (i < 64) {
-    const int a0 = r.id[lane], a1 = r.id[64 + lane];
-    const bool f0 = a0 >= 0 && r.first[a0] == lane, f1 = a1 >= 0 && r.first[a1] == 64 + lane;
-    const uint64_t b0 = __ballot(f0), b1 = __ballot(f1), below = (1ull << lane) - 1;
-    if (f0) plan.expert[__popcll(b0 & below)] = a0;
-    if (f1) plan.expert[__popcll(b0) + __popcll(b1 & below)] = a1;
-    if (lane == 0) plan.experts = __popcll(b0) + __popcll(b1);
+  wave_fence();
+  bool first[2] = {id[0] >= 0, id[1] >= 0};
+  for (int j = 0; j < n; ++j) {
+    const int o = r.id[j];
+    if (j < lane && o == id[0]) first[0] = false;
+    if (j < 64 + lane && o == id[1]) first[1] = false;
   }
-  __syncthreads();
-  const int ne = plan.experts;
-  for (int j = i; j < ne * kCols; j += blockDim.x) {
+  const uint64_t b0 = __ballot(first[0]), b1 = __ballot(first[1]), below = (1ull << lane) - 1;
+  if (first[0]) plan.expert[__popcll(b0 & below)] = id[0];
+  if (first[1]) plan.expert[__popcll(b0) + __popcll(b1 & below)] = id[1];
+  if (lane == 0) plan.experts = __popcll(b0) + __popcll(b1);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) bits |= __shfl_xor(bits, m, 64);
+  return bits;
+}
+
+// Per expert and token the route (the lowest, -1 for none) and its weight; a
+// repeated id, which only stays without route checks, adds up in the weight.
+__device__ __forceinline__ void map_routes(const DecodeArgs& a, const Routes& r, DecodePlan& plan, int i, int threads) {
+  for (int j = i; j < plan.experts * kCols; j += threads) {
     const int t = j & 15, e = plan.expert[j >> 4];
     int slot = -1;
     float sum = 0.0f;
@@ -157,59 +164,153 @@ __device__ __forceinline__ void plan_routes(const DecodeArgs& a, Routes& r, Deco
     plan.row[j] = slot;
     plan.weight[j] = sum;
   }
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // FC1
 // ---------------------------------------------------------------------------
 
+// Codes and scale of one 128-column block of h: 16 lanes, 8 columns each.
+__device__ __forceinline__ void store_block(const DecodeArgs& a, const float h[8], int row, int blk, int lane16) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+  const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
+  *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)row * a.inter + blk * 128 + lane16 * 8) = quant8(h, s);
+  if (lane16 == 0) a.hs[(int64_t)row * (a.inter / 128) + blk] = s;
+}
+
 // One workgroup per CU walks over tasks of 16 columns of h of one expert.
 // Eight waves stream: wave w takes K-blocks [w kbs / 8, (w + 1) kbs / 8), at
 // most NK, of every task; it keeps its part of the token rows, quantised, in
-// registers for all tasks, and has D K-blocks of weights in flight, running on
-// into the next task.  Four more waves take turns at finishing tasks: sum of
+// registers for all tasks, and has one K-block of weights (4 KB) in flight,
+// running on into the next task.  More in flight only makes every wait for
+// memory longer: a copy of this access pattern without arithmetic reads 6.96
+// TB/s with one K-block per wave, 6.52 with two and 6.50 with seven (939 MB),
+// and the call takes 67 us against 69 with two (T=1 H=7168 I=2048 K=8).
+// Four more waves take turns at finishing tasks: sum of
 // the eight parts, SwiGLU, the stores of h, and the quantisation of a
 // 128-column block that is complete.  They wait for memory several times a
 // task, which a streaming wave could only do by letting its loads run dry.
 // The two kinds meet in a ring of kRing sums in LDS with counters, not
 // barriers, so no wave waits for the others' memory.
-template <int NK, int D>
+template <int NK>
 __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a) {
-  static_assert(NK % D == 0, "a K-block's ring slot is the same in every task");
   __shared__ Routes routes;
   __shared__ DecodePlan plan;
   __shared__ v4f red[kRing][kWaves][2][64];  // [task % kRing][wave][gate, up][lane]
   __shared__ int32_t filled[kRing];           // streaming waves that have put their sums, over all tasks
   __shared__ int32_t emptied[kRing];          // tasks finished
+  __shared__ int32_t mapped;                  // finishing waves whose part of the plan stands
+  __shared__ float hbuf[2][kCols][128];       // h of a block that one workgroup makes alone, [block parity]
+  __shared__ int32_t done[2];                 // its finished sixteenths
+  __shared__ float xscale[sizeof(red) / 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, grp = lane >> 4;
   const int kbs = a.hidden / 128, nb = a.inter / 128;
 
-  if (tid < kRing) filled[tid] = emptied[tid] = 0;
-  plan_routes(a, routes, plan);  // ends with a barrier
-  if (blockIdx.x == 0) {  // FC2 takes the plan from here
-    if (tid == 0 && a.status) *a.status = routes.status;
-    const uint32_t* from = reinterpret_cast<const uint32_t*>(&plan);
-    uint32_t* to = reinterpret_cast<uint32_t*>(a.plan);
-    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kFc1Threads) to[i] = from[i];
+  const int kb0 = wave * kbs / kWaves, nk = wave < kWaves ? (wave + 1) * kbs / kWaves - kb0 : 0;
+  // The streaming waves' token operands (columns past the last token repeat
+  // it), while a finishing wave lists the experts.
+  v8i xb[NK];
+  float sx[NK];
+  if (wave == kWaves) {
+    if (lane < kRing) filled[lane] = emptied[lane] = 0;
+    if (lane < 2) done[lane] = 0;
+    if (lane == kRing) mapped = 0;
+    const uint32_t bits = check_routes(a, routes, plan, lane);
+    if (blockIdx.x == 0 && lane == 0 && a.status) *a.status = bits;
   }
-  const int per_expert = a.inter / 16;
-  const int tasks = __builtin_amdgcn_readfirstlane(plan.experts) * per_expert;
-
-  const int stride = gridDim.x;
-  const auto task_at = [&](int task, int& n, int& blk, int& sub) {
-    n = task / per_expert;
-    const int c = task - n * per_expert;
-    blk = c >> 3;
-    sub = c & 7;
+  if (a.x_scale) {
+    if (wave < kWaves && nk > 0) {
+      const int64_t t = min(col, a.tokens - 1);
+      const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const int at = min(k, nk - 1);
+        const u32x4* q = reinterpret_cast<const u32x4*>(x + at * 128);
+        xb[k] = operand(Frag{q[0], q[1]});
+        sx[k] = a.x_scale[t * kbs + kb0 + at];
+      }
+    }
+  } else {
+    // BF16 rows: each 128-column block is quantised once, by eight lanes, into
+    // the LDS that holds sums later, as many tokens at a time as fit.
+    uint8_t* const codes = reinterpret_cast<uint8_t*>(&red[0][0][0][0]);
+    const int fit = min(kCols, (int)sizeof(red) / a.hidden);
+    for (int t0 = 0; t0 < a.tokens; t0 += fit) {
+      const int rows = min(fit, a.tokens - t0);
+      for (int g = tid >> 3; g < rows * kbs; g += kFc1Threads / 8) {
+        const int t = g / kbs, kb = g - t * kbs, c = kb * 128 + (tid & 7) * 16;
+        const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) +
+                                                        (int64_t)(t0 + t) * a.hidden + c);
+        const u32x4 r[2] = {q[0], q[1]};
+        float v[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w = r[i / 4][i % 4];
+          v[2 * i] = bf16_to_f32(w & 0xffffu);
+          v[2 * i + 1] = bf16_to_f32(w >> 16);
+          m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
+        }
+        const float scale = __uint_as_float(row8_max(m)) / kE4m3Max;
+        const q_u32x2 lo = quant8(v, scale), hi = quant8(v + 8, scale);
+        *reinterpret_cast<u32x4*>(codes + t * a.hidden + c) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        if ((tid & 7) == 0) xscale[t * kbs + kb] = scale;
+      }
+      __syncthreads();
+      const int t = min(col, a.tokens - 1) - t0;
+      if (nk > 0 && t >= 0 && t < rows) {
+        const uint8_t* x = codes + t * a.hidden + kb0 * 128 + grp * 32;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const int at = min(k, nk - 1);
+          const u32x4* q = reinterpret_cast<const u32x4*>(x + at * 128);
+          xb[k] = operand(Frag{q[0], q[1]});
+          sx[k] = xscale[t * kbs + kb0 + at];
+        }
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  // Tasks.  Whole blocks of 128 columns (eight tasks in a row, whose h never
+  // leaves the workgroup) as long as there is one for every workgroup; the
+  // tasks of the blocks that remain are dealt out one by one.
+  const int blocks = __builtin_amdgcn_readfirstlane(plan.experts) * nb;
+  const int grid = gridDim.x;
+  const int whole = blocks / grid * 8;  // of this workgroup
+  const int loose = (blocks - blocks / grid * grid) * 8;
+  const int turns = whole + (loose > (int)blockIdx.x ? (loose - (int)blockIdx.x + grid - 1) / grid : 0);
+  const auto task_at = [&](int turn, int& n, int& blk, int& sub) {
+    int b;
+    if (turn < whole) {
+      b = (turn >> 3) * grid + (int)blockIdx.x;
+      sub = turn & 7;
+    } else {
+      const int i = (turn - whole) * grid + (int)blockIdx.x;
+      b = (whole >> 3) * grid + (i >> 3);
+      sub = i & 7;
+    }
+    n = b / nb;
+    blk = b - n * nb;
   };
 
   if (wave >= kWaves) {
     // ---- finishing waves: turns wave - kWaves, + kRing, ... ----
-    int turn = wave - kWaves;
-    for (int task = blockIdx.x + turn * stride; task < tasks; task += kRing * stride, turn += kRing) {
+    map_routes(a, routes, plan, tid - kThreads, kRing * 64);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (lane == 0) __hip_atomic_fetch_add(&mapped, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    while (__hip_atomic_load(&mapped, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < kRing)
+      __builtin_amdgcn_s_sleep(1);
+    if (blockIdx.x == 0) {  // FC2 takes the plan from here
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(&plan);
+      uint32_t* to = reinterpret_cast<uint32_t*>(a.plan);
+      for (int i = tid - kThreads; i < (int)(sizeof(DecodePlan) / 4); i += kRing * 64) to[i] = from[i];
+    }
+    for (int turn = wave - kWaves; turn < turns; turn += kRing) {
       const int buf = turn % kRing, round = turn / kRing;
       while (__hip_atomic_load(&filled[buf], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < kWaves * (round + 1))
         __builtin_amdgcn_s_sleep(1);
@@ -221,17 +322,39 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
       }
       if (lane == 0) __hip_atomic_store(&emptied[buf], round + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
       int n, blk, sub;
-      task_at(task, n, blk, sub);
+      task_at(turn, n, blk, sub);
       // lane l: columns 4 (l / 16) + 0..3 of the tile, token l % 16
       const int slot = plan.row[n * kCols + col];
+      float h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = swiglu(g[i], u[i]);
+      if (turn < whole) {
+        const int par = (turn >> 3) & 1;
+        *reinterpret_cast<v4f*>(&hbuf[par][col][sub * 16 + grp * 4]) = v4f{h[0], h[1], h[2], h[3]};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        int old = 0;
+        if (lane == 0) old = __hip_atomic_fetch_add(&done[par], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (__builtin_amdgcn_readfirstlane(old) != 7) continue;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+        if (lane == 0) __hip_atomic_store(&done[par], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        // The buffer is free for the block after the next: its first sums can
+        // only be put after this wave has emptied a later turn.
+        for (int t0 = 0; t0 < a.tokens; t0 += 4) {  // 16 lanes per row, 8 columns each
+          const int to = plan.row[n * kCols + t0 + grp];
+          if (to < 0) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = hbuf[par][t0 + grp][col * 8 + i];
+          store_block(a, v, to, blk, col);
+        }
+        continue;
+      }
       if (slot >= 0) {
         uint64_t* dst = reinterpret_cast<uint64_t*>(a.hf + (int64_t)slot * a.inter + blk * 128 + sub * 16 + grp * 4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = __float_as_uint(swiglu(g[2 * i], u[2 * i]));
-          const uint32_t hi = __float_as_uint(swiglu(g[2 * i + 1], u[2 * i + 1]));
-          __hip_atomic_store(dst + i, (uint64_t)lo | ((uint64_t)hi << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
+        for (int i = 0; i < 2; ++i)
+          __hip_atomic_store(dst + i, (uint64_t)__float_as_uint(h[2 * i]) | ((uint64_t)__float_as_uint(h[2 * i + 1]) << 32),
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       // The stores are write-through (agent scope) and complete before the
       // arrival; the eighth to arrive at a 128-column block reads it with
@@ -244,47 +367,42 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
         if (old == 7) __hip_atomic_store(ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
       }
       if (__builtin_amdgcn_readfirstlane(old) != 7) continue;
-      for (int t0 = 0; t0 < a.tokens; t0 += 4) {  // 16 lanes per row, 8 columns each
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+      for (int t0 = 0; t0 < a.tokens; t0 += 4) {
         const int to = plan.row[n * kCols + t0 + grp];
         if (to < 0) continue;
-        const int c = blk * 128 + col * 8;
-        const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + c);
+        const uint64_t* src = reinterpret_cast<const uint64_t*>(a.hf + (int64_t)to * a.inter + blk * 128 + col * 8);
         uint64_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = __hip_atomic_load(src + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        float h[8];
-        uint32_t m = 0;
+        float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[2 * i] = __uint_as_float((uint32_t)p[i]);
-          h[2 * i + 1] = __uint_as_float((uint32_t)(p[i] >> 32));
-          m = max(m, max((uint32_t)p[i] & 0x7fffffffu, (uint32_t)(p[i] >> 32) & 0x7fffffffu));
+          v[2 * i] = __uint_as_float((uint32_t)p[i]);
+          v[2 * i + 1] = __uint_as_float((uint32_t)(p[i] >> 32));
         }
-        const float s = __uint_as_float(row16_max(m)) / kE4m3Max;
-        *reinterpret_cast<q_u32x2*>(a.hq + (int64_t)to * a.inter + c) = quant8(h, s);
-        if (col == 0) a.hs[(int64_t)to * nb + blk] = s;
+        store_block(a, v, to, blk, col);
       }
     }
     return;
   }
 
   // ---- streaming waves ----
-  const int kb0 = wave * kbs / kWaves, nk = (wave + 1) * kbs / kWaves - kb0;
   struct Stage {
     Frag g, u;
   };
-  Stage st[D];
-  // weights of a task's column tile; a task past the last repeats the last
-  auto base_of = [&](int task) -> const uint8_t* {
+  Stage st;
+  // weights of a turn's column tile; a turn past the last repeats the last
+  auto base_of = [&](int turn) -> const uint8_t* {
     int n, blk, sub;
-    task_at(min(task, tasks - 1), n, blk, sub);
+    task_at(min(turn, turns - 1), n, blk, sub);
     const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
     return a.w13 + (((int64_t)e * nb + blk) * kbs + kb0) * kTileBytes + sub * kFragBytes + lane * 16;
   };
   // weight scales of the wave's K-blocks: gate in lanes 0.., up in lanes 32..
-  auto scales_of = [&](int task) -> float {
+  auto scales_of = [&](int turn) -> float {
     int n, blk, sub;
-    task_at(min(task, tasks - 1), n, blk, sub);
+    task_at(min(turn, turns - 1), n, blk, sub);
     const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
     const int j = min(lane & 31, nk - 1);
     return a.w13_scale[((int64_t)e * 2 * nb + (lane < 32 ? blk : nb + blk)) * kbs + kb0 + j];
@@ -294,80 +412,31 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
     s.g = load_frag_nt(p);
     s.u = load_frag_nt(p + 8 * kFragBytes);
   };
-  int task = blockIdx.x;
-  if (task >= tasks) return;
+  if (turns == 0) return;
   const uint8_t* base = nullptr;
   float wsc = 0.0f;
   if (nk > 0) {
-    base = base_of(task);
-    wsc = scales_of(task);
-#pragma unroll
-    for (int k = 0; k < D; ++k)
-      if (k < nk) load(st[k], base, k);
+    base = base_of(0);
+    wsc = scales_of(0);
+    load(st, base, 0);
   }
-  // the wave's token operands: columns past the last token repeat it
-  v8i xb[NK];
-  float sx[NK];
-  {
-    const int64_t t = min(col, a.tokens - 1);
-    if (a.x_scale) {
-      const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const int at = k < nk ? k : 0;  // a wave without K-blocks reads the row's first
-        const u32x4* q = reinterpret_cast<const u32x4*>(nk ? x + at * 128 : static_cast<const uint8_t*>(a.x));
-        xb[k] = operand(Frag{q[0], q[1]});
-        sx[k] = a.x_scale[t * kbs + (nk ? kb0 + at : 0)];
-      }
-    } else {
-      const uint16_t* x = static_cast<const uint16_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const u32x4* q = reinterpret_cast<const u32x4*>(nk ? x + (k < nk ? k : 0) * 128
-                                                           : static_cast<const uint16_t*>(a.x));
-        u32x4 r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = q[i];
-        float v[32];
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t w = r[i / 4][i % 4];
-          v[2 * i] = bf16_to_f32(w & 0xffffu);
-          v[2 * i + 1] = bf16_to_f32(w >> 16);
-          m = max(m, max(__float_as_uint(v[2 * i]) & 0x7fffffffu, __float_as_uint(v[2 * i + 1]) & 0x7fffffffu));
-        }
-        sx[k] = __uint_as_float(col_max(m)) / kE4m3Max;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const q_u32x2 c = quant8(v + 8 * i, sx[k]);
-          xb[k][2 * i] = (int)c[0];
-          xb[k][2 * i + 1] = (int)c[1];
-        }
-      }
-    }
-  }
-
-  for (int turn = 0; task < tasks; task += stride, ++turn) {
+  for (int turn = 0; turn < turns; ++turn) {
     v4f accg = {0.0f, 0.0f, 0.0f, 0.0f}, accu = accg;
     if (nk > 0) {
-      const uint8_t* next = base_of(task + stride);
-      const float wsc_next = scales_of(task + stride);
+      const uint8_t* next = base_of(turn + 1);
+      const float wsc_next = scales_of(turn + 1);
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        if (k < nk) {
-          Stage& s = st[k % D];
-          const float sg = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), k));
-          const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), 32 + k));
-          accg = add_scaled(accg, mfma_e4m3(s.g, xb[k]), sx[k], sg);
-          accu = add_scaled(accu, mfma_e4m3(s.u, xb[k]), sx[k], su);
-        }
-        // the K-block D ahead, in this task or the next
-        if (k + D < NK) {
-          if (k + D < nk) load(st[k % D], base, k + D);
-        } else if (k + D - NK < nk) {
-          load(st[k % D], next, k + D - NK);
-        }
+        if (k >= nk) break;
+        const float sg = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), k));
+        const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), 32 + k));
+        const v4f pg = mfma_e4m3(st.g, xb[k]), pu = mfma_e4m3(st.u, xb[k]);
+        if (k + 1 < nk)
+          load(st, base, k + 1);
+        else
+          load(st, next, 0);
+        accg = add_scaled(accg, pg, sx[k], sg);
+        accu = add_scaled(accu, pu, sx[k], su);
       }
       base = next;
       wsc = wsc_next;
@@ -388,16 +457,16 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
 
 // Workgroup `tile`: 16 F columns of the output, all tokens.  The (expert,
 // K-block) pairs of the call are split evenly over the waves in order.
-template <int F, int D>
-__global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
+template <int F, int D, int W>
+__global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   __shared__ DecodePlan plan;
-  __shared__ v4f red[kWaves][F][64];
+  __shared__ v4f red[W][F][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   {
     const uint32_t* from = reinterpret_cast<const uint32_t*>(a.plan);
     uint32_t* to = reinterpret_cast<uint32_t*>(&plan);
-    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += kThreads) to[i] = from[i];
+    for (int i = tid; i < (int)(sizeof(DecodePlan) / 4); i += W * 64) to[i] = from[i];
   }
   __syncthreads();
   const int ne = __builtin_amdgcn_readfirstlane(plan.experts);
@@ -406,7 +475,7 @@ __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
   const int tile = blockIdx.x;
   const int nt = tile * F / 16, rb = tile * F % 16;  // weight tile of 256 rows, its first fragment
   const int pairs = ne * nb;
-  const int p0 = wave * pairs / kWaves, p1 = (wave + 1) * pairs / kWaves;
+  const int p0 = wave * pairs / W, p1 = (wave + 1) * pairs / W;
 
   struct Stage {
     Frag w[F];
@@ -463,13 +532,13 @@ __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
   for (int f = 0; f < F; ++f) red[wave][f][lane] = acc[f];
   __syncthreads();
   // output pairs of columns: values 2 i, 2 i + 1 of MFMA lane l
-  for (int v = tid; v < F * 128; v += kThreads) {
+  for (int v = tid; v < F * 128; v += W * 64) {
     const int f = v >> 7, l = (v >> 1) & 63, i = (v & 1) * 2;
     const int t = l & 15;
     if (t >= a.tokens) continue;
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       s0 += red[w][f][l][i];
       s1 += red[w][f][l][i + 1];
     }
@@ -478,29 +547,32 @@ __global__ __launch_bounds__(kThreads) void decode_fc2_kernel(DecodeArgs a) {
   }
 }
 
-template <int NK, int D>
+template <int NK>
 void launch_fc1(const DecodeArgs& a, hipStream_t s) {
   // a task at least per workgroup, at most one workgroup per CU
   const int64_t tasks = (int64_t)(a.tokens * a.top_k) * (a.inter / 16);
   const unsigned grid = (unsigned)(tasks < a.grid ? tasks : a.grid);
-  hipLaunchKernelGGL((decode_fc1_kernel<NK, D>), dim3(grid), dim3(kFc1Threads), 0, s, a);
+  hipLaunchKernelGGL((decode_fc1_kernel<NK>), dim3(grid), dim3(kFc1Threads), 0, s, a);
 }
 
 }  // namespace
 
 int launch_decode(const DecodeArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  constexpr int F2 = 1;
   const int per_wave = (a.hidden / 128 + kWaves - 1) / kWaves;  // K-blocks of FC1
   if (per_wave <= 2)
-    launch_fc1<2, 2>(a, s);
+    launch_fc1<2>(a, s);
   else if (per_wave <= 4)
-    launch_fc1<4, 2>(a, s);
+    launch_fc1<4>(a, s);
   else if (per_wave <= 8)
-    launch_fc1<8, 2>(a, s);
+    launch_fc1<8>(a, s);
   else
-    launch_fc1<16, 2>(a, s);
-  hipLaunchKernelGGL((decode_fc2_kernel<F2, 4>), dim3(a.hidden / (16 * F2)), dim3(kThreads), 0, s, a);
+    launch_fc1<16>(a, s);
+  const int tiles = a.hidden / 16;
+  if (tiles <= a.grid)
+    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 16>), dim3(tiles), dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 8>), dim3(tiles), dim3(512), 0, s, a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

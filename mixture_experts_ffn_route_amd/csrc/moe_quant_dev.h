@@ -19,6 +19,13 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // row_mirror: other half
 }
 
+// The same over groups of 8 lanes.
+__device__ __forceinline__ uint32_t row8_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));
+}
+
 // e4m3 codes of 8 values of a block with scale s: those of the quotients
 // v / s.  A quotient is formed from a reciprocal and one correction step; a
 // scale below 2^-90, whose remainders could underflow, divides.  A block
