@@ -277,12 +277,17 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
   }
   __syncthreads();
   // Tasks.  Whole blocks of 128 columns (eight tasks in a row, whose h never
-  // leaves the workgroup) as long as there is one for every workgroup; the
-  // tasks of the blocks that remain are dealt out one by one.
+  // leaves the workgroup) as long as there is one for every workgroup.  The
+  // tasks of the blocks that remain are dealt out one by one, unless they are
+  // blocks for most workgroups: exchanging h through memory then costs more
+  // than the idle ones (208 blocks left for 256 workgroups, T=8 H=7168 I=2048:
+  // 222 us dealt out, 212 whole; 128 left, T=1: 68 and 71).
   const int blocks = __builtin_amdgcn_readfirstlane(plan.experts) * nb;
   const int grid = gridDim.x;
-  const int whole = blocks / grid * 8;  // of this workgroup
-  const int loose = (blocks - blocks / grid * grid) * 8;
+  int rounds = blocks / grid;  // of whole blocks
+  if ((blocks - rounds * grid) * 8 > grid * 5) ++rounds;
+  const int whole = 8 * (rounds - (rounds * grid > blocks && (rounds - 1) * grid + (int)blockIdx.x >= blocks ? 1 : 0));
+  const int loose = max(blocks - rounds * grid, 0) * 8;
   const int turns = whole + (loose > (int)blockIdx.x ? (loose - (int)blockIdx.x + grid - 1) / grid : 0);
   const auto task_at = [&](int turn, int& n, int& blk, int& sub) {
     int b;
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
       sub = turn & 7;
     } else {
       const int i = (turn - whole) * grid + (int)blockIdx.x;
-      b = (whole >> 3) * grid + (i >> 3);
+      b = rounds * grid + (i >> 3);
       sub = i & 7;
     }
     n = b / nb;
@@ -455,8 +460,10 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
 // FC2 and the combine
 // ---------------------------------------------------------------------------
 
-// Workgroup `tile`: 16 F columns of the output, all tokens.  The (expert,
-// K-block) pairs of the call are split evenly over the waves in order.
+// Workgroup `tile`: 16 F columns of the output, all tokens.  Wave w takes
+// every W-th (expert, K-block) pair of the call, so that the waves read
+// neighbouring weight tiles (T=16 H=7168: 230 us for the call against 234 with
+// a contiguous share each).
 template <int F, int D, int W>
 __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   __shared__ DecodePlan plan;
@@ -475,7 +482,7 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   const int tile = blockIdx.x;
   const int nt = tile * F / 16, rb = tile * F % 16;  // weight tile of 256 rows, its first fragment
   const int pairs = ne * nb;
-  const int p0 = wave * pairs / W, p1 = (wave + 1) * pairs / W;
+
 
   struct Stage {
     Frag w[F];
@@ -483,7 +490,7 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
     float sh, sw, rw;
   };
   Stage st[D];
-  int ln = p0 / nb, lk = p0 - ln * nb;  // pair of the next load
+  int ln = wave / nb, lk = wave - ln * nb;  // pair of the next load
   auto load = [&](Stage& s) {
     const int e = __builtin_amdgcn_readfirstlane(plan.expert[ln]);
     const int r = plan.row[ln * kCols + col];
@@ -499,10 +506,7 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
     s.sw = a.w2_scale[((int64_t)e * (a.hidden / 128) + tile * F / 8) * nb + lk];
     s.rw = plan.weight[ln * kCols + col];
     if (r < 0) s.sh = -1.0f;  // a scale is not negative: the column has no such route
-    if (++lk == nb) {
-      lk = 0;
-      ++ln;
-    }
+    for (lk += W; lk >= nb; lk -= nb) ++ln;
   };
   v4f acc[F];
 #pragma unroll
@@ -519,13 +523,13 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (p0 + d < p1) load(st[d]);
-  for (int p = p0; p < p1; p += D) {
+    if (wave + d * W < pairs) load(st[d]);
+  for (int p = wave; p < pairs; p += D * W) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (p + d >= p1) break;
+      if (p + d * W >= pairs) break;
       compute(st[d]);
-      if (p + d + D < p1) load(st[d]);
+      if (p + (d + D) * W < pairs) load(st[d]);
     }
   }
 #pragma unroll
@@ -564,15 +568,23 @@ int launch_decode(const DecodeArgs& a, void* stream) {
     launch_fc1<2>(a, s);
   else if (per_wave <= 4)
     launch_fc1<4>(a, s);
-  else if (per_wave <= 8)
-    launch_fc1<8>(a, s);
+  else if (per_wave <= 7)
+    launch_fc1<7>(a, s);
+  else if (per_wave <= 10)
+    launch_fc1<10>(a, s);
   else
     launch_fc1<16>(a, s);
   const int tiles = a.hidden / 16;
-  if (tiles <= a.grid)
-    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 16>), dim3(tiles), dim3(1024), 0, s, a);
-  else
+  // Two tiles per workgroup where that still is a workgroup for three of four
+  // CUs (the token operand of a K-block then serves twice the weights: H=7168
+  // T=8 202 us against 209); else one, with sixteen waves where the tiles do
+  // not fill the CUs (H=2048 T=5 I=768: 29 us against 37 with eight).
+  if (tiles * 2 > a.grid * 3)
+    hipLaunchKernelGGL((decode_fc2_kernel<2, 2, 8>), dim3(tiles / 2), dim3(512), 0, s, a);
+  else if (tiles > a.grid)
     hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 8>), dim3(tiles), dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 16>), dim3(tiles), dim3(1024), 0, s, a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
