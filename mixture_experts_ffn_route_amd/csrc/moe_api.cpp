@@ -530,8 +530,8 @@ extern "C" moe_status_t moe_layer_decode(moe_layer_t* l, const void* x, const fl
     return moe::fail(MOE_ERR_CAPACITY, "num_tokens %d exceeds max_rows %d or the few-token layer's %d", num_tokens,
                      l->max_rows, moe::kDecodeTokens);
   const moe_config_t& c = l->cfg;
-  if (moe::is_mx(c.weight_format))
-    return moe::fail(MOE_ERR_UNSUPPORTED, "the few-token layer takes E4M3_BLOCK128 weights");
+  if (x_scale && c.act_format != MOE_ACT_E4M3_1X128)
+    return moe::fail(MOE_ERR_INVALID_ARG, "x_scale is only meaningful for E4M3_1X128 activations");
   if ((uintptr_t)status_bits & 3) return moe::fail(MOE_ERR_INVALID_ARG, "status_bits must be 4-byte aligned");
   if (num_tokens > 0) {
     if (!x || !topk_idx || !topk_w || !out_bf16)
@@ -559,10 +559,16 @@ extern "C" moe_status_t moe_layer_decode(moe_layer_t* l, const void* x, const fl
   a.flags = c.flags;
   a.w13 = region<uint8_t>(l, MOE_REGION_W13T);
   a.w2 = region<uint8_t>(l, MOE_REGION_W2T);
-  a.w13_scale = static_cast<const float*>(l->w.w13_scale);
-  a.w2_scale = static_cast<const float*>(l->w.w2_scale);
+  if (moe::is_mx(c.weight_format)) {
+    a.w13_exp = region<uint32_t>(l, MOE_REGION_W13S);
+    a.w2_exp = region<uint32_t>(l, MOE_REGION_W2S);
+  } else {
+    a.w13_scale = static_cast<const float*>(l->w.w13_scale);
+    a.w2_scale = static_cast<const float*>(l->w.w2_scale);
+  }
   const int64_t slots = (int64_t)(l->max_rows < moe::kDecodeTokens ? l->max_rows : moe::kDecodeTokens) * c.top_k;
   a.hf = region<float>(l, moe::kRegionDecode);
+  a.hb = region<uint16_t>(l, moe::kRegionDecode);  // h is one or the other
   a.hq = reinterpret_cast<uint8_t*>(a.hf + slots * c.intermediate);
   a.hs = reinterpret_cast<float*>(a.hq + slots * c.intermediate);
   a.plan = reinterpret_cast<moe::DecodePlan*>(a.hs + slots * (c.intermediate / 128));
@@ -570,7 +576,7 @@ extern "C" moe_status_t moe_layer_decode(moe_layer_t* l, const void* x, const fl
   a.arrive = region<int32_t>(l, moe::kRegionDecodeArrive);
   a.out = static_cast<uint16_t*>(out_bf16);
   a.status = status_bits;
-  if (moe::launch_decode(a, stream) != 0) return hip_fail("decode launch");
+  if (moe::launch_decode(a, c.weight_format, stream) != 0) return hip_fail("decode launch");
   return MOE_OK;
 }
 

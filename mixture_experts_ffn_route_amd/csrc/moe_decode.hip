@@ -33,6 +33,8 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
@@ -64,6 +66,64 @@ __device__ __forceinline__ Frag load_frag_nt(const uint8_t* p) {
 __device__ __forceinline__ v4f mfma_e4m3(const Frag& a, const v8i& b) {
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), b, zero, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+}
+
+// Eight e4m3 codes as bfloat16, exactly.
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The same for MX codes (e4m3, or e5m2 with E5M2) times the power of two whose
+// E8M0 exponent is `e`, held in a float's exponent bits.
+template <bool E5M2>
+__device__ __forceinline__ bf16x8 widen8_mx(uint32_t lo, uint32_t hi, float e) {
+  bf16x2 a, b, c, d;
+  if constexpr (E5M2) {
+    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((int)lo, e, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((int)lo, e, true);
+    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((int)hi, e, false);
+    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((int)hi, e, true);
+  } else {
+    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, e, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, e, true);
+    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, e, false);
+    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, e, true);
+  }
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// One K-block of MX weights (16 rows) and BF16 rows on the BF16 MFMA.  A
+// lane's first 16 weight bytes are columns 16 g.. of the block (g = lane / 16)
+// and its last 16 columns 64 + 16 g..; x[0], x[1] and x[2], x[3] hold the same
+// columns of its token, and e0, e1 are the two halves' exponent words with
+// this row block's byte at `shift`.
+template <bool E5M2>
+__device__ __forceinline__ v4f mfma_mx_bf16(const Frag& w, const u32x4 (&x)[4], uint32_t e0, uint32_t e1, int shift) {
+  const float f0 = __uint_as_float((e0 >> shift & 0xffu) << 23), f1 = __uint_as_float((e1 >> shift & 0xffu) << 23);
+  v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8_mx<E5M2>(w.lo[2 * i], w.lo[2 * i + 1], f0),
+                                                __builtin_bit_cast(bf16x8, x[i]), p, 0, 0, 0);
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8_mx<E5M2>(w.hi[2 * i], w.hi[2 * i + 1], f1),
+                                                __builtin_bit_cast(bf16x8, x[2 + i]), p, 0, 0, 0);
+  }
+  return p;
+}
+// Lane of the exponent words that covers the first half of this lane's
+// columns; the second half's is 32 further.
+__device__ __forceinline__ int mx_word(int lane) { return (lane & 15) + 16 * (lane >> 5); }
+// BF16 columns of K-block `kb` of a row that go with this lane's weight bytes.
+__device__ __forceinline__ void load_bf16_k(u32x4 (&x)[4], const uint16_t* row, int kb, int grp) {
+  const u32x4* q = reinterpret_cast<const u32x4*>(row + kb * 128 + grp * 16);
+  x[0] = q[0];
+  x[1] = q[1];
+  x[2] = q[8];
+  x[3] = q[9];
 }
 
 // acc + p * (sx * sw) for scales of any size: the product's mantissas and
@@ -194,7 +254,12 @@ __device__ __forceinline__ void store_block(const DecodeArgs& a, const float h[8
 // task, which a streaming wave could only do by letting its loads run dry.
 // The two kinds meet in a ring of kRing sums in LDS with counters, not
 // barriers, so no wave waits for the others' memory.
-template <int NK>
+//
+// With MX weights (FMT 1 e4m3, 2 e5m2) the rows stay BF16: a K-block's token
+// operand (twice the size) is loaded with its weights instead of staying in
+// registers, and h is rounded to BF16 column by column, so that its tasks
+// need no exchange at all.
+template <int NK, int FMT>
 __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a) {
   __shared__ Routes routes;
   __shared__ DecodePlan plan;
@@ -222,7 +287,9 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
     const uint32_t bits = check_routes(a, routes, plan, lane);
     if (blockIdx.x == 0 && lane == 0 && a.status) *a.status = bits;
   }
-  if (a.x_scale) {
+  if constexpr (FMT != 0) {
+    // nothing to prepare
+  } else if (a.x_scale) {
     if (wave < kWaves && nk > 0) {
       const int64_t t = min(col, a.tokens - 1);
       const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.hidden + (int64_t)kb0 * 128 + grp * 32;
@@ -284,8 +351,8 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
   // 222 us dealt out, 212 whole; 128 left, T=1: 68 and 71).
   const int blocks = __builtin_amdgcn_readfirstlane(plan.experts) * nb;
   const int grid = gridDim.x;
-  int rounds = blocks / grid;  // of whole blocks
-  if ((blocks - rounds * grid) * 8 > grid * 5) ++rounds;
+  int rounds = FMT == 0 ? blocks / grid : 0;  // of whole blocks
+  if (FMT == 0 && (blocks - rounds * grid) * 8 > grid * 5) ++rounds;
   const int whole = 8 * (rounds - (rounds * grid > blocks && (rounds - 1) * grid + (int)blockIdx.x >= blocks ? 1 : 0));
   const int loose = max(blocks - rounds * grid, 0) * 8;
   const int turns = whole + (loose > (int)blockIdx.x ? (loose - (int)blockIdx.x + grid - 1) / grid : 0);
@@ -333,6 +400,12 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
       float h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[i] = swiglu(g[i], u[i]);
+      if constexpr (FMT != 0) {
+        if (slot >= 0)
+          *reinterpret_cast<q_u32x2*>(a.hb + (int64_t)slot * a.inter + blk * 128 + sub * 16 + grp * 4) =
+              q_u32x2{bf16x2_rne(h[0], h[1]), bf16x2_rne(h[2], h[3])};
+        continue;
+      }
       if (turn < whole) {
         const int par = (turn >> 3) & 1;
         *reinterpret_cast<v4f*>(&hbuf[par][col][sub * 16 + grp * 4]) = v4f{h[0], h[1], h[2], h[3]};
@@ -417,7 +490,61 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
     s.g = load_frag_nt(p);
     s.u = load_frag_nt(p + 8 * kFragBytes);
   };
+  auto put = [&](int turn, const v4f& accg, const v4f& accu) {
+    const int buf = turn % kRing, round = turn / kRing;
+    while (__hip_atomic_load(&emptied[buf], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < round)
+      __builtin_amdgcn_s_sleep(1);
+    red[buf][wave][0][lane] = accg;
+    red[buf][wave][1][lane] = accu;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (lane == 0) __hip_atomic_fetch_add(&filled[buf], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  };
   if (turns == 0) return;
+
+  if constexpr (FMT != 0) {
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)min(col, a.tokens - 1) * a.hidden;
+    struct MxStage {
+      Frag g, u;
+      u32x4 x[4];
+      uint32_t eg[2], eu[2];
+    };
+    MxStage st;
+    int at_turn = 0, at_k = 0;  // next to load
+    int shift_next = 0;
+    auto load_mx = [&]() {
+      int n, blk, sub;
+      task_at(at_turn, n, blk, sub);
+      const int e = __builtin_amdgcn_readfirstlane(plan.expert[n]);
+      const int64_t tile = ((int64_t)e * nb + blk) * kbs + kb0 + at_k;
+      const uint8_t* p = a.w13 + tile * kTileBytes + sub * kFragBytes + lane * 16;
+      st.g = load_frag_nt(p);
+      st.u = load_frag_nt(p + 8 * kFragBytes);
+      const uint32_t* w = a.w13_exp + tile * 256 + (sub >> 2) * 64 + mx_word(lane);
+      st.eg[0] = w[0];
+      st.eg[1] = w[32];
+      st.eu[0] = w[128];
+      st.eu[1] = w[160];
+      load_bf16_k(st.x, x, kb0 + at_k, grp);
+      shift_next = 8 * (sub & 3);
+      if (++at_k == nk) {
+        at_k = 0;
+        ++at_turn;
+      }
+    };
+    if (nk > 0) load_mx();
+    for (int turn = 0; turn < turns; ++turn) {
+      v4f accg = {0.0f, 0.0f, 0.0f, 0.0f}, accu = accg;
+      for (int k = 0; k < nk; ++k) {
+        const MxStage now = st;
+        const int shift = shift_next;
+        if (at_turn < turns) load_mx();
+        accg += mfma_mx_bf16<FMT == 2>(now.g, now.x, now.eg[0], now.eg[1], shift);
+        accu += mfma_mx_bf16<FMT == 2>(now.u, now.x, now.eu[0], now.eu[1], shift);
+      }
+      put(turn, accg, accu);
+    }
+    return;
+  }
   const uint8_t* base = nullptr;
   float wsc = 0.0f;
   if (nk > 0) {
@@ -432,27 +559,36 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
       const float wsc_next = scales_of(turn + 1);
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        if (k >= nk) break;
+        if (k >= nk) continue;
         const float sg = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), k));
         const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsc), 32 + k));
-        const v4f pg = mfma_e4m3(st.g, xb[k]), pu = mfma_e4m3(st.u, xb[k]);
+        const v8i wg = operand(st.g), wu = operand(st.u);
         if (k + 1 < nk)
           load(st, base, k + 1);
         else
           load(st, next, 0);
+        // FC1 multiplies on the BF16 MFMA, whose sums of exact products keep
+        // float32; the FP8 one loses about 2^-11 of the largest product,
+        // which moves codes of h across ties (error of the output against 64
+        // bits 1.9e-3 to 2.6e-3, here 1.7e-3, its bfloat16 rounding).  The
+        // x codes stay narrow: the empty statement keeps the compiler from
+        // widening them once for all tasks, for which registers are lacking.
+        v4f pg = {0.0f, 0.0f, 0.0f, 0.0f}, pu = pg;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int x0 = xb[k][2 * i], x1 = xb[k][2 * i + 1];
+          asm volatile("" : "+v"(x0), "+v"(x1));
+          const bf16x8 x = widen8(x0, x1);
+          pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(wg[2 * i], wg[2 * i + 1]), x, pg, 0, 0, 0);
+          pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(wu[2 * i], wu[2 * i + 1]), x, pu, 0, 0, 0);
+        }
         accg = add_scaled(accg, pg, sx[k], sg);
         accu = add_scaled(accu, pu, sx[k], su);
       }
       base = next;
       wsc = wsc_next;
     }
-    const int buf = turn % kRing, round = turn / kRing;
-    while (__hip_atomic_load(&emptied[buf], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < round)
-      __builtin_amdgcn_s_sleep(1);
-    red[buf][wave][0][lane] = accg;
-    red[buf][wave][1][lane] = accu;
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (lane == 0) __hip_atomic_fetch_add(&filled[buf], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    put(turn, accg, accu);
   }
 }
 
@@ -464,7 +600,7 @@ __global__ __launch_bounds__(kFc1Threads, 1) void decode_fc1_kernel(DecodeArgs a
 // every W-th (expert, K-block) pair of the call, so that the waves read
 // neighbouring weight tiles (T=16 H=7168: 230 us for the call against 234 with
 // a contiguous share each).
-template <int F, int D, int W>
+template <int F, int D, int W, int FMT>
 __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   __shared__ DecodePlan plan;
   __shared__ v4f red[W][F][64];
@@ -486,39 +622,50 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
 
   struct Stage {
     Frag w[F];
-    u32x4 h[2];
-    float sh, sw, rw;
+    u32x4 h[FMT == 0 ? 2 : 4];
+    uint32_t e[2];                    // MX: exponent words
+    float sh, sw, rw;                 // e4m3: scales; the routing weight
+    bool there;                       // whether the column's token has a route to the expert
   };
   Stage st[D];
   int ln = wave / nb, lk = wave - ln * nb;  // pair of the next load
   auto load = [&](Stage& s) {
     const int e = __builtin_amdgcn_readfirstlane(plan.expert[ln]);
     const int r = plan.row[ln * kCols + col];
-    const uint8_t* p =
-        a.w2 + (((int64_t)e * n_tiles + nt) * nb + lk) * (int64_t)kTileBytes + rb * kFragBytes + lane * 16;
+    const int64_t t = ((int64_t)e * n_tiles + nt) * nb + lk;
+    const uint8_t* p = a.w2 + t * kTileBytes + rb * kFragBytes + lane * 16;
 #pragma unroll
     for (int f = 0; f < F; ++f) s.w[f] = load_frag_nt(p + f * kFragBytes);
     const int64_t hr = r >= 0 ? r : 0;  // some row; the column does not count
-    const u32x4* q = reinterpret_cast<const u32x4*>(a.hq + hr * a.inter + lk * 128 + grp * 32);
-    s.h[0] = q[0];
-    s.h[1] = q[1];
-    s.sh = a.hs[hr * nb + lk];
-    s.sw = a.w2_scale[((int64_t)e * (a.hidden / 128) + tile * F / 8) * nb + lk];
+    if constexpr (FMT == 0) {
+      const u32x4* q = reinterpret_cast<const u32x4*>(a.hq + hr * a.inter + lk * 128 + grp * 32);
+      s.h[0] = q[0];
+      s.h[1] = q[1];
+      s.sh = a.hs[hr * nb + lk];
+      s.sw = a.w2_scale[((int64_t)e * (a.hidden / 128) + tile * F / 8) * nb + lk];
+    } else {
+      load_bf16_k(s.h, a.hb + hr * a.inter, lk, grp);
+      const uint32_t* w = a.w2_exp + t * 256 + (rb >> 2) * 64 + mx_word(lane);  // F blocks within one word
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s.e[i] = w[32 * i];
+    }
     s.rw = plan.weight[ln * kCols + col];
-    if (r < 0) s.sh = -1.0f;  // a scale is not negative: the column has no such route
+    s.there = r >= 0;
     for (lk += W; lk >= nb; lk -= nb) ++ln;
   };
   v4f acc[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   auto compute = [&](Stage& s) {
-    const v8i b = operand(Frag{s.h[0], s.h[1]});
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      const v4f y = add_scaled(v4f{0.0f, 0.0f, 0.0f, 0.0f}, mfma_e4m3(s.w[f], b), s.sh, s.sw);
+      v4f y;
+      if constexpr (FMT == 0)
+        y = add_scaled(v4f{0.0f, 0.0f, 0.0f, 0.0f}, mfma_e4m3(s.w[f], operand(Frag{s.h[0], s.h[1]})), s.sh, s.sw);
+      else
+        y = mfma_mx_bf16<FMT == 2>(s.w[f], s.h, s.e[0], s.e[1], 8 * ((rb + f) & 3));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[f][i] = s.sh < 0.0f ? acc[f][i] : fmaf(s.rw, y[i], acc[f][i]);
+      for (int i = 0; i < 4; ++i) acc[f][i] = s.there ? fmaf(s.rw, y[i], acc[f][i]) : acc[f][i];
     }
   };
 #pragma unroll
@@ -551,40 +698,53 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   }
 }
 
-template <int NK>
+template <int NK, int FMT>
 void launch_fc1(const DecodeArgs& a, hipStream_t s) {
   // a task at least per workgroup, at most one workgroup per CU
   const int64_t tasks = (int64_t)(a.tokens * a.top_k) * (a.inter / 16);
   const unsigned grid = (unsigned)(tasks < a.grid ? tasks : a.grid);
-  hipLaunchKernelGGL((decode_fc1_kernel<NK>), dim3(grid), dim3(kFc1Threads), 0, s, a);
+  hipLaunchKernelGGL((decode_fc1_kernel<NK, FMT>), dim3(grid), dim3(kFc1Threads), 0, s, a);
 }
 
-}  // namespace
-
-int launch_decode(const DecodeArgs& a, void* stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const int per_wave = (a.hidden / 128 + kWaves - 1) / kWaves;  // K-blocks of FC1
-  if (per_wave <= 2)
-    launch_fc1<2>(a, s);
-  else if (per_wave <= 4)
-    launch_fc1<4>(a, s);
-  else if (per_wave <= 7)
-    launch_fc1<7>(a, s);
-  else if (per_wave <= 10)
-    launch_fc1<10>(a, s);
-  else
-    launch_fc1<16>(a, s);
+template <int FMT>
+void launch_fc2(const DecodeArgs& a, hipStream_t s) {
   const int tiles = a.hidden / 16;
   // Two tiles per workgroup where that still is a workgroup for three of four
   // CUs (the token operand of a K-block then serves twice the weights: H=7168
   // T=8 202 us against 209); else one, with sixteen waves where the tiles do
   // not fill the CUs (H=2048 T=5 I=768: 29 us against 37 with eight).
   if (tiles * 2 > a.grid * 3)
-    hipLaunchKernelGGL((decode_fc2_kernel<2, 2, 8>), dim3(tiles / 2), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decode_fc2_kernel<2, 2, 8, FMT>), dim3(tiles / 2), dim3(512), 0, s, a);
   else if (tiles > a.grid)
-    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 8>), dim3(tiles), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 8, FMT>), dim3(tiles), dim3(512), 0, s, a);
   else
-    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 16>), dim3(tiles), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((decode_fc2_kernel<1, 2, 16, FMT>), dim3(tiles), dim3(1024), 0, s, a);
+}
+
+}  // namespace
+
+int launch_decode(const DecodeArgs& a, int weight_format, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (weight_format == MOE_WEIGHT_MXFP8_E4M3) {
+    launch_fc1<1, 1>(a, s);
+    launch_fc2<1>(a, s);
+  } else if (weight_format == MOE_WEIGHT_MXFP8_E5M2) {
+    launch_fc1<1, 2>(a, s);
+    launch_fc2<2>(a, s);
+  } else {
+    const int per_wave = (a.hidden / 128 + kWaves - 1) / kWaves;  // K-blocks of FC1
+    if (per_wave <= 2)
+      launch_fc1<2, 0>(a, s);
+    else if (per_wave <= 4)
+      launch_fc1<4, 0>(a, s);
+    else if (per_wave <= 7)
+      launch_fc1<7, 0>(a, s);
+    else if (per_wave <= 10)
+      launch_fc1<10, 0>(a, s);
+    else
+      launch_fc1<16, 0>(a, s);
+    launch_fc2<0>(a, s);
+  }
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -243,6 +243,9 @@ struct DecodeArgs {
   const uint8_t* w2;
   const float* w13_scale;   // [E, 2I/128, H/128]
   const float* w2_scale;    // [E, H/128, I/128]
+  const uint32_t* w13_exp;  // MXFP8: exponent tiles (1 KB per weight tile)
+  const uint32_t* w2_exp;
+  uint16_t* hb;             // MXFP8: [T * K, I] bf16 h
   float* hf;                // [T * K, I] FP32 h
   uint8_t* hq;              // [T * K, I] e4m3 h
   float* hs;                // [T * K, I/128]
@@ -252,7 +255,7 @@ struct DecodeArgs {
   uint16_t* out;            // bf16 [T, H]
   uint32_t* status;         // MOE_DEV_* bits of the call, or null
 };
-int launch_decode(const DecodeArgs& a, void* stream);
+int launch_decode(const DecodeArgs& a, int weight_format, void* stream);
 
 // MXFP8 weight formats (either element type, E8M0 scales per 32).
 inline bool is_mx(int weight_format) {

@@ -190,6 +190,60 @@ def test_stream_and_graph_replays():
         assert torch.equal(out, want)
 
 
+def _setup_mx(T, H, I, E, K, elem, seed=0, masked=0.0):
+    shape = MoEShape(T, H, I, E, K, "topk")
+    inp = make_layer_inputs(shape, seed=seed, masked_fraction=masked,
+                            weight_format="mxfp8" if elem == "e4m3" else "mxfp8_e5m2")
+    dev = to_device(inp)
+    return inp, dev, make_layer(shape, dev, mx=elem)
+
+
+def _oracle_mx(inp, elem):
+    return moe_ref.forward_mx(inp.x_bf16, inp.topk_idx, inp.topk_w, inp.w13, inp.w13_scale, inp.w2, inp.w2_scale,
+                              elem=elem)
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("T,H,I,E,K,masked", [
+    (1, 2048, 768, 32, 6, 0.0), (5, 2048, 768, 32, 6, 0.3), (16, 1152, 384, 16, 8, 0.0), (3, 128, 128, 1, 1, 0.0),
+    (4, 384, 128, 3, 2, 0.0), (9, 896, 256, 5, 4, 0.5), (2, 16384, 128, 4, 2, 0.0), (2, 128, 16384, 4, 2, 0.0),
+    (16, 256, 256, 16, 4, 1.0)])
+def test_mxfp8_weights(T, H, I, E, K, masked, elem):
+    inp, dev, layer = _setup_mx(T, H, I, E, K, elem, seed=T, masked=masked)
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    got = layer.decode(dev.x, dev.topk_idx, dev.topk_w, status=status)
+    res = _oracle_mx(inp, elem)
+    assert_output_close(_bits(got), res.out_bits, f"mx {elem}")
+    assert int(status) == res.status
+    assert_output_close(_bits(got), _bits(run_forward(layer, dev)), "forward")
+
+
+def test_mxfp8_exponents_of_any_size():
+    """Weight exponents 60 and -70 away from the usual against activations of
+    the opposite size: widening is exact, so nothing changes."""
+    inp, dev, layer0 = _setup_mx(5, 512, 256, 8, 2, "e4m3", seed=6)
+    want = layer0.decode(dev.x, dev.topk_idx, dev.topk_w)
+    for p in (-60, 70):
+        d = to_device(inp)
+        x = torch.ldexp(dev.x.float(), torch.tensor(float(p), device="cuda")).bfloat16()
+        d.w13_scale = (dev.w13_scale.int() - p).to(torch.uint8)
+        layer = make_layer(inp.shape, d, mx=True)
+        assert torch.equal(layer.decode(x, dev.topk_idx, dev.topk_w), want)
+
+
+def test_mxfp8_bad_rows_touch_no_other():
+    inp, dev, layer = _setup_mx(6, 512, 256, 4, 2, "e4m3", seed=7)
+    want = layer.decode(dev.x, dev.topk_idx, dev.topk_w)
+    x = dev.x.clone()
+    x[2, 300] = float("nan")
+    got = layer.decode(x, dev.topk_idx, dev.topk_w)
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[2]).all()
+    with pytest.raises(MoEError):   # codes are for the FP8 path
+        layer.decode(torch.zeros(6, 512, dtype=torch.uint8, device="cuda"), dev.topk_idx, dev.topk_w,
+                     x_scale=torch.ones(6, 4, device="cuda"))
+
+
 def test_no_tokens_and_refusals():
     inp, dev, layer = _setup(16, 256, 128, 8, 2, seed=11, max_rows=32)
     status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
