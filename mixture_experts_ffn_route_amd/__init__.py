@@ -11,3 +11,4 @@ from ._lib import MoEError  # noqa: F401
 from .layer import MoELayer  # noqa: F401
 from .norm import NormOutput, rms_norm_quant  # noqa: F401
 from .router import MoERouter  # noqa: F401
+from .block import MoEBlock  # noqa: F401

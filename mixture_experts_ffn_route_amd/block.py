@@ -1,0 +1,54 @@
+"""The MoE block of a decoder layer: residual norm, router and layer.
+
+    block = MoEBlock(norm_weight, router, layer)
+    out, residual = block.forward(attention_out, residual)
+
+``out`` is what the next layer adds to ``residual``.
+"""
+
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib as L
+from .layer import MoELayer
+from .norm import rms_norm_quant
+from .router import MoERouter
+
+# Batches of up to this many tokens take the few-token layer: it is faster than
+# stage + forward up to 8 tokens (H=7168 I=2048 K=8 of 32 experts, all here:
+# T=1 66 us against 83, T=8 200 against 205; H=2048 I=768 K=6: T=1 18 against
+# 34) and slower from 16 on (222 against 220; 44 against 42).
+FEW_TOKENS = 8
+
+
+class MoEBlock:
+    """``router`` has to give local expert ids of ``layer`` (its
+    local_experts are the layer's).  FP8 layers take the norm's e4m3 rows,
+    MXFP8 layers its BF16 rows, which the router reads in both cases."""
+
+    def __init__(self, norm_weight: torch.Tensor, router: MoERouter, layer: MoELayer, *, eps: float = 1e-6):
+        if router.hidden != layer.hidden or router.top_k != layer.top_k:
+            raise ValueError(f"router (hidden {router.hidden}, top_k {router.top_k}) and layer (hidden "
+                             f"{layer.hidden}, top_k {layer.top_k}) do not fit")
+        if router.cfg.local_experts != layer.cfg.num_experts:
+            raise ValueError(f"the router maps to {router.cfg.local_experts} local experts, the layer has "
+                             f"{layer.cfg.num_experts}")
+        self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
+        self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+        """x: bfloat16 [T, H]; residual: [T, H] or None.  Returns the experts'
+        output (bfloat16 [T, H]) and x + residual."""
+        n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8, bf16=True)
+        idx, w = self.router.route(n.y)
+        rows, scale = (n.codes, n.scale) if self.fp8 else (n.y, None)
+        if x.shape[0] <= FEW_TOKENS:
+            out = self.layer.decode(rows, idx, w, x_scale=scale, out=out)
+        else:
+            out = self.layer.stage(rows, idx, w, x_scale=scale, out=out)
+            self.layer.forward()
+        return out, n.residual
