@@ -81,7 +81,7 @@ struct RouterSelectArgs {
   const float* bias;    // [row]: zeros where there is none
   int32_t tokens, hidden, experts, row, splits;
   int32_t top_k, groups, group_size, top_groups;
-  int32_t lanes_per_group, per_lane;  // see router_select_kernel
+  int32_t lane_shift, per_lane;  // log2 of the lanes per group; see router_select_kernel
   int32_t sigmoid, renormalize;
   float scale;
   int32_t expert_base, local_experts;
@@ -341,6 +341,26 @@ __device__ __forceinline__ float sigmoid_fast(float l) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * l));
 }
 
+// Batcher's odd-even merge sort, N a power of two.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1) {
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1) {
+#pragma unroll
+      for (int i = 0; i + k < N; ++i) {
+        // pairs (i, i + k) of this pass
+        if (i >= k % p && ((i - k % p) / k) % 2 == 0 && i / (2 * p) == (i + k) / (2 * p)) {
+          const uint32_t a = v[i], b = v[i + k];
+          v[i] = max(a, b);
+          v[i + k] = min(a, b);
+        }
+      }
+    }
+  }
+}
+
 // Where the experts of a token sit: lane q of its 16 belongs to group
 // q / lanes and holds `per_lane` experts of it from (q % lanes) * per_lane on,
 // at most EPL (one group: 16 lanes).  An expert's slot, q EPL + j, rises with
@@ -359,7 +379,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const bool live = t < a.tokens;
   const int64_t tt = live ? t : a.tokens - 1;
   // this lane's experts
-  const int grp = q / a.lanes_per_group, sub = q - grp * a.lanes_per_group;
+  const int grp = q >> a.lane_shift, sub = q - (grp << a.lane_shift);
   const int e0 = grp * a.group_size + sub * a.per_lane;
   const int count = grp < a.groups ? max(0, min(a.per_lane, a.group_size - sub * a.per_lane)) : 0;
 
@@ -380,40 +400,73 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     }
   };
   load_row(a.bias, bias);
+  const float* row_logits;
   if constexpr (SPLIT) {
     // the K parts of the wave's tokens, summed in order
     const int n4 = (int)min((int64_t)4, a.tokens - tw) * (a.row / 4);
     const f32x4* p = reinterpret_cast<const f32x4*>(a.part + tw * a.row);
     const int64_t step = (int64_t)a.tokens * a.row / 4;
-    for (int i = lane; i < n4; i += 64) {
-      f32x4 part[kMaxSplits];
+    // up to 32 loads of a lane in flight; pieces past the end repeat the last
+    auto sum_parts = [&](auto parts) {
+      constexpr int S = decltype(parts)::value, U = 32 / S;
+      for (int i0 = lane; i0 - lane < n4; i0 += 64 * U) {
+        f32x4 v[U][S];
 #pragma unroll
-      for (int s = 0; s < kMaxSplits; ++s) part[s] = p[min(s, a.splits - 1) * step + i];
-      f32x4 v = part[0];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int s = 1; s < kMaxSplits; ++s)
-        if (s < a.splits) v += part[s];
-      reinterpret_cast<f32x4*>(sums)[i] = v;
-    }
+          for (int s = 0; s < S; ++s) v[u][s] = p[min(s, a.splits - 1) * step + min(i0 + 64 * u, n4 - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          f32x4 t = v[u][0];
+#pragma unroll
+          for (int s = 1; s < S; ++s)
+            if (s < a.splits) t += v[u][s];
+          if (i0 + 64 * u < n4) reinterpret_cast<f32x4*>(sums)[i0 + 64 * u] = t;
+        }
+      }
+    };
+    if (a.splits <= 2)
+      sum_parts(std::integral_constant<int, 2>{});
+    else if (a.splits <= 4)
+      sum_parts(std::integral_constant<int, 4>{});
+    else
+      sum_parts(std::integral_constant<int, kMaxSplits>{});
     __syncthreads();
-    load_row(sums + (tt - tw) * a.row, l);
+    row_logits = sums + (tt - tw) * a.row;
   } else {
-    load_row(a.part + tt * a.row, l);
+    row_logits = a.part + tt * a.row;
   }
+  load_row(row_logits, l);
   float n2 = 0.0f;
   for (int s = q; s < a.splits; s += 16) n2 += a.norm2[(int64_t)s * a.tokens + tt];
   n2 = row_sum(n2);
 
   auto choice = [&](float logit, float bias) { return a.sigmoid ? sigmoid_fast(logit) + bias : logit; };
-  uint32_t key[EPL];
+  uint32_t key[EPL], rest[EPL];
+  auto make_keys = [&]() {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      key[j] = j < count ? ordered(choice(l[j], bias[j])) : 0u;
+      rest[j] = kNoRest;
+    }
+  };
+  make_keys();
   float largest = 0.0f;
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const bool in = j < count;
-    key[j] = in ? ordered(choice(l[j], bias[j])) : 0u;
-    largest = fmaxf(largest, in ? fabsf(l[j]) : 0.0f);
-    top = fmaxf(top, in ? l[j] : -INFINITY);
+    largest = fmaxf(largest, j < count ? fabsf(l[j]) : 0.0f);
+    top = fmaxf(top, j < count ? l[j] : -INFINITY);
+  }
+  // softmax over all experts, where the K scores' sum does not cancel it
+  float all_max = 0.0f, all_sum = 1.0f;
+  if (!a.sigmoid && !a.renormalize) {
+    all_max = unordered(row_max(ordered(top)));
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (j < count) z += expf(l[j] - all_max);
+    all_sum = row_sum(z);
   }
   largest = __uint_as_float(row_max(__float_as_uint(largest)));  // not negative
   const float logit_margin = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
@@ -429,43 +482,48 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   // are exact
   const bool guard = live && margin < INFINITY && n2 > 0.0f;
 
-  // FP64 logit of expert e for the token of row `from`, in every lane.
-  auto dot = [&](int from, int e) -> double {
-    const uint16_t* xr = a.x + (tw + (from >> 4)) * a.x_stride;
-    const uint16_t* wr = a.w + (int64_t)e * a.hidden;
+  // FP64 logits of two (token row, expert) pairs at a time, in every lane, so
+  // that a pair of neighbours costs one trip to memory.
+  auto dot2 = [&](int from0, int expert0, int from1, int expert1, double& out0, double& out1) {
+    const uint16_t* rows[4] = {a.x + (tw + (from0 >> 4)) * a.x_stride, a.w + (int64_t)expert0 * a.hidden,
+                               a.x + (tw + (from1 >> 4)) * a.x_stride, a.w + (int64_t)expert1 * a.hidden};
     constexpr int kBatch = 7;  // loads in flight per row
-    double d0 = 0.0, d1 = 0.0;
+    double d[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
     for (int base = lane * 8; base - lane * 8 < a.hidden; base += kBatch * 512) {
-      u32x4 xv[kBatch], wv[kBatch];
+      u32x4 v[4][kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = base + k * 512 < a.hidden ? base + k * 512 : 0;
-        xv[k] = *reinterpret_cast<const u32x4*>(xr + i);
-        wv[k] = *reinterpret_cast<const u32x4*>(wr + i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r][k] = *reinterpret_cast<const u32x4*>(rows[r] + i);
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (base + k * 512 >= a.hidden) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d0 = fma((double)bf16_to_f32(xv[k][i] & 0xffffu), (double)bf16_to_f32(wv[k][i] & 0xffffu), d0);
-          d1 = fma((double)bf16_to_f32(xv[k][i] >> 16), (double)bf16_to_f32(wv[k][i] >> 16), d1);
-        }
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t xv = v[2 * o][k][i], wv = v[2 * o + 1][k][i];
+            // a product of two bfloat16 has 16 bits: exact in float32
+            d[o][0] += (double)(bf16_to_f32(xv & 0xffffu) * bf16_to_f32(wv & 0xffffu));
+            d[o][1] += (double)(__uint_as_float(xv & 0xffff0000u) * __uint_as_float(wv & 0xffff0000u));
+          }
       }
     }
-    double d = d0 + d1;
+    out0 = d[0][0] + d[0][1];
+    out1 = d[1][0] + d[1][1];
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m, 64);
-    return d;
+    for (int m = 1; m < 64; m <<= 1) {
+      out0 += __shfl_xor(out0, m, 64);
+      out1 += __shfl_xor(out1, m, 64);
+    }
   };
   auto choice64 = [&](double logit, int e) -> double {
     return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (double)a.bias[e] : logit;
   };
 
   // Choices of marked slots (bits of the lanes' `need`) in FP64.
-  uint32_t rest[EPL];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) rest[j] = kNoRest;
   auto recompute = [&](uint64_t need) {
     for (uint64_t lanes = __ballot(need != 0); lanes; lanes = __ballot(need != 0)) {
       const int from = __builtin_ctzll(lanes);
@@ -473,7 +531,9 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
                             (uint32_t)__builtin_amdgcn_readlane((int)need, from);
       const int j0 = __builtin_ctzll(bits);
       const int e = __builtin_amdgcn_readlane(e0, from) + j0;
-      const double d = dot(from, e), c = choice64(d, e);
+      double d, same;
+      dot2(from, e, from, e, d, same);
+      const double c = choice64(d, e);
       const uint32_t hi = ordered((float)c), lo = ordered((float)(c - (double)(float)c));
       if (lane == from) {
         need &= need - 1;
@@ -488,6 +548,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     }
   };
 
+  bool in = true;  // whether this lane's group stays
   if (a.groups > 1) {
     const bool two = a.sigmoid && a.group_size > 1;
     // the group's two largest choices, in all its lanes
@@ -501,23 +562,23 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       k2 = max(min(k1, o1), max(k2, o2));
       k1 = max(k1, o1);
     };
-    if (a.lanes_per_group > 1) merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
-    if (a.lanes_per_group > 2) merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
-    if (a.lanes_per_group > 4) merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
+    if (a.lane_shift > 0) merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
+    if (a.lane_shift > 1) merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
+    if (a.lane_shift > 2) merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
     const float v = two ? unordered(k1) + unordered(k2) : unordered(k1);
     const bool valid = grp < a.groups;
     // lanes of groups ahead of this one, by rotating the row
     const uint32_t vk = valid ? ordered(v) : 0u;
     int ahead = 0;
-#define MOE_ROT(N)                                                                      \
-  {                                                                                     \
-    const uint32_t o = dpp<0x120 + N>(vk);                                              \
-    ahead += (o > vk || (o == vk && ((q - N) & 15) / a.lanes_per_group < grp)) ? 1 : 0; \
+#define MOE_ROT(N)                                                                  \
+  {                                                                                 \
+    const uint32_t o = dpp<0x120 + N>(vk);                                          \
+    ahead += (o > vk || (o == vk && ((q - N) & 15) >> a.lane_shift < grp)) ? 1 : 0; \
   }
     MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
     MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
-    bool in = valid && ahead < a.top_groups * a.lanes_per_group;
+    in = valid && ahead < a.top_groups << a.lane_shift;
     // smallest value that stays, largest that does not
     const float lo = unordered(row_min(in ? vk : 0xffffffffu));
     const float hi = unordered(row_max(valid && !in ? vk : 0u));
@@ -540,7 +601,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
         put(key[j] > 1u ? (double)unordered(key[j]) + (double)unordered_rest(rest[j]) : -INFINITY);
-      for (int m = 1; m < a.lanes_per_group; m <<= 1) {
+      for (int m = 1; m < 1 << a.lane_shift; m <<= 1) {
         const double o1 = __shfl_xor(c1, m, 64), o2 = __shfl_xor(c2, m, 64);
         put(o1);
         put(o2);
@@ -548,14 +609,10 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       const double gv = two ? c1 + c2 : c1;
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
-        const double o = __shfl(gv, row0 + g * a.lanes_per_group, 64);
+        const double o = __shfl(gv, row0 + (g << a.lane_shift), 64);
         rank += (o > gv || (o == gv && g < grp)) ? 1 : 0;
       }
       in = valid && rank < a.top_groups;
-    }
-    if (!in) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = 0u;
     }
   }
 
@@ -565,38 +622,40 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   uint32_t pk[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j)
-    pk[j] = key[j] ? (max(key[j], kSlots) & ~kSlotMask) | (kSlotMask - (uint32_t)(q * EPL + j)) : 0u;
-  uint32_t mk = 0;     // lane k: the k-th packed key
-  float ml = 0.0f;     //   its logit
+    pk[j] = in && key[j] ? (max(key[j], kSlots) & ~kSlotMask) | (kSlotMask - (uint32_t)(q * EPL + j)) : 0u;
+  // With up to 16 slots each lane sorts its own first, so that a maximum looks
+  // at one key per lane (T=4096: the selection's instructions halve).
+  if constexpr (EPL <= 16) sort_descending<EPL>(pk);
+  uint32_t mk = 0;  // lane k: the k-th packed key
   auto take = [&](int k) -> uint32_t {
-    uint32_t m = 0;
+    uint32_t m = pk[0];
+    if constexpr (EPL > 16) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) m = max(m, pk[j]);
+      for (int j = 1; j < EPL; ++j) m = max(m, pk[j]);
+    }
     m = row_max(m);
-    float sl = 0.0f;
+    if constexpr (EPL > 16) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const bool hit = pk[j] == m;
-      sl = hit ? l[j] : sl;
-      pk[j] = hit ? 0u : pk[j];
+      for (int j = 0; j < EPL; ++j) pk[j] = pk[j] == m ? 0u : pk[j];
+    } else {
+      const bool hit = pk[0] == m;
+#pragma unroll
+      for (int j = 0; j + 1 < EPL; ++j) pk[j] = hit ? pk[j + 1] : pk[j];
+      pk[EPL - 1] = hit ? 0u : pk[EPL - 1];
     }
-    const int owner = row0 + (int)((kSlotMask - (m & kSlotMask)) / EPL);
-    const float ol = __shfl(sl, owner, 64);
-    if (q == k) {
-      mk = m;
-      ml = ol;
-    }
+    if (q == k) mk = m;
     return m;
   };
   for (int k = 0; k <= a.top_k; ++k) (void)take(k);
   auto expert_of = [&](uint32_t m) -> int {
     const int slot = (int)(kSlotMask - (m & kSlotMask));
-    const int qs = slot / EPL, gs = qs / a.lanes_per_group;
-    return gs * a.group_size + (qs - gs * a.lanes_per_group) * a.per_lane + slot % EPL;
+    const int qs = slot / EPL, gs = qs >> a.lane_shift;
+    return gs * a.group_size + (qs - (gs << a.lane_shift)) * a.per_lane + slot % EPL;
   };
   // largest choice that a packed key can stand for
   auto upper = [&](uint32_t m) { return m >= 2 * kSlots ? unordered(m | kSlotMask) : -INFINITY; };
   int id = mk ? expert_of(mk) : 0;
+  float ml = row_logits[id];  // of the lane's entry
   float c = mk ? choice(ml, a.bias[id]) : -INFINITY;
   float mine = ml;
   // Too close: neighbours among the K within the largest of their margins,
@@ -617,6 +676,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     }
     if (!more) {
       id = mk ? expert_of(mk) : 0;
+      ml = row_logits[id];
       c = mk ? choice(ml, a.bias[id]) : -INFINITY;
       mine = ml;
       // those within the margins of another, in FP64
@@ -631,12 +691,17 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
       double exact = c;
-      for (uint64_t todo = __ballot(redo && mineclose && mk != 0); todo; todo &= todo - 1) {
-        const int from = __builtin_ctzll(todo);
-        const int e = __builtin_amdgcn_readlane(id, from);
-        const double d = dot(from, e), f = choice64(d, e);
-        if (lane == from) {
-          exact = f;
+      uint64_t todo = __ballot(redo && mineclose && mk != 0);
+      while (todo) {
+        const int f0 = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const int f1 = todo ? __builtin_ctzll(todo) : f0;
+        todo &= todo - 1;  // 0 stays 0
+        double d0, d1;
+        dot2(f0, __builtin_amdgcn_readlane(id, f0), f1, __builtin_amdgcn_readlane(id, f1), d0, d1);
+        if (lane == f0 || lane == f1) {
+          const double d = lane == f0 ? d0 : d1;
+          exact = choice64(d, id);
           mine = (float)d;
         }
       }
@@ -660,7 +725,15 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       }
     } else {
       // Too many for the list: every choice within the margin of its
-      // neighbour, among all experts.
+      // neighbour, among all experts.  The keys are made again, which keeps
+      // their registers free until here.
+      load_row(row_logits, l);
+      load_row(a.bias, bias);
+      make_keys();
+      if (!in) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = 0u;
+      }
       auto extract = [&](auto exact) -> uint64_t {
         constexpr bool kExact = decltype(exact)::value;
         uint64_t taken = 0, need = 0;
@@ -724,13 +797,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     const float m = unordered(row_max(slot ? ordered(mine) : 0u));
     w = slot ? expf(mine - m) : 0.0f;
   } else {
-    const float m = unordered(row_max(ordered(top)));
-    float z = 0.0f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (j < count) z += expf(l[j] - m);
-    z = row_sum(z);
-    w = slot ? expf(mine - m) / z : 0.0f;
+    w = slot ? expf(mine - all_max) / all_sum : 0.0f;
   }
   if (a.renormalize) {
     const float sum = row_sum(w);
@@ -1033,7 +1100,7 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   const moe::Lanes n = moe::lanes_for(c);
   a.groups = n.groups;
   a.group_size = c.num_experts / n.groups;
-  a.lanes_per_group = n.lanes;
+  a.lane_shift = n.lanes == 16 ? 4 : n.lanes == 8 ? 3 : n.lanes == 4 ? 2 : n.lanes == 2 ? 1 : 0;
   a.per_lane = n.per_lane;
   a.top_groups = c.top_groups;
   a.sigmoid = c.score == MOE_SCORE_SIGMOID;
