@@ -525,25 +525,36 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 
   // Choices of marked slots (bits of the lanes' `need`) in FP64.
   auto recompute = [&](uint64_t need) {
-    for (uint64_t lanes = __ballot(need != 0); lanes; lanes = __ballot(need != 0)) {
-      const int from = __builtin_ctzll(lanes);
-      const uint64_t bits = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(need >> 32), from) << 32) |
-                            (uint32_t)__builtin_amdgcn_readlane((int)need, from);
-      const int j0 = __builtin_ctzll(bits);
-      const int e = __builtin_amdgcn_readlane(e0, from) + j0;
-      double d, same;
-      dot2(from, e, from, e, d, same);
-      const double c = choice64(d, e);
-      const uint32_t hi = ordered((float)c), lo = ordered((float)(c - (double)(float)c));
-      if (lane == from) {
-        need &= need - 1;
+    int from[2], j0[2], e[2];
+    // the next marked slot, which loses its mark
+    auto next = [&](int k) -> bool {
+      const uint64_t lanes = __ballot(need != 0);
+      if (!lanes) return false;
+      from[k] = __builtin_ctzll(lanes);
+      const uint64_t bits = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(need >> 32), from[k]) << 32) |
+                            (uint32_t)__builtin_amdgcn_readlane((int)need, from[k]);
+      j0[k] = __builtin_ctzll(bits);
+      e[k] = __builtin_amdgcn_readlane(e0, from[k]) + j0[k];
+      if (lane == from[k]) need &= need - 1;
+      return true;
+    };
+    while (next(0)) {
+      if (!next(1)) from[1] = from[0], j0[1] = j0[0], e[1] = e[0];
+      double d[2];
+      dot2(from[0], e[0], from[1], e[1], d[0], d[1]);
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-          if (j == j0) {
-            l[j] = (float)d;
-            key[j] = hi;
-            rest[j] = lo;
-          }
+      for (int k = 0; k < 2; ++k) {
+        const double c = choice64(d[k], e[k]);
+        const uint32_t hi = ordered((float)c), lo = ordered((float)(c - (double)(float)c));
+        if (lane == from[k]) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j)
+            if (j == j0[k]) {
+              l[j] = (float)d[k];
+              key[j] = hi;
+              rest[j] = lo;
+            }
+        }
       }
     }
   };
