@@ -5,23 +5,31 @@
 //                       h = silu(g) u, h -> e4m3 1x128
 //   decode_fc2_kernel   y = h W2^T, out[t] = bf16(sum_k w[t, k] y_k)
 //
-// The weights of the chosen experts are the whole traffic, so everything is
-// arranged around streaming them once:
-//  * The MFMA takes 16 weight rows x 16 tokens x 128, and 16 columns hold
-//    every token: no staging, no compaction and no token tiles.  A lane's
-//    weight operand is 32 bytes of the create-time tiles, loaded straight into
-//    registers, 1 KB per instruction.
+// The weights of the chosen experts are nearly the whole traffic (T=1 H=7168
+// I=2048 K=8: 352 MB, 52 us at the 6.8 TB/s that a plain read reaches; T=16:
+// 1.40 GB, 206 us), so everything is arranged around streaming them once:
+//  * The MFMA takes 16 weight rows x 16 tokens, and 16 columns hold every
+//    token: no staging, no compaction and no token tiles.  A lane's weight
+//    operand of a K-block is 32 bytes of the create-time tiles, loaded straight
+//    into registers, 1 KB per instruction.
 //  * A workgroup takes few output columns of one expert (FC1) or of all of
-//    them (FC2), and its eight waves split the K-blocks, so that a single
-//    token's few experts still make several hundred workgroups.  The waves'
-//    sums meet in LDS at the end.
-//  * A token's operand for a K-block is 32 of its columns per lane, which the
-//    lane loads and (for BF16 input) quantises itself; the block maximum takes
-//    two lane swaps.
-//  * h is quantised per 128 columns, which several workgroups make: each
-//    stores its FP32 columns and the last to arrive quantises the block.
+//    them (FC2), and its waves split the K-blocks, so that a single token's
+//    few experts still make several hundred workgroups.  The waves' sums meet
+//    in LDS.
+//  * BF16 rows for FP8 weights are quantised by every FC1 workgroup for itself
+//    (T=16 H=7168: 229 KB of rows, from L2, each block by eight lanes; 235 us
+//    for the call against 226 with e4m3 rows given).
+//  * h is quantised per 128 columns.  A workgroup makes whole blocks where the
+//    chosen experts have enough of them; the tasks of the others go to several
+//    workgroups, which store FP32 columns, and the last to arrive quantises
+//    the block.
 //  * FC2 adds the experts' rows in FP32 with the routing weights applied to
 //    the partial sums, so there are no y rows and no combine.
+// The whole call, FP8 weights and e4m3 rows, H=7168 I=2048 K=8 of 32 experts:
+// T=1 66 us, 2 111, 4 165, 8 208, 16 226 (5.3 to 6.2 TB/s; FC1 takes two
+// thirds); MXFP8 66, 102, 162, 218, 269.  H=2048 I=768 K=6: T=1 18 us, 5 33,
+// 16 44, where the two launches' starts and ends, about 10 us, are what is
+// left beside the stream.
 #include <hip/hip_runtime.h>
 
 #include "moe_device.h"
@@ -618,7 +626,6 @@ __global__ __launch_bounds__(W * 64) void decode_fc2_kernel(DecodeArgs a) {
   const int tile = blockIdx.x;
   const int nt = tile * F / 16, rb = tile * F % 16;  // weight tile of 256 rows, its first fragment
   const int pairs = ne * nb;
-
 
   struct Stage {
     Frag w[F];

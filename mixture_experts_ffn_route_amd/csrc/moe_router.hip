@@ -12,6 +12,13 @@
 // Ties go to the lowest group and the lowest expert; a NaN ranks below
 // every number.
 //
+// Its floor is the token rows read once and the product on the MFMA: T=4096
+// H=7168 E=256 9 and 11 us, T=32768 68 and 89.  A call takes 10 us (T=1), 24
+// (512), 42 (4096), 163 (32768), of which the product 4, 8, 22 and 127 and the
+// 64-bit decisions about 10 from T=512 on: a token whose groups or experts lie
+// close needs two or three trips to memory, one after the other, and the launch
+// waits for the slowest.
+//
 // Two launches:
 //  * router_gemm_kernel: FP32 logits on the BF16 MFMA, split over K where a
 //    batch has few token tiles.  Experts are the MFMA rows and tokens its
@@ -879,13 +886,24 @@ struct Plan {
 
 // Few tokens take narrow expert tiles, so that the K split, whose parts the
 // selection reads back, stays at most kMaxSplits; many take wide tiles, which
-// read the token rows once.
+// read the token rows once.  Where the steps lie hardly matters below a
+// thousand tokens and much above (H=7168 E=256, us for the whole call with the
+// next smaller, this and the next larger tile):
+//   tokens: T=512 - / 23.7 / 24.4, 4096 46.3 / 42.4 / 44.0, 16384 121.7 / 98.3 / -
+//   experts: T=32 - / 14.1 / 13.1, 256 23.7 / 22.4 / 23.0, 4096 46.0 / 42.4 / -,
+//            8192 73.9 / 65.9 / 70.3, 16384 103.1 / 98.3 / -
+// Where one block holds all experts the rows are everything that is read, and
+// more, smaller workgroups bring them faster (H=2048 E=32: T=1024 11.5 us with
+// 32 tokens against 12.8 with 64, T=8192 17.6 against 23.3 with 128, T=32768
+// 48.6 with 64 against 52.3; H=7168 E=16 T=32768 64 tokens 99, 32 109, 128
+// 102).
 Plan plan_for(const moe_router_config_t& c, int64_t tokens) {
   Plan p;
   p.bt = tokens <= 512 ? 32 : (tokens <= 4096 ? 64 : 128);
   const int blocks = (c.num_experts + 31) / 32;
   p.be = tokens <= 32 ? 1 : (tokens <= 256 ? 2 : (tokens <= 8192 ? 4 : 8));
   while (p.be / 2 >= blocks) p.be /= 2;
+  if (blocks == 1) p.bt = tokens <= 8192 ? 32 : 64;
   const int64_t tiles = (tokens + p.bt - 1) / p.bt * ((blocks + p.be - 1) / p.be);
   const int chunks = c.hidden / kKC;
   int64_t want = kTargetGroups / tiles;
@@ -984,12 +1002,16 @@ void launch_gemm(const RouterGemmArgs& g, int be, dim3 grid, hipStream_t s) {
       return;
     }
   }
+  if constexpr (BT < 128) {  // and one block with fewer only
+    if (be == 1) {
+      hipLaunchKernelGGL((router_gemm_kernel<BT, 1, 1>), grid, block, 0, s, g);
+      return;
+    }
+  }
   if (be == 4)
     hipLaunchKernelGGL((router_gemm_kernel<BT, 4, 1>), grid, block, 0, s, g);
-  else if (be == 2)
-    hipLaunchKernelGGL((router_gemm_kernel<BT, 2, 1>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((router_gemm_kernel<BT, 1, 1>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((router_gemm_kernel<BT, 2, 1>), grid, block, 0, s, g);
 }
 
 template <int EPL>

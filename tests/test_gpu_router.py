@@ -91,6 +91,15 @@ def test_batch_sizes(T, H, E):
     check(r, x, reference(x, w, 8, "sigmoid", b, 4, 2), experts=E)
 
 
+@pytest.mark.parametrize("T", [512, 513, 4097, 8192, 8193, 9001])
+@pytest.mark.parametrize("E,K", [(8, 2), (32, 6), (60, 8), (300, 8)])
+def test_expert_tiles_and_batches(T, E, K):
+    """One block of experts, two, and more than one workgroup holds."""
+    x, w, _ = _inputs(T, 512, E, T + E)
+    r = MoERouter(w, K, max_rows=T)
+    check(r, x, reference(x, w, K, "softmax"), experts=E)
+
+
 @pytest.mark.parametrize("T,H", [(3, 7168), (300, 7168), (2500, 7168), (5, 16384), (1100, 16384)])
 def test_long_rows(T, H):
     x, w, b = _inputs(T, H, 256, T + H, bias=True)
