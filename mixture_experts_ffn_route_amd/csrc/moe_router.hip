@@ -15,9 +15,10 @@
 // Its floor is the token rows read once and the product on the MFMA: T=4096
 // H=7168 E=256 9 and 11 us, T=32768 68 and 89.  A call takes 10 us (T=1), 24
 // (512), 42 (4096), 163 (32768), of which the product 4, 8, 22 and 127 and the
-// 64-bit decisions about 10 from T=512 on: a token whose groups or experts lie
-// close needs two or three trips to memory, one after the other, and the launch
-// waits for the slowest.
+// 64-bit decisions about 10 from T=512 on: two FP64 logits take a wave 4 us (2
+// x 7168 products, converted and added one by one), a token whose groups or
+// experts lie close needs two to six of them, and the launch waits for the
+// slowest.
 //
 // Two launches:
 //  * router_gemm_kernel: FP32 logits on the BF16 MFMA, split over K where a
@@ -500,16 +501,19 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   auto dot2 = [&](int from0, int expert0, int from1, int expert1, double& out0, double& out1) {
     const uint16_t* rows[4] = {a.x + (tw + (from0 >> 4)) * a.x_stride, a.w + (int64_t)expert0 * a.hidden,
                                a.x + (tw + (from1 >> 4)) * a.x_stride, a.w + (int64_t)expert1 * a.hidden};
-    constexpr int kBatch = 7;  // loads in flight per row
+    // Two batches of loads, one on its way while the other is added up.
+    constexpr int kBatch = 2;  // pieces of a row per batch: the additions, not the loads, take the time
     double d[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
-    for (int base = lane * 8; base - lane * 8 < a.hidden; base += kBatch * 512) {
-      u32x4 v[4][kBatch];
+    u32x4 v[2][4][kBatch];
+    auto fetch = [&](u32x4 (&to)[4][kBatch], int base) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = base + k * 512 < a.hidden ? base + k * 512 : 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r][k] = *reinterpret_cast<const u32x4*>(rows[r] + i);
+        for (int r = 0; r < 4; ++r) to[r][k] = *reinterpret_cast<const u32x4*>(rows[r] + i);
       }
+    };
+    auto add = [&](const u32x4 (&from)[4][kBatch], int base) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (base + k * 512 >= a.hidden) continue;
@@ -517,12 +521,20 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
         for (int o = 0; o < 2; ++o)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t xv = v[2 * o][k][i], wv = v[2 * o + 1][k][i];
+            const uint32_t xv = from[2 * o][k][i], wv = from[2 * o + 1][k][i];
             // a product of two bfloat16 has 16 bits: exact in float32
             d[o][0] += (double)(bf16_to_f32(xv & 0xffffu) * bf16_to_f32(wv & 0xffffu));
             d[o][1] += (double)(__uint_as_float(xv & 0xffff0000u) * __uint_as_float(wv & 0xffff0000u));
           }
       }
+    };
+    constexpr int kStep = kBatch * 512;
+    fetch(v[0], lane * 8);
+    for (int base = lane * 8; base - lane * 8 < a.hidden; base += 2 * kStep) {
+      fetch(v[1], base + kStep);
+      add(v[0], base);
+      fetch(v[0], base + 2 * kStep);
+      add(v[1], base + kStep);
     }
     out0 = d[0][0] + d[0][1];
     out1 = d[1][0] + d[1][1];
