@@ -17,11 +17,15 @@ from .layer import MoELayer
 from .norm import rms_norm_quant
 from .router import MoERouter
 
-# Batches of up to this many tokens take the few-token layer: it is faster than
-# stage + forward up to 8 tokens (H=7168 I=2048 K=8 of 32 experts, all here:
-# T=1 66 us against 83, T=8 200 against 205; H=2048 I=768 K=6: T=1 18 against
-# 34) and slower from 16 on (222 against 220; 44 against 42).
+# Batches of up to this many tokens take the few-token layer, which is faster
+# than stage + forward up to there (us, 32 experts, all here).  FP8 rows,
+# H=7168 I=2048 K=8: T=1 66 against 84, T=8 201 against 203, T=10 216 against
+# 217, T=12 222 against 221; H=2048 I=768 K=6: T=1 18 against 33, T=8 37
+# against 40, T=10 41 against 40.  MXFP8 weights: T=5 183 against 185, T=6 196
+# against 193, T=8 215 against 205; at the smaller sizes T=5 31 against 36, T=8
+# 39 against 40.
 FEW_TOKENS = 8
+FEW_TOKENS_MX = 5
 
 
 class MoEBlock:
@@ -38,6 +42,7 @@ class MoEBlock:
                              f"{layer.cfg.num_experts}")
         self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
+        self.few = FEW_TOKENS if self.fp8 else FEW_TOKENS_MX
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
@@ -46,7 +51,7 @@ class MoEBlock:
         n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8, bf16=True)
         idx, w = self.router.route(n.y)
         rows, scale = (n.codes, n.scale) if self.fp8 else (n.y, None)
-        if x.shape[0] <= FEW_TOKENS:
+        if x.shape[0] <= self.few:
             out = self.layer.decode(rows, idx, w, x_scale=scale, out=out)
         else:
             out = self.layer.stage(rows, idx, w, x_scale=scale, out=out)

@@ -69,7 +69,7 @@ def _experts(inp, mx, n, ids, w, base):
 
 
 @pytest.mark.parametrize("mx", [False, "e4m3"])
-@pytest.mark.parametrize("T", [1, 8, 9, 40])   # the few-token layer, and stage + forward
+@pytest.mark.parametrize("T", [1, 5, 6, 8, 9, 40])  # the few-token layer, and stage + forward
 def test_block_matches_its_steps(T, mx):
     inp, gate, bias, weight, block, x, r = _make(T, mx, seed=T)
     out, res = block.forward(x, r)
