@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from ._args import check, current_raw_stream, ptr
+from ._args import check, current_raw_stream, empty_rows, ptr
 
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -96,7 +96,7 @@ class MoELayer:
         check(topk_idx, "topk_idx", routes, _I32, dev)
         check(topk_w, "topk_w", routes, _F32, dev)
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            out = empty_rows(T, self.hidden, torch.bfloat16, dev)
         else:
             check(out, "out", shape, _BF16, dev)
         if status is not None:

@@ -12,7 +12,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib as L
-from ._args import check, current_raw_stream, ptr
+from ._args import check, current_raw_stream, empty_rows, ptr
 
 _TYPES = {torch.bfloat16: L.MOE_TYPE_BF16, torch.float32: L.MOE_TYPE_F32}
 _BF16, _F32, _CODES = (torch.bfloat16,), (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
@@ -51,12 +51,12 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if out is None:
         q = s = y = ro = None
         if codes:
-            q = torch.empty(shape, dtype=torch.uint8, device=dev)
-            s = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+            q = empty_rows(T, H, torch.uint8, dev)
+            s = empty_rows(T, H // 128, torch.float32, dev)
         if bf16:
-            y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            y = empty_rows(T, H, torch.bfloat16, dev)
         if residual is not None:
-            ro = torch.empty(shape, dtype=residual.dtype, device=dev)
+            ro = empty_rows(T, H, residual.dtype, dev)
         out = NormOutput(q, s, y, ro)
     else:
         q, s, y, ro = out

@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from ._args import check, current_raw_stream, ptr
+from ._args import check, current_raw_stream, empty_rows, ptr
 
 _SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
@@ -68,11 +68,11 @@ class MoERouter:
         check(x, "x", (T, self.hidden), _BF16, dev, True)
         shape = (T, self.top_k)
         if topk_idx is None:
-            topk_idx = torch.empty(shape, dtype=torch.int32, device=dev)
+            topk_idx = empty_rows(T, self.top_k, torch.int32, dev)
         else:
             check(topk_idx, "topk_idx", shape, _I32, dev)
         if topk_w is None:
-            topk_w = torch.empty(shape, dtype=torch.float32, device=dev)
+            topk_w = empty_rows(T, self.top_k, torch.float32, dev)
         else:
             check(topk_w, "topk_w", shape, _F32, dev)
         if ids is not None:
