@@ -362,7 +362,8 @@ typedef struct {
  *   scale = max|y| / 448 per 128 columns, code = e4m3 RNE_sat(y / scale).
  * codes and scales are what moe_stage_inputs and moe_layer_decode take as
  * prequantised rows.  Every output is rounded once, from FP32 values: the
- * codes are those of y, not of the BF16 row.
+ * codes are those of y, not of the BF16 row; with an FP32 residual those from
+ * 2^-6 up are the codes of 64-bit arithmetic.
  *  x              device bfloat16 [T, H], rows x_stride elements apart.
  *  residual       device [T, H] of residual_type, rows residual_stride
  *                 elements apart; NULL: s = x.

@@ -26,14 +26,10 @@ __device__ __forceinline__ uint32_t row8_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));
 }
 
-// e4m3 codes of 8 values of a block with scale s: those of the quotients
-// v / s.  A quotient is formed from a reciprocal and one correction step; a
-// scale below 2^-90, whose remainders could underflow, divides.  A block
-// that holds a NaN or an infinity has such a scale and NaN codes.
-__device__ __forceinline__ q_u32x2 quant8(const float v[8], float s) {
-  if (s == 0.0f) return q_u32x2{0u, 0u};
-  if (!isfinite(s)) return q_u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
-  float q[8];
+// Quotients v / s of 8 values of a block with scale s, finite and not zero:
+// from a reciprocal and one correction step; a scale below 2^-90, whose
+// remainders could underflow, divides.
+__device__ __forceinline__ void quotients8(const float v[8], float s, float q[8]) {
   if (s >= 0x1p-90f) {
     const float inv = 1.0f / s;
 #pragma unroll
@@ -45,6 +41,10 @@ __device__ __forceinline__ q_u32x2 quant8(const float v[8], float s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
   }
+}
+
+// Their e4m3 codes.
+__device__ __forceinline__ q_u32x2 codes8(const float q[8]) {
   q_u32x2 w;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -52,6 +52,21 @@ __device__ __forceinline__ q_u32x2 quant8(const float v[8], float s) {
     w[j] = (uint32_t)cvt2_e4m3(q[4 * j + 2], q[4 * j + 3], lo, true);
   }
   return w;
+}
+
+// Codes of a block whose scale is zero (all values are), or not finite (it
+// holds a NaN or an infinity): zero, NaN.
+__device__ __forceinline__ q_u32x2 codes_without_scale(float s) {
+  const uint32_t w = s == 0.0f ? 0u : 0x7f7f7f7fu;
+  return q_u32x2{w, w};
+}
+
+// Codes of 8 values of a block with scale s.
+__device__ __forceinline__ q_u32x2 quant8(const float v[8], float s) {
+  if (s == 0.0f || !isfinite(s)) return codes_without_scale(s);
+  float q[8];
+  quotients8(v, s, q);
+  return codes8(q);
 }
 
 }  // namespace moe

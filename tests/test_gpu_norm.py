@@ -69,6 +69,29 @@ def _inputs(T, H, rtype, wtype, seed, scale=1.0):
     return x, r, w
 
 
+@pytest.mark.parametrize("wtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [2048, 7168])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_codes_are_those_of_64_bits(H, wtype, in_place):
+    """FP32 residual: a few of a million quotients lie closer to the middle of
+    two codes than FP32 can tell.  The factor 1/sqrt(mean + eps) cancels in
+    y / scale, so the formula's own rounding is a few 2^-53.  Codes below
+    2^-6 may go by FP32's quotient."""
+    T = 2 ** 21 // H
+    x, r, w = _inputs(T, H, torch.float32, wtype, 17)
+    b = _formula(x, r, w, 1e-6)[0] * w.double().cpu().numpy()
+    q = b.reshape(T, H // 128, 128) * 448.0
+    q = q / (np.abs(q).max(axis=2, keepdims=True) / 448.0)
+    want = formats.e4m3_encode_rne_sat(q)
+    out = None
+    if in_place:  # the new residual over the old one, the BF16 rows over x
+        out = NormOutput(torch.empty(T, H, dtype=torch.uint8, device="cuda"), torch.empty(T, H // 128, device="cuda"),
+                         x, r)
+    got = rms_norm_quant(x, w, r, out=out)
+    codes = got.codes.cpu().numpy().view(np.uint8).reshape(want.shape)
+    assert np.array_equal(codes[np.abs(q) >= 2.0 ** -6], want[np.abs(q) >= 2.0 ** -6])
+
+
 @pytest.mark.parametrize("rtype", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("wtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H", [(1, 128), (3, 256), (1, 7168), (37, 7168), (5, 8192), (4, 8320), (2, 16384),
