@@ -429,7 +429,9 @@ moe_status_t moe_router_workspace_query(const moe_router_config_t* cfg, int32_t 
  *             kernels' order, and read in place where choices lie close: the
  *             caller keeps it alive and unchanged while the handle exists.
  *  bias       device float32 [E] or NULL, added to sigmoid scores for the
- *             selection only; copied into the workspace.
+ *             selection only; copied into the workspace.  Of any size: an
+ *             expert's bias, infinite or NaN too, concerns that expert alone
+ *             (-inf switches it off while top_k others are left).
  *  workspace  device, 256-byte aligned, ws_bytes >= the query's.
  * The launches of one handle must not overlap on the device (its workspace
  * holds the logits of the call in progress). */

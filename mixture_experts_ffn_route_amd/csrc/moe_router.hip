@@ -34,6 +34,7 @@
 // The ids are those of 64-bit arithmetic: where two choices that matter lie
 // closer than twice the margin
 //   B = kLogitMargin * (|x| max_e|w_e| / sqrt(H) + max_e|l_e|)
+// (and, of a sigmoid, what evaluating it and adding its own bias may cost)
 // the wave computes these experts' logits again in FP64 (two or three of
 // them as a rule) and selects among FP64 choices.  |x| |w| / sqrt(H) is the
 // size of a logit whose terms have random signs, and the FP32 error grows with
@@ -82,7 +83,7 @@ struct RouterGemmArgs {
 struct RouterSelectArgs {
   const float* part;
   const float* norm2;
-  const float* limits;  // [0] max |w_e|, [1] max |bias|
+  const float* limits;  // [0] max |w_e|
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* w;  // [E, H] as the caller holds it
@@ -484,17 +485,21 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   }
   largest = __uint_as_float(row_max(__float_as_uint(largest)));  // not negative
   const float logit_margin = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
-  // Margin of a choice: a sigmoid's slope is s (1 - s), 1/4 at most, and
-  // evaluating it and adding the bias costs less than 2^-20 of their size.
-  const float eval = a.sigmoid ? 0x1p-20f * (1.0f + a.limits[1]) : 0.0f;
-  const float margin = a.sigmoid ? fmaf(0.25f, logit_margin, eval) : logit_margin;
-  auto margin_of = [&](float logit) {
+  // Margin of a choice c.  A sigmoid's slope is s (1 - s), 1/4 at most;
+  // evaluating it costs less than 2^-20, adding its bias a rounding of c.  It
+  // grows with |c| so slowly that c - margin and c + margin rise with c: what
+  // holds for a largest choice holds for those below it, however large their
+  // biases are.  Choices that are not finite are exact as they are.
+  const float ev = a.sigmoid ? 0x1p-22f : 0.0f, eval = a.sigmoid ? 0x1p-20f : 0.0f;
+  const float base = a.sigmoid ? fmaf(0.25f, logit_margin, eval) : logit_margin;
+  auto margin_of = [&](float c) { return fmaf(ev, fabsf(c), base); };
+  auto slope_margin = [&](float logit) {
     const float s = sigmoid_fast(logit);
     return a.sigmoid ? fmaf(1.01f * s * (1.0f - s), logit_margin, eval) : logit_margin;
   };
   // not for rows with a NaN or an overflow, nor for zero rows, whose logits
   // are exact
-  const bool guard = live && margin < INFINITY && n2 > 0.0f;
+  const bool guard = live && logit_margin < INFINITY && n2 > 0.0f;
 
   // FP64 logits of two (token row, expert) pairs at a time, in every lane, so
   // that a pair of neighbours costs one trip to memory.
@@ -601,7 +606,8 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     if (a.lane_shift > 0) merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
     if (a.lane_shift > 1) merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
     if (a.lane_shift > 2) merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
-    const float v = two ? unordered(k1) + unordered(k2) : unordered(k1);
+    const float b1 = unordered(k1), b2 = two ? unordered(k2) : 0.0f;
+    const float v = (two ? k2 : k1) > 1u ? b1 + b2 : NAN;
     const bool valid = grp < a.groups;
     // lanes of groups ahead of this one, by rotating the row
     const uint32_t vk = valid ? ordered(v) : 0u;
@@ -615,19 +621,20 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
     in = valid && ahead < a.top_groups << a.lane_shift;
-    // smallest value that stays, largest that does not
-    const float lo = unordered(row_min(in ? vk : 0xffffffffu));
-    const float hi = unordered(row_max(valid && !in ? vk : 0u));
-    const float g4 = 4.0f * margin;
-    const bool close = guard && lo - hi <= g4;
+    // least that the values that stay can be, most that the others can be
+    const float gm = fmaf(ev, fabsf(b1) + fabsf(b2), two ? 2.0f * base : base);
+    const bool number = fabsf(v) < INFINITY;
+    const float lo = unordered(row_min(in ? ordered(number ? v - gm : v) : 0xffffffffu));
+    const float hi = unordered(row_max(valid && !in ? ordered(number ? v + gm : v) : 0u));
+    const bool close = guard && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && lo <= hi;
     if (__ballot(close)) {
       // FP64 for the members that can make the values of groups at the border
-      const bool at = close && valid && (fabsf(v - lo) <= g4 || fabsf(v - hi) <= g4);
-      const float from = unordered(two ? k2 : k1) - 2.0f * margin;
+      const bool at = close && valid && number && (in ? v - gm <= hi : v + gm >= lo);
+      const float least = two ? b2 : b1, from = least - margin_of(least);
       uint64_t need = 0;
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
-        if (at && key[j] > 1u && unordered(key[j]) >= from) need |= 1ull << j;
+        if (at && key[j] > 1u && unordered(key[j]) + margin_of(unordered(key[j])) >= from) need |= 1ull << j;
       recompute(need);
       double c1 = -INFINITY, c2 = -INFINITY;
       auto put = [&](double c) {
@@ -642,11 +649,15 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
         put(o1);
         put(o2);
       }
-      const double gv = two ? c1 + c2 : c1;
+      double gv = two ? c1 + c2 : c1;
+      gv = vk > 1u && gv == gv ? gv : -INFINITY;
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
         const double o = __shfl(gv, row0 + (g << a.lane_shift), 64);
-        rank += (o > gv || (o == gv && g < grp)) ? 1 : 0;
+        const uint32_t ok = (uint32_t)__shfl((int)vk, row0 + (g << a.lane_shift), 64);
+        // -inf is not recomputed, and before NaN
+        const bool tie_first = gv == -INFINITY && ok != vk ? ok > vk : g < grp;
+        rank += (o > gv || (o == gv && tie_first)) ? 1 : 0;
       }
       in = valid && rank < a.top_groups;
     }
@@ -697,18 +708,22 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   // Too close: neighbours among the K within the largest of their margins,
   // or the last of them and what follows within its margin and any.
   const uint32_t after = dpp<kNext>(mk);
-  const float among = unordered(row_max(q < a.top_k ? ordered(margin_of(ml)) : 0u));
-  const bool tight = guard && q < a.top_k && c - upper(after) <= among + (q + 1 < a.top_k ? among : margin);
+  const float among = unordered(row_max(q < a.top_k ? ordered(slope_margin(ml)) : 0u));
+  const float next = upper(after);
+  const bool number = fabsf(c) < INFINITY;
+  const bool tight = guard && q < a.top_k && number && fabsf(next) < INFINITY &&
+                     c - next <= fmaf(ev, fabsf(c) + fabsf(next), among + (q + 1 < a.top_k ? among : base));
   if (__ballot(tight)) {
     // Some token of the wave has neighbours too close to call.  Its list goes
     // on while choices may belong to the K after all.
     const bool mineclose = ((__ballot(tight) >> row0) & 0xffffu) != 0;
-    const float border = unordered(row_min(q < a.top_k ? ordered(c) : 0xffffffffu)) - (among + margin);
+    const float border =
+        unordered(row_min(q < a.top_k && number ? ordered(c - fmaf(ev, fabsf(c), among)) : 0xffffffffu));
     int n = a.top_k + 1;
     bool more = true;
     for (; n < 16 && more; ++n) {
       const uint32_t m = take(n);
-      more = __ballot(mineclose && upper(m) >= border) != 0;
+      more = __ballot(mineclose && upper(m) + margin_of(upper(m)) >= border) != 0;
     }
     if (!more) {
       id = mk ? expert_of(mk) : 0;
@@ -717,7 +732,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       mine = ml;
       // those within the margins of another, in FP64
       bool redo = false;
-      const float mm = margin_of(ml);
+      const float mm = fabsf(c) < INFINITY ? fmaf(ev, fabsf(c), slope_margin(ml)) : 0.0f;
 #define MOE_ROT(N)                                                     \
   {                                                                    \
     const float o = dppf<0x120 + N>(c);                                \
@@ -726,7 +741,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
       MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
-      double exact = c;
+      double exact = c == c ? c : -INFINITY;
       uint64_t todo = __ballot(redo && mineclose && mk != 0);
       while (todo) {
         const int f0 = __builtin_ctzll(todo);
@@ -741,14 +756,15 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
           mine = (float)d;
         }
       }
-      // their order, ties to the lowest expert; lane k takes the k-th
+      // their order, ties to the lowest expert (-inf and NaN are in order as
+      // they stand); lane k takes the k-th
       if (!mk) exact = -INFINITY;
       int rank = 0;
       for (int i = 0; i < 16; ++i) {
         const double o = __shfl(exact, row0 + i, 64);
         const int oe = __shfl(id, row0 + i, 64);
         const bool there = __shfl((int)(mk != 0), row0 + i, 64) != 0;
-        rank += there && (!mk || o > exact || (o == exact && oe < id)) ? 1 : 0;
+        rank += there && (!mk || o > exact || (o == exact && (o == -INFINITY ? i < q : oe < id))) ? 1 : 0;
       }
       int at = row0;
       for (int i = 0; i < 16; ++i)
@@ -798,13 +814,14 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
           const bool own = s / EPL == (uint32_t)q;
           if constexpr (!kExact) {
             const float ck = unordered(m);
-            const bool number = m > 1u;
-            if (number && guard && before - ck <= 2.0f * margin) {
+            const bool number = fabsf(ck) < INFINITY;
+            if (number && guard && before < INFINITY && before - ck <= margin_of(before) + margin_of(ck)) {
               if (own) need |= 1ull << (s % EPL);
               if (ps / EPL == (uint32_t)q) need |= 1ull << (ps % EPL);
             }
             if (k == a.top_k - 1) last = ck;
-            if (!__ballot(k < a.top_k || (number && guard && ck >= last - 2.0f * margin))) break;
+            const bool reach = last > -INFINITY && ck + margin_of(ck) >= last - margin_of(last);
+            if (!__ballot(k < a.top_k || (number && guard && reach))) break;
             before = number ? ck : INFINITY;
             ps = s;
           } else {
@@ -867,8 +884,7 @@ __global__ __launch_bounds__(256) void router_tile_kernel(const uint16_t* w, u32
   dst[c] = v;
 }
 
-// limits[0] = max_e |w_e|, limits[1] = max_e |bias_e|, and the padded copy of
-// the biases; one wave per expert slot of a logit row.  A maximum does not
+// limits[0] = max_e |w_e|, and the padded copy of the biases; one wave per expert slot of a logit row.  A maximum does not
 // depend on the order of the atomics; as bits, a NaN is larger than every
 // number.
 __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, const float* bias, int experts,
@@ -884,10 +900,7 @@ __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, co
   }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-  if (threadIdx.x == 0) {
-    atomicMax(&limits[0], __float_as_uint(sqrtf(s)) & 0x7fffffffu);
-    atomicMax(&limits[1], __float_as_uint(b) & 0x7fffffffu);
-  }
+  if (threadIdx.x == 0) atomicMax(&limits[0], __float_as_uint(sqrtf(s)) & 0x7fffffffu);
 }
 
 // Token tile and K split of a batch.

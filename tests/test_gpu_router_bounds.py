@@ -1,0 +1,93 @@
+"""Where the router's ids are hardest to get right: selection biases of any
+size, rows and gates whose logits lie close for a reason, sums that cancel.
+
+Every choice is that of 64-bit arithmetic (``ids_64``): a NaN ranks below every
+number, ties go to the lowest group and expert.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_router import U, _inputs
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from mixture_experts_ffn_route_amd import MoERouter
+
+
+def _descending(v):
+    """Positions of ``v``'s rows in descending order; a NaN after -inf, ties by position."""
+    return np.lexsort((-np.where(np.isnan(v), -np.inf, v), np.isnan(v)), axis=-1)
+
+
+def ids_64(logits, score, K, bias=None, groups=1, top_groups=1):
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    with np.errstate(all="ignore"):
+        choice = logits if score == "softmax" else 1.0 / (1.0 + np.exp(-logits))
+        if bias is not None:
+            choice = choice + bias.double().cpu().numpy()
+        gone = np.zeros((T, E), dtype=bool)
+        if top_groups < groups:
+            n = E // groups
+            by = choice.reshape(T, groups, n)
+            top = np.take_along_axis(by, _descending(by), axis=2)
+            value = top[:, :, 0] if score == "softmax" or n == 1 else top[:, :, 0] + top[:, :, 1]
+            out = _descending(value)[:, top_groups:]
+            for g in range(out.shape[1]):
+                for j in range(n):
+                    gone[np.arange(T), out[:, g] * n + j] = True
+        # experts of other groups after everything else
+        order = np.lexsort((-np.where(np.isnan(choice), -np.inf, choice), np.isnan(choice), gone), axis=-1)
+    return order[:, :K]
+
+
+def _logits(x, w):
+    with np.errstate(all="ignore"):
+        return x.double().cpu().numpy() @ w.double().cpu().numpy().T
+
+
+def _ids(x, w, K, **kw):
+    r = MoERouter(w, K, max_rows=x.shape[0], **kw)
+    ids = torch.empty(x.shape[0], K, dtype=torch.int32, device="cuda")
+    r.route(x, ids=ids)
+    return ids.cpu().numpy()
+
+
+def _close_gates(H, E, seed):
+    """Gates that differ in the last places of a few elements: the logits of a
+    row lie within about 1e-5 of each other."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn(1, H, generator=g, device="cuda") * H ** -0.5).bfloat16().expand(E, H).clone()
+    w[:, :8] = (3e-6 * torch.randn(E, 8, generator=g, device="cuda")).bfloat16()
+    return w
+
+
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("off", [-1e4, -1e9, -3e38, 1e9, float("-inf"), float("inf"), float("nan")])
+def test_one_bias_of_any_size(off, groups, top_groups):
+    T, H, E, K = 700, 512, 256, 8
+    w = _close_gates(H, E, 3)
+    x, _, _ = _inputs(T, H, 1, 3)
+    bias = 1e-6 * torch.randn(E, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
+    bias[37] = off
+    got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
+    assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups))
+
+
+@pytest.mark.parametrize("E,groups,top_groups", [(64, 1, 1), (256, 8, 4), (256, 8, 7), (1024, 16, 5)])
+@pytest.mark.parametrize("off", [-1e9, float("-inf"), float("nan")])
+def test_most_experts_switched_off(E, groups, top_groups, off):
+    """Whole groups of them, groups with one expert left, and fewer experts
+    left than the token takes."""
+    T, H, K = 90, 512, 8
+    x, w, b = _inputs(T, H, E, 5, bias=True)
+    g = torch.Generator().manual_seed(E)
+    for left in (3, K, E // 4):
+        bias = b.clone()
+        bias[torch.randperm(E, generator=g)[left:].cuda()] = off
+        got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
+        want = ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups)
+        assert np.array_equal(got, want), left
