@@ -346,10 +346,18 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return k < 2u ? -INFINITY : __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// The rest of a choice as an ordered integer; it is a small number or 0.
+// A choice known in FP64 is a float and a rest: the difference in units of
+// 2^-53 of the float's binade (FP64's own steps there, or halves of them), as
+// an ordered integer.  It is below 2^30.
 constexpr uint32_t kNoRest = 0x80000000u;
-__device__ __forceinline__ float unordered_rest(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+__device__ __forceinline__ int rest_exponent(float hi) { return max(ilogbf(hi), -126) - 53; }
+__device__ __forceinline__ uint32_t rest_of(double c) {
+  const float hi = (float)c;
+  return kNoRest + (uint32_t)(int)ldexp(c - (double)hi, -rest_exponent(hi));
+}
+__device__ __forceinline__ double with_rest(uint32_t key, uint32_t rest) {
+  const float hi = unordered(key);
+  return rest == kNoRest ? (double)hi : (double)hi + ldexp((double)(int)(rest - kNoRest), rest_exponent(hi));
 }
 
 __device__ __forceinline__ float sigmoid_fast(float l) {
@@ -381,8 +389,8 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
 // at most EPL (one group: 16 lanes).  An expert's slot, q EPL + j, rises with
 // its number.
 //
-// A choice known in FP64 is kept as a pair of floats, its value rounded and
-// the rest: key (ordered) then rest.  The rest is 0 for choices known in FP32.
+// A choice known in FP64 is kept as its value rounded to float32 and the rest:
+// key (ordered) then rest.  The rest is 0 for choices known in FP32.
 template <int EPL, bool SPLIT>
 __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   constexpr uint32_t kSlots = 16 * EPL;    // a power of two
@@ -575,7 +583,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const double c = choice64(d[k], e[k]);
-        const uint32_t hi = ordered((float)c), lo = ordered((float)(c - (double)(float)c));
+        const uint32_t hi = ordered((float)c), lo = rest_of(c);
         if (lane == from[k]) {
 #pragma unroll
           for (int j = 0; j < EPL; ++j)
@@ -643,7 +651,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       };
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
-        put(key[j] > 1u ? (double)unordered(key[j]) + (double)unordered_rest(rest[j]) : -INFINITY);
+        put(key[j] > 1u ? with_rest(key[j], rest[j]) : -INFINITY);
       for (int m = 1; m < 1 << a.lane_shift; m <<= 1) {
         const double o1 = __shfl_xor(c1, m, 64), o2 = __shfl_xor(c2, m, 64);
         put(o1);

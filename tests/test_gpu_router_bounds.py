@@ -91,3 +91,15 @@ def test_most_experts_switched_off(E, groups, top_groups, off):
         got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
         want = ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups)
         assert np.array_equal(got, want), left
+
+
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("common", [-3e4, 1e6, 1e9])
+def test_large_common_biases(common, groups, top_groups):
+    """All biases large: FP32 tells none of the choices apart, FP64 most."""
+    T, H, E, K = 60, 512, 256, 8
+    x, _, _ = _inputs(T, H, 1, 2)
+    w = _close_gates(H, E, 2)
+    bias = torch.full((E,), common, device="cuda")
+    got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
+    assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups))
