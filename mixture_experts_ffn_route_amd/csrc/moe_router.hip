@@ -92,6 +92,7 @@ struct RouterSelectArgs {
   int32_t top_k, groups, group_size, top_groups;
   int32_t lane_shift, per_lane;  // log2 of the lanes per group; see router_select_kernel
   int32_t sigmoid, renormalize;
+  int32_t biased;
   float scale;
   int32_t expert_base, local_experts;
   int32_t* idx;
@@ -492,7 +493,14 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     all_sum = row_sum(z);
   }
   largest = __uint_as_float(row_max(__float_as_uint(largest)));  // not negative
-  const float logit_margin = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
+  // Rows whose logits FP64 can tell apart where FP32 cannot.  Rows of zeros
+  // and rows whose squared norm leaves float32's range go by their FP32 logits
+  // as they are: what lies close there is evaluated again in FP64 from these.
+  // Without a bias the choices of a row of zeros are all equal, and in order.
+  const float bound = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
+  const bool guard = live && bound < INFINITY && n2 >= 0x1p-100f;
+  const bool decide = live && (guard || a.biased || largest > 0.0f);
+  const float logit_margin = guard ? bound : 0.0f;
   // Margin of a choice c.  A sigmoid's slope is s (1 - s), 1/4 at most;
   // evaluating it costs less than 2^-20, adding its bias a rounding of c.  It
   // grows with |c| so slowly that c - margin and c + margin rise with c: what
@@ -505,10 +513,6 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     const float s = sigmoid_fast(logit);
     return a.sigmoid ? fmaf(1.01f * s * (1.0f - s), logit_margin, eval) : logit_margin;
   };
-  // not for rows with a NaN or an overflow, nor for zero rows, whose logits
-  // are exact
-  const bool guard = live && logit_margin < INFINITY && n2 > 0.0f;
-
   // FP64 logits of two (token row, expert) pairs at a time, in every lane, so
   // that a pair of neighbours costs one trip to memory.
   auto dot2 = [&](int from0, int expert0, int from1, int expert1, double& out0, double& out1) {
@@ -597,6 +601,23 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     }
   };
 
+  // The same from the FP32 logits, for the marked slots of rows that go by these.
+  auto from_logits = [&](uint64_t marked) {
+#pragma unroll 1
+    for (int j0 = 0; j0 < EPL; ++j0) {
+      const bool now = (marked >> j0) & 1u;
+      if (!__ballot(now)) continue;
+      const int e = now ? e0 + j0 : 0;
+      const double c = choice64(row_logits[e], e);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (now && j == j0) {
+          key[j] = ordered((float)c);
+          rest[j] = rest_of(c);
+        }
+    }
+  };
+
   bool in = true;  // whether this lane's group stays
   if (a.groups > 1) {
     const bool two = a.sigmoid && a.group_size > 1;
@@ -634,7 +655,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     const bool number = fabsf(v) < INFINITY;
     const float lo = unordered(row_min(in ? ordered(number ? v - gm : v) : 0xffffffffu));
     const float hi = unordered(row_max(valid && !in ? ordered(number ? v + gm : v) : 0u));
-    const bool close = guard && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && lo <= hi;
+    const bool close = decide && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && lo <= hi;
     if (__ballot(close)) {
       // FP64 for the members that can make the values of groups at the border
       const bool at = close && valid && number && (in ? v - gm <= hi : v + gm >= lo);
@@ -643,7 +664,8 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
         if (at && key[j] > 1u && unordered(key[j]) + margin_of(unordered(key[j])) >= from) need |= 1ull << j;
-      recompute(need);
+      recompute(guard ? need : 0);
+      from_logits(guard ? 0 : need);
       double c1 = -INFINITY, c2 = -INFINITY;
       auto put = [&](double c) {
         c2 = fmax(c2, fmin(c1, c));
@@ -719,7 +741,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const float among = unordered(row_max(q < a.top_k ? ordered(slope_margin(ml)) : 0u));
   const float next = upper(after);
   const bool number = fabsf(c) < INFINITY;
-  const bool tight = guard && q < a.top_k && number && fabsf(next) < INFINITY &&
+  const bool tight = decide && q < a.top_k && number && fabsf(next) < INFINITY &&
                      c - next <= fmaf(ev, fabsf(c) + fabsf(next), among + (q + 1 < a.top_k ? among : base));
   if (__ballot(tight)) {
     // Some token of the wave has neighbours too close to call.  Its list goes
@@ -750,7 +772,8 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
       MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
       double exact = c == c ? c : -INFINITY;
-      uint64_t todo = __ballot(redo && mineclose && mk != 0);
+      if (redo && !guard && mk != 0) exact = choice64(ml, id);
+      uint64_t todo = __ballot(redo && guard && mineclose && mk != 0);
       while (todo) {
         const int f0 = __builtin_ctzll(todo);
         todo &= todo - 1;
@@ -845,6 +868,11 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
         return need;
       };
       recompute(extract(std::false_type{}));
+      uint64_t all = 0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (mineclose && !guard && fabsf(unordered(key[j])) < INFINITY) all |= 1ull << j;
+      from_logits(all);
       extract(std::true_type{});
     }
   }
@@ -1065,6 +1093,7 @@ struct moe_router {
   uint8_t* ws;
   moe::RouterLayout L;
   int32_t max_rows;
+  bool biased;
 };
 
 namespace {
@@ -1108,6 +1137,7 @@ extern "C" moe_status_t moe_router_create(const moe_router_config_t* cfg, int32_
   r->ws = static_cast<uint8_t*>(workspace);
   r->L = L;
   r->max_rows = max_rows;
+  r->biased = bias != nullptr;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t pieces = (int64_t)((cfg->num_experts + 31) / 32) * (cfg->hidden / 16) * 64;
   uint32_t* limits = reinterpret_cast<uint32_t*>(r->ws + L.limits);
@@ -1185,6 +1215,7 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.top_groups = c.top_groups;
   a.sigmoid = c.score == MOE_SCORE_SIGMOID;
   a.renormalize = c.renormalize;
+  a.biased = r->biased;
   a.scale = c.scale;
   a.expert_base = c.expert_base;
   a.local_experts = c.local_experts;

@@ -103,3 +103,33 @@ def test_large_common_biases(common, groups, top_groups):
     bias = torch.full((E,), common, device="cuda")
     got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
     assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups))
+
+
+@pytest.mark.parametrize("E", [40, 256, 640])
+@pytest.mark.parametrize("step", [1e-6, 1e-9, 1e-12])
+def test_zero_rows_go_by_their_biases(E, step):
+    """Padding rows: every score is 1/2, and the biases lie `step` apart."""
+    T, H, K = 12, 256, 8
+    x, w, _ = _inputs(T, H, E, 6)
+    x[3:] = 0
+    bias = (step * torch.randperm(E, generator=torch.Generator().manual_seed(E))).float().cuda()
+    bias[5] = bias[9]
+    for groups, top_groups in ((1, 1), (8, 3)):
+        got = _ids(x, w, K, score="sigmoid", bias=bias, num_groups=groups, top_groups=top_groups)
+        assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, bias, groups, top_groups))
+
+
+@pytest.mark.parametrize("power", [100, -100])
+def test_rows_beyond_float32_squares(power):
+    """Such rows go by their FP32 logits, here exact: 1 + k 2^-20 times 2^power."""
+    T, H, E, K = 9, 256, 256, 8
+    k = torch.randperm(E, generator=torch.Generator().manual_seed(1))
+    w = torch.zeros(E, H, device="cuda", dtype=torch.bfloat16)
+    w[:, 0] = 1
+    w[:, 100] = k.cuda().bfloat16()
+    x = torch.zeros(T, H, device="cuda", dtype=torch.bfloat16)
+    x[:, 0] = 2.0 ** power
+    x[:, 100] = 2.0 ** (power - 20)
+    for groups, top_groups in ((1, 1), (8, 3)):
+        got = _ids(x, w, K, num_groups=groups, top_groups=top_groups)
+        assert np.array_equal(got, ids_64(_logits(x, w), "softmax", K, None, groups, top_groups))
