@@ -418,7 +418,8 @@ typedef struct moe_router moe_router_t;
  * The chosen experts are those of 64-bit arithmetic on the given x, W and
  * bias, whatever the batch they come in: choices that lie within the FP32
  * product's rounding errors of each other are computed again in FP64.  (Rows
- * whose squared norm leaves float32's range go by their FP32 logits.)
+ * whose squared norm leaves float32's range go by their FP32 logits; so do all
+ * rows beside a gate row of finite weights whose squared norm does.)
  *
  * moe_router_workspace_query: device bytes for batches of up to max_rows
  * tokens.  Host only. */

@@ -479,7 +479,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    largest = fmaxf(largest, j < count ? fabsf(l[j]) : 0.0f);
+    largest = fmaxf(largest, j < count && fabsf(l[j]) < INFINITY ? fabsf(l[j]) : 0.0f);
     top = fmaxf(top, j < count ? l[j] : -INFINITY);
   }
   // softmax over all experts, where the K scores' sum does not cancel it
@@ -920,7 +920,8 @@ __global__ __launch_bounds__(256) void router_tile_kernel(const uint16_t* w, u32
   dst[c] = v;
 }
 
-// limits[0] = max_e |w_e|, and the padded copy of the biases; one wave per expert slot of a logit row.  A maximum does not
+// limits[0] = max |w_e| of the experts without an infinite or NaN weight (whose
+// logits are neither numbers nor close to any), and the padded copy of the biases; one wave per expert slot of a logit row.  A maximum does not
 // depend on the order of the atomics; as bits, a NaN is larger than every
 // number.
 __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, const float* bias, int experts,
@@ -930,10 +931,13 @@ __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, co
   if (threadIdx.x == 0) bias_copy[e] = b;
   if (e >= experts) return;
   float s = 0.0f;
+  bool bad = false;
   for (int i = threadIdx.x; i < hidden; i += 64) {
     const float v = bf16_to_f32(w[(int64_t)e * hidden + i]);
     s = fmaf(v, v, s);
+    bad |= !(fabsf(v) < INFINITY);
   }
+  if (__ballot(bad)) return;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
   if (threadIdx.x == 0) atomicMax(&limits[0], __float_as_uint(sqrtf(s)) & 0x7fffffffu);

@@ -133,3 +133,15 @@ def test_rows_beyond_float32_squares(power):
     for groups, top_groups in ((1, 1), (8, 3)):
         got = _ids(x, w, K, num_groups=groups, top_groups=top_groups)
         assert np.array_equal(got, ids_64(_logits(x, w), "softmax", K, None, groups, top_groups))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_bad_gate_row_leaves_the_others_in_order(bad, score):
+    T, H, E, K = 300, 512, 256, 8
+    x, _, _ = _inputs(T, H, 1, 9)
+    w = _close_gates(H, E, 9)
+    w[77, 300] = bad
+    for groups, top_groups in ((1, 1), (8, 4)):
+        got = _ids(x, w, K, score=score, num_groups=groups, top_groups=top_groups)
+        assert np.array_equal(got, ids_64(_logits(x, w), score, K, None, groups, top_groups))
