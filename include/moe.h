@@ -417,7 +417,8 @@ typedef struct moe_router moe_router_t;
  *
  * The chosen experts are those of 64-bit arithmetic on the given x, W and
  * bias, whatever the batch they come in: choices that lie within the FP32
- * product's rounding errors of each other are computed again in FP64.  (Rows
+ * product's rounding errors of each other, bounded by the partial sums that
+ * each row really had, are computed again in FP64.  (Rows
  * whose squared norm leaves float32's range go by their FP32 logits; so do all
  * rows beside a gate row of finite weights whose squared norm does.)
  *

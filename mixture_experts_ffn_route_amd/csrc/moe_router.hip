@@ -32,13 +32,25 @@
 //    DPP row operation for four tokens at once.
 //
 // The ids are those of 64-bit arithmetic: where two choices that matter lie
-// closer than twice the margin
-//   B = kLogitMargin * (|x| max_e|w_e| / sqrt(H) + max_e|l_e|)
-// (and, of a sigmoid, what evaluating it and adding its own bias may cost)
-// the wave computes these experts' logits again in FP64 (two or three of
-// them as a rule) and selects among FP64 choices.  |x| |w| / sqrt(H) is the
-// size of a logit whose terms have random signs, and the FP32 error grows with
-// it and with the logits themselves.
+// closer than the bounds on their FP32 errors (and, of a sigmoid, on what
+// evaluating it and adding its own bias may cost), the wave computes these
+// experts' logits again in FP64 (two or three of them as a rule) and selects
+// among FP64 choices.
+//
+// The bound on a logit's error follows its sum.  With u = 2^-24, a step of an
+// accumulator (one MFMA: C + 16 products, added in two halves) errs by at most
+//   kStepError u |partial sum| + kProductError u max|product|
+// (measured: 2.0, and 2.9 where all products are lost beside C; 7.0 for a
+// large product beside small ones), so the logit by
+//   u (kStepError sum_k |p_k| + kProductError |x| V),
+//   V = max_e sqrt(sum over the steps of max w_e^2) >= sum_k max|product| / |x|.
+// The product samples the partial sums p_k, the largest of each token over the
+// experts, every S steps.  Between two samples a partial sum differs from the
+// nearer one by the steps between, each at most |x_k| |w_k|; every step stands
+// between at most S / 2 partial sums (and the half of its own) and their
+// sample, and sum |x_k| |w_k| <= |x| |w|:
+//   sum_k |p_k| <= S sum |samples| + (S / 2 + 1 / 2) |x| |w|.
+// So rows of large terms that cancel are covered like any other.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <string.h>
@@ -66,7 +78,7 @@ constexpr int kTargetGroups = 256;  // workgroups a split over K aims at
 constexpr int kMaxSplits = 8;
 constexpr int kMaxGroups = 16;
 constexpr int kMaxTopK = 8;
-constexpr float kLogitMargin = 0x1p-17f;
+constexpr float kStepError = 3.0f, kProductError = 8.0f;  // in units of 2^-24
 
 struct RouterGemmArgs {
   const uint16_t* x;
@@ -78,12 +90,17 @@ struct RouterGemmArgs {
   int32_t splits, chunks_per_split;
   float* part;       // [splits][tokens][row]
   float* norm2;      // [splits][tokens]: squared norms of the token rows' parts
+  float* partial;    // [expert tiles][splits][tokens]: sums of |partial sum| over the steps
 };
 
 struct RouterSelectArgs {
   const float* part;
   const float* norm2;
-  const float* limits;  // [0] max |w_e|
+  const float* partial;
+  int32_t tiles;        // expert tiles of `partial`
+  float steps;          // of all accumulators together
+  float slack;          // steps between samples, as above
+  const float* limits;  // [0] max |w_e|, [1] V
   const uint16_t* x;
   int64_t x_stride;
   const uint16_t* w;  // [E, H] as the caller holds it
@@ -105,6 +122,10 @@ struct RouterSelectArgs {
 // consecutive rows touch 16 different bank groups.
 __device__ __forceinline__ int piece_at(int r, int c) { return r * kPieces + (c ^ (r & (kPieces - 1))); }
 
+// Chunks of 128 columns per sample of the partial sums, for so many accumulators
+// a wave: a sample looks at all of them.
+constexpr int samples_every(int accumulators) { return accumulators >= 8 ? 2 : 1; }
+
 // BT tokens (32, 64 or 128) x WE * EW * 32 experts per workgroup.  Wave
 // (we, wk): expert blocks [we * EW, +EW) of the tile, and K steps wk of every
 // chunk (8 / WE wave groups share a chunk's eight 16-wide steps).  ONCE: no
@@ -117,13 +138,17 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
   constexpr int STEPS = kKC / 16 / WK;              // MFMA steps of a wave per chunk
   constexpr int TB = BT / 32;                       // token blocks
   constexpr int NP = BT * kPieces / kGemmThreads;   // staged pieces per thread
+  constexpr int NS = samples_every(EW * TB);        // chunks per sample of the partial sums
   static_assert(NP >= 1 && STEPS >= 1, "tile shape");
   constexpr int kStage = 3 * BT * kPieces, kRed = WE * EW * 4 * 64;  // 16-byte pieces
   __shared__ __attribute__((aligned(1024))) u32x4 lds[kStage > kRed ? kStage : kRed];
+  __shared__ uint32_t partial[WK][BT];  // per wave group and token, as bits
+  static_assert(WK > 1, "the wave groups' sum has the barriers that partial needs");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int we = wave % WE, wk = wave / WE;
+  for (int i = tid; i < WK * BT; i += kGemmThreads) (&partial[0][0])[i] = 0u;
   const int t0 = blockIdx.x * BT;
   const int eb0 = (int)blockIdx.y * (WE * EW) + we * EW;
   const int split = blockIdx.z;
@@ -239,9 +264,38 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
     buf = next;
     __syncthreads();
   };
+  // |partial sum| of the token, the largest of this lane's experts; a segment
+  // counts with its last one.
+  float seen[TB], last[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) seen[t] = 0.0f;
+  auto sample = [&]() {
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      float m = 0.0f;  // a NaN does not count, an infinity does
+#pragma unroll
+      for (int b = 0; b < EW; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(acc[b][t][i]));
+      seen[t] += m;
+      last[t] = m;
+    }
+  };
   for (int c = c0; c < c1; c += 2) {
     chunk(xr[0], c);
-    if (c + 1 < c1) chunk(xr[1], c + 1);
+    if (NS == 1 || c + 1 >= c1) sample();
+    if (c + 1 < c1) {
+      chunk(xr[1], c + 1);
+      sample();
+    }
+  }
+  // The group's, over all lanes and waves of a token; adding the groups and
+  // parts are a few steps more.
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    float v = fmaf(seen[t], (float)(STEPS * NS), last[t] * (float)(WK + a.splits));
+    v = fmaxf(v, __shfl_xor(v, 32, 64));
+    if (lane < 32) atomicMax(&partial[wk][t * 32 + lane], __float_as_uint(v));
   }
 
   // Sum of the wave groups, one 32-token block at a time: groups 1.. leave
@@ -282,6 +336,12 @@ __global__ __launch_bounds__(kGemmThreads, 1) void router_gemm_kernel(RouterGemm
       const int t = t0 + pr + j * (kGemmThreads / kPieces);
       if (pc == 0 && t < a.tokens) a.norm2[(int64_t)split * a.tokens + t] = v;
     }
+  }
+  if (tid < BT && t0 + tid < a.tokens) {
+    float v = 0.0f;
+#pragma unroll
+    for (int g = 0; g < WK; ++g) v += __uint_as_float(partial[g][tid]);
+    a.partial[((int64_t)blockIdx.y * a.splits + split) * a.tokens + t0 + tid] = v;
   }
   if (wk != 0) return;
 #pragma unroll
@@ -407,6 +467,22 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const int e0 = grp * a.group_size + sub * a.per_lane;
   const int count = grp < a.groups ? max(0, min(a.per_lane, a.group_size - sub * a.per_lane)) : 0;
 
+  // Squared norms of the row's parts and sums of |partial sum|, the largest of
+  // the expert tiles (this half row's): asked for first, wanted last.
+  const int part = q & 7;
+  static_assert(kMaxSplits <= 8, "a lane of eight per part");
+  const bool has_part = part < a.splits;
+  const int64_t at_part = (int64_t)(has_part ? part : 0) * a.tokens + tt;
+  float n2 = a.norm2[at_part];
+  float sampled = 0.0f;
+  for (int y = 0; y < a.tiles; y += 8) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = a.partial[(int64_t)min(y + 2 * i + (q >> 3), a.tiles - 1) * a.splits * a.tokens + at_part];
+    sampled = fmaxf(fmaxf(sampled, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+  }
+
   // Its logits and biases.  Slots past the count read the lane's first
   // expert (the row's first, if it has none).
   float l[EPL], bias[EPL];
@@ -461,9 +537,9 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     row_logits = a.part + tt * a.row;
   }
   load_row(row_logits, l);
-  float n2 = 0.0f;
-  for (int s = q; s < a.splits; s += 16) n2 += a.norm2[(int64_t)s * a.tokens + tt];
-  n2 = row_sum(n2);
+  n2 = 0.5f * row_sum(has_part ? n2 : 0.0f);  // both halves of the row hold it
+  sampled = fmaxf(sampled, dppf<0x128>(sampled));  // row_ror:8, the other half's tiles
+  sampled = 0.5f * row_sum(has_part ? sampled : 0.0f);
 
   auto choice = [&](float logit, float bias) { return a.sigmoid ? sigmoid_fast(logit) + bias : logit; };
   uint32_t key[EPL], rest[EPL];
@@ -497,7 +573,10 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   // and rows whose squared norm leaves float32's range go by their FP32 logits
   // as they are: what lies close there is evaluated again in FP64 from these.
   // Without a bias the choices of a row of zeros are all equal, and in order.
-  const float bound = kLogitMargin * (sqrtf(n2) * a.limits[0] * rsqrtf((float)a.hidden) + largest);
+  const float xw = sqrtf(n2) * a.limits[0];
+  // beside a gate row with an infinity the samples say nothing
+  const float partials = sampled < INFINITY ? fmaf(a.slack, xw, sampled) : a.steps * xw;
+  const float bound = 1.02f * 0x1p-24f * fmaf(kStepError, partials, kProductError * a.limits[1] * sqrtf(n2));
   const bool guard = live && bound < INFINITY && n2 >= 0x1p-100f;
   const bool decide = live && (guard || a.biased || largest > 0.0f);
   const float logit_margin = guard ? bound : 0.0f;
@@ -920,27 +999,42 @@ __global__ __launch_bounds__(256) void router_tile_kernel(const uint16_t* w, u32
   dst[c] = v;
 }
 
-// limits[0] = max |w_e| of the experts without an infinite or NaN weight (whose
-// logits are neither numbers nor close to any), and the padded copy of the biases; one wave per expert slot of a logit row.  A maximum does not
-// depend on the order of the atomics; as bits, a NaN is larger than every
-// number.
+// limits[0] = max |w_e| and limits[1] = max of sqrt(sum over 16-column steps
+// of max w_e^2), over the experts without an infinite or NaN weight (whose
+// logits are neither numbers nor close to any), and the padded copy of the
+// biases; one wave per expert slot of a logit row.  A maximum does not depend
+// on the order of the atomics.
 __global__ __launch_bounds__(64) void router_limits_kernel(const uint16_t* w, const float* bias, int experts,
                                                            int hidden, uint32_t* limits, float* bias_copy) {
   const int e = blockIdx.x;
-  const float b = bias && e < experts ? bias[e] : 0.0f;
-  if (threadIdx.x == 0) bias_copy[e] = b;
+  if (threadIdx.x == 0) bias_copy[e] = bias && e < experts ? bias[e] : 0.0f;
   if (e >= experts) return;
-  float s = 0.0f;
+  float squares = 0.0f, steps = 0.0f;
   bool bad = false;
-  for (int i = threadIdx.x; i < hidden; i += 64) {
-    const float v = bf16_to_f32(w[(int64_t)e * hidden + i]);
-    s = fmaf(v, v, s);
-    bad |= !(fabsf(v) < INFINITY);
+  for (int i = threadIdx.x * 8; i - (int)threadIdx.x * 8 < hidden; i += 512) {  // two threads a step
+    float most = 0.0f;
+    if (i < hidden) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = bf16_to_f32(w[(int64_t)e * hidden + i + k]);
+        squares = fmaf(v, v, squares);
+        most = fmaxf(most, fabsf(v));
+        bad |= !(fabsf(v) < INFINITY);
+      }
+    }
+    most = fmaxf(most, __shfl_xor(most, 1, 64));
+    if (!(threadIdx.x & 1)) steps = fmaf(most, most, steps);
   }
   if (__ballot(bad)) return;
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-  if (threadIdx.x == 0) atomicMax(&limits[0], __float_as_uint(sqrtf(s)) & 0x7fffffffu);
+  for (int m = 1; m < 64; m <<= 1) {
+    squares += __shfl_xor(squares, m, 64);
+    steps += __shfl_xor(steps, m, 64);
+  }
+  if (threadIdx.x == 0) {
+    atomicMax(&limits[0], __float_as_uint(sqrtf(squares)));
+    atomicMax(&limits[1], __float_as_uint(sqrtf(steps)));
+  }
 }
 
 // Token tile and K split of a batch.
@@ -996,7 +1090,7 @@ Lanes lanes_for(const moe_router_config_t& c) {
 }
 
 struct RouterLayout {
-  size_t w, limits, bias, part, norm2, total;
+  size_t w, limits, bias, part, norm2, partial, total;
 };
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -1013,7 +1107,8 @@ RouterLayout router_layout(const moe_router_config_t& c, int64_t max_rows) {
   L.bias = L.limits + 256;
   L.part = L.bias + align256((size_t)row_of(c.num_experts) * 4);
   L.norm2 = L.part + align256((size_t)rows * row_of(c.num_experts) * 4);
-  L.total = L.norm2 + align256((size_t)rows * 4);
+  L.partial = L.norm2 + align256((size_t)rows * 4);
+  L.total = L.partial + align256((size_t)rows * (row_of(c.num_experts) / 32) * 4);
   return L;
 }
 
@@ -1190,6 +1285,7 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   g.chunks_per_split = p.chunks_per_split;
   g.part = reinterpret_cast<float*>(r->ws + r->L.part);
   g.norm2 = reinterpret_cast<float*>(r->ws + r->L.norm2);
+  g.partial = reinterpret_cast<float*>(r->ws + r->L.partial);
   const dim3 grid((num_tokens + p.bt - 1) / p.bt, (g.blocks + p.be - 1) / p.be, p.splits);
   if (p.bt == 32)
     moe::launch_gemm<32>(g, p.be, grid, s);
@@ -1200,6 +1296,13 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   moe::RouterSelectArgs a;
   a.part = g.part;
   a.norm2 = g.norm2;
+  a.partial = g.partial;
+  a.tiles = (int32_t)grid.y;
+  // as launch_gemm's kernels take them
+  const int groups = moe::kGemmWaves / (p.be < 4 ? p.be : 4);
+  const int sampled = moe::kKC / 16 / groups * moe::samples_every((p.be == 8 ? 2 : 1) * (p.bt / 32));
+  a.steps = (float)(c.hidden / 16 + groups + p.splits);
+  a.slack = (float)(sampled / 2) + 0.5f;
   a.limits = reinterpret_cast<const float*>(r->ws + r->L.limits);
   a.x = g.x;
   a.x_stride = x_stride;

@@ -145,3 +145,30 @@ def test_a_bad_gate_row_leaves_the_others_in_order(bad, score):
     for groups, top_groups in ((1, 1), (8, 4)):
         got = _ids(x, w, K, score=score, num_groups=groups, top_groups=top_groups)
         assert np.array_equal(got, ids_64(_logits(x, w), score, K, None, groups, top_groups))
+
+
+def _cancelling(kind, T, H, E, seed):
+    """Rows and gates whose running sums rise far above their logits."""
+    x, w, _ = _inputs(T, H, E, seed)
+    if kind == "outliers":      # two channels that cancel, at the ends of the row
+        x[:, 0], x[:, H - 1] = 4096, -4096
+        w[:, 0] = w[:, H - 1] = 1
+    elif kind == "neighbours":  # the same inside one K-block
+        x[:, 64], x[:, 65 + 16] = 4096, -4096
+        w[:, 64] = w[:, 65 + 16] = 1
+    else:                       # products of one sign in each half of the row
+        half = torch.where(torch.arange(H, device="cuda") < H // 2, 1.0, -1.0).bfloat16()
+        x, w = x.abs(), (w.abs() * half)
+        w = (w.float() * 0.02 + H ** -0.5 * half.float()).bfloat16()
+    return x, w
+
+
+@pytest.mark.parametrize("kind", ["outliers", "neighbours", "halves"])
+@pytest.mark.parametrize("T,H,score", [(9000, 7168, "sigmoid"), (8200, 7168, "softmax"), (5000, 7168, "sigmoid"),
+                                       (1100, 7168, "softmax"), (300, 16384, "sigmoid"), (20, 7168, "sigmoid"),
+                                       (1, 16384, "softmax")])
+def test_sums_that_cancel(T, H, score, kind):
+    E, K = 256, 8
+    x, w = _cancelling(kind, T, H, E, T)
+    got = _ids(x, w, K, score=score)
+    assert np.array_equal(got, ids_64(_logits(x, w), score, K))
