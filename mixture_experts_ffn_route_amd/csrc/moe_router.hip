@@ -960,7 +960,15 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const bool slot = q < a.top_k;
   float w;
   if (a.sigmoid) {
-    w = slot ? 1.0f / (1.0f + expf(-mine)) : 0.0f;
+    // exp(-l) overflows below -88: there a score is exp(l), and where the
+    // scores' sum cancels, all of them are taken exp(m) times as large, m the
+    // largest logit if it is negative.
+    const float m = fminf(unordered(row_max(slot ? ordered(mine) : 0u)), 0.0f);
+    const bool small = a.renormalize && unordered(row_min(slot ? ordered(mine) : 0xffffffffu)) < -80.0f;
+    const float by = small && m > -INFINITY ? m : 0.0f;
+    w = small || mine < -80.0f ? expf(fminf(mine, 0.0f) - by) / (1.0f + expf(-fabsf(mine)))
+                               : 1.0f / (1.0f + expf(-mine));
+    w = slot ? (mine == mine ? w : mine) : 0.0f;
   } else if (a.renormalize) {  // the sum over all experts cancels
     const float m = unordered(row_max(slot ? ordered(mine) : 0u));
     w = slot ? expf(mine - m) : 0.0f;

@@ -172,3 +172,33 @@ def test_sums_that_cancel(T, H, score, kind):
     x, w = _cancelling(kind, T, H, E, T)
     got = _ids(x, w, K, score=score)
     assert np.array_equal(got, ids_64(_logits(x, w), score, K))
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("size", [-0.4, -2.0, -20.0, 20.0])
+def test_weights_of_far_sigmoid_scores(size, renormalize):
+    """Scores down to exp(-2000), together with ordinary ones where ``size`` is
+    small: their ratios are ordinary all the same.
+
+    Rows have one element and gates two values, so that the logits are exact.
+    A weight is K scores' quotient: exp, sums, quotients and the scale make 32
+    half steps, and an exponent of up to 100 that is rounded once (2^-24 of
+    it) 100 more.  What is left below 2^-126 has its own steps of 2^-149, times
+    the scale."""
+    T, H, E, K = 40, 256, 16, 6
+    w = torch.zeros(E, H, device="cuda", dtype=torch.bfloat16)
+    w[:, 3] = torch.arange(1, E + 1, device="cuda").bfloat16()
+    x = torch.zeros(T, H, device="cuda", dtype=torch.bfloat16)
+    x[:, 3] = (size * torch.linspace(0.5, 6, T, device="cuda")).bfloat16()
+    logits = _logits(x, w)
+    r = MoERouter(w, K, max_rows=T, score="sigmoid", renormalize=renormalize, scale=2.5)
+    ids = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    _, got = r.route(x, ids=ids)
+    assert np.array_equal(ids.cpu().numpy(), ids_64(logits, "sigmoid", K))
+    l = np.take_along_axis(logits, ids.cpu().numpy().astype(np.int64), axis=1)
+    log_score = -np.logaddexp(0.0, -l)
+    if renormalize:
+        log_score = log_score - np.logaddexp.reduce(log_score, axis=1, keepdims=True)
+    want = 2.5 * np.exp(log_score)
+    got = got.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= 132 * U * want + 4 * 2.0 ** -149)
