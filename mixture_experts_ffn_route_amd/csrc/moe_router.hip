@@ -588,9 +588,12 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const float ev = a.sigmoid ? 0x1p-22f : 0.0f, eval = a.sigmoid ? 0x1p-20f : 0.0f;
   const float base = a.sigmoid ? fmaf(0.25f, logit_margin, eval) : logit_margin;
   auto margin_of = [&](float c) { return fmaf(ev, fabsf(c), base); };
+  // At a known logit the slope is s (1 - s) there, and within the margin at
+  // most exp(logit_margin) times that.
+  const float steeper = logit_margin < 1.0f ? fmaf(2.0f, logit_margin, 1.01f) : INFINITY;
   auto slope_margin = [&](float logit) {
     const float s = sigmoid_fast(logit);
-    return a.sigmoid ? fmaf(1.01f * s * (1.0f - s), logit_margin, eval) : logit_margin;
+    return a.sigmoid ? fmaf(fminf(0.25f, s * (1.0f - s) * steeper), logit_margin, eval) : logit_margin;
   };
   // FP64 logits of two (token row, expert) pairs at a time, in every lane, so
   // that a pair of neighbours costs one trip to memory.

@@ -202,3 +202,16 @@ def test_weights_of_far_sigmoid_scores(size, renormalize):
     want = 2.5 * np.exp(log_score)
     got = got.double().cpu().numpy()
     assert np.all(np.abs(got - want) <= 132 * U * want + 4 * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("size", [30.0, 3e3, 3e5, 3e8])
+def test_large_rows(size):
+    """Logits in the hundreds to billions, whose FP32 errors are as large as a
+    sigmoid's whole slope."""
+    T, H, E, K = 200, 2048, 128, 8
+    x, w, b = _inputs(T, H, E, 12, bias=True)
+    x = (size * x.float()).bfloat16()
+    w[:, 1:] = w[:1, 1:]  # the gates differ in one column
+    for groups, top_groups in ((1, 1), (4, 2)):
+        got = _ids(x, w, K, score="sigmoid", bias=b, num_groups=groups, top_groups=top_groups)
+        assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, b, groups, top_groups))
