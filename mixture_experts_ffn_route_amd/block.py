@@ -40,6 +40,8 @@ class MoEBlock:
         if router.cfg.local_experts != layer.cfg.num_experts:
             raise ValueError(f"the router maps to {router.cfg.local_experts} local experts, the layer has "
                              f"{layer.cfg.num_experts}")
+        if router.device != layer.workspace.device:
+            raise ValueError(f"router on device {router.device}, layer on {layer.workspace.device}")
         self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
         self.few = FEW_TOKENS if self.fp8 else FEW_TOKENS_MX

@@ -41,17 +41,26 @@ class MoELayer:
             raise ValueError("workspace too small")
         self.workspace = workspace
         self._keep = (w13, w13_scale, w2, w2_scale)  # the handle reads these in place
-        self.handle = L.moe_layer_create(self.cfg, expected_m, max_rows, capacity_factor, _ptr(w13),
-                                         _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(workspace),
-                                         self.ws_bytes, self._stream())
+        with torch.cuda.device(workspace.device):
+            self.handle = L.moe_layer_create(self.cfg, expected_m, max_rows, capacity_factor, _ptr(w13),
+                                             _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(workspace),
+                                             self.ws_bytes, self._stream())
         self._staged = None
 
     @staticmethod
     def _stream() -> int:
         return torch.cuda.current_stream().cuda_stream
 
+    def _elsewhere(self) -> bool:
+        """Whether another device than the layer's is current; its calls then
+        switch to it, for launches go to the current device's stream."""
+        return self.workspace.device.index != torch.cuda.current_device()
+
     def stage(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
               x_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if self._elsewhere():
+            with torch.cuda.device(self.workspace.device):
+                return self.stage(x, topk_idx, topk_w, x_scale, out)
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.hidden), dtype=torch.bfloat16, device=x.device)
@@ -64,6 +73,9 @@ class MoELayer:
         return out
 
     def forward(self) -> None:
+        if self._elsewhere():
+            with torch.cuda.device(self.workspace.device):
+                return self.forward()
         L.moe_layer_forward(self.handle, self._stream())
 
     def forward_noalloc(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, out: torch.Tensor,
@@ -71,6 +83,9 @@ class MoELayer:
         """Stage + forward with the per-call regions in the library's static
         device scratch (moe_layer_forward_noalloc): ``out`` and the optional
         int32 ``status`` word are caller tensors, nothing is allocated."""
+        if self._elsewhere():
+            with torch.cuda.device(self.workspace.device):
+                return self.forward_noalloc(x, topk_idx, topk_w, out, x_scale, status)
         for t in (x, topk_idx, topk_w, out) + tuple(t for t in (x_scale, status) if t is not None):
             if not t.is_contiguous():
                 raise ValueError("inputs must be contiguous")
@@ -85,7 +100,7 @@ class MoELayer:
         The optional int32 ``status`` word receives the call's MOE_DEV_*
         bits."""
         dev = self.workspace.device
-        if dev.index != torch.cuda.current_device():
+        if self._elsewhere():
             with torch.cuda.device(dev):
                 return self.decode(x, topk_idx, topk_w, x_scale, out, status)
         T = x.shape[0]
@@ -106,6 +121,9 @@ class MoELayer:
         return out
 
     def status(self) -> int:
+        if self._elsewhere():
+            with torch.cuda.device(self.workspace.device):
+                return self.status()
         return L.moe_read_status(self.handle, self._stream())
 
     def region(self, name: str, dtype: torch.dtype, shape=None) -> torch.Tensor:
