@@ -45,17 +45,23 @@ class MoEBlock:
         self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
         self.few = FEW_TOKENS if self.fp8 else FEW_TOKENS_MX
+        if layer.capacity_factor < 1.0:
+            self.few = 0  # the few-token layer drops no routes
 
-    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """x: bfloat16 [T, H]; residual: [T, H] or None.  Returns the experts'
-        output (bfloat16 [T, H]) and x + residual."""
+        output (bfloat16 [T, H]) and x + residual.  The optional int32
+        ``status`` word ([1]) receives the call's MOE_DEV_* bits
+        (``layer.status()`` has those of stage + forward only)."""
         n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8, bf16=True)
         idx, w = self.router.route(n.y)
         rows, scale = (n.codes, n.scale) if self.fp8 else (n.y, None)
         if x.shape[0] <= self.few:
-            out = self.layer.decode(rows, idx, w, x_scale=scale, out=out)
+            out = self.layer.decode(rows, idx, w, x_scale=scale, out=out, status=status)
         else:
             out = self.layer.stage(rows, idx, w, x_scale=scale, out=out)
             self.layer.forward()
+            if status is not None:
+                status.copy_(self.layer.region("status", torch.int32)[:1])
         return out, n.residual

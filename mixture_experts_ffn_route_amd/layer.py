@@ -33,7 +33,7 @@ class MoELayer:
                 raise ValueError("weights must be contiguous device tensors")
         self.cfg = L.make_config(hidden, intermediate, num_experts, top_k, weight_format, act_format, flags)
         self.hidden, self.top_k = hidden, top_k
-        self.max_rows = max_rows
+        self.max_rows, self.capacity_factor = max_rows, capacity_factor
         self.ws_bytes = L.moe_workspace_query(self.cfg, expected_m, max_rows, capacity_factor)
         if workspace is None:
             workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=w13.device)
