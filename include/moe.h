@@ -363,7 +363,8 @@ typedef struct {
  * codes and scales are what moe_stage_inputs and moe_layer_decode take as
  * prequantised rows.  Every output is rounded once, from FP32 values: the
  * codes are those of y, not of the BF16 row; with an FP32 residual those from
- * 2^-6 up are the codes of 64-bit arithmetic.
+ * 2^-6 up are the codes of 64-bit arithmetic, else those whose quotients lie in
+ * the middle of two codes (scales from 2^-100 up).
  *  x              device bfloat16 [T, H], rows x_stride elements apart.
  *  residual       device [T, H] of residual_type, rows residual_stride
  *                 elements apart; NULL: s = x.

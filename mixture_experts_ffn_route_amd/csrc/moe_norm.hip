@@ -82,19 +82,20 @@ __device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
   return u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
 }
 
+// The row's factor cancels in a code's quotient: y / scale = 448 p / max p with
+// p = s w, taken from p 2^k (k: the factor's exponent, so that p is near y),
+// where sums and products of short mantissas are exact and a quotient in the
+// middle of two codes comes out there (one in 3000 of BF16 rows).
+//
 // With an FP32 residual the codes are those of 64-bit arithmetic: a quotient
-// next to the middle between two codes, where its own roundings would decide,
-// is decided exactly, as long as s w stays within float32's range (T=1 4.5 us
-// against 4.1 without, T=4096 H=7168 75.0 against 72.0).  BF16 residuals go
-// without: sums and products of short mantissas lie exactly in the middle often
-// enough (one in 3000) that a fifth of the waves would take the longer way
-// (T=4096 53.9 us against 49.8, T=32768 346 against 307).
+// next to such a middle, where the roundings of p and max p would decide, is
+// decided exactly.
 //
 // from_middle: how far quotient q lies from that middle, in units of its last
 // place from kNear units below it on.  Codes are 2^20 units apart (from 2^-6
 // up; those below are not looked at: a step is 2^-9 there, beside a maximum of
-// 448).  A quotient carries eight roundings at most (sum, factor and weight of
-// its y and of the block's maximum, scale, quotient): 2^-21 of it, 4 to 8 units.
+// 448).  A quotient carries six roundings at most (sum and product of its p and
+// of the maximum, 7/8 p, its own): six half steps, 3 to 6 units.
 constexpr uint32_t kNear = 12;
 __device__ __forceinline__ uint32_t from_middle(float q) {
   return (__float_as_uint(q) - 0x80000u + kNear) & 0xfffffu;
@@ -143,17 +144,21 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(NormArgs a) {
     __syncthreads();  // the other parity's sums of the last row may still be read
     sum = 0.0;
     for (int i = 0; i < waves; ++i) sum += part[parity][i];
-    const float f = (float)(1.0 / sqrt(sum / a.hidden + (double)a.eps));
+    // 1 / rms = near * rest: a power of two (within float32's range) and the rest
+    const double factor = 1.0 / sqrt(sum / a.hidden + (double)a.eps);
+    const int k = !(factor >= 0x1p-126) ? -126 : factor >= 0x1p127 ? 127 : ilogb(factor);
+    const float near = __uint_as_float((uint32_t)(k + 127) << 23), rest = (float)ldexp(factor, -k);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = c * nt + tid;
       if (j >= chunks) continue;  // whole DPP rows: chunks and nt are multiples of 16
-      float y[8];
-      uint32_t m = 0;  // maximum of |y| as bits: a NaN is larger than every number
+      float p[8], y[8];
+      uint32_t m = 0;  // maximum of |p| as bits: a NaN is larger than every number
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        y[i] = s[c][i] * f * w[c][i];
-        m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+        p[i] = s[c][i] * near * w[c][i];
+        y[i] = p[i] * rest;
+        m = max(m, __float_as_uint(p[i]) & 0x7fffffffu);
       }
       // residual_out may be the residual and the BF16 rows x, which are read
       // again below where the sums are not exact
@@ -173,63 +178,59 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(NormArgs a) {
       };
       if constexpr (R != 2) store_rows();
       if (a.codes) {
-        const float scale = __uint_as_float(row16_max(m)) / kE4m3Max;
-        q_u32x2 codes;
-        if constexpr (R != 2) {
-          codes = quant8(y, scale);
-        } else {
-          const bool scaled = scale != 0.0f && isfinite(scale);
-          codes = codes_without_scale(scale);
-          float q[8];
-          uint32_t near = ~0u;
-          if (scaled) {
-            quotients8(y, scale, q);
+        const float top = __uint_as_float(row16_max(m));
+        const float scale = top * rest / kE4m3Max;
+        q_u32x2 codes = codes_without_scale(scale);
+        const bool scaled = scale != 0.0f && isfinite(scale);
+        // p / 512 against max p / 512 * 7 / 8, both exact; blocks of the smallest
+        // scales, whose own rounding counts, by their scale
+        const bool small = scale < 0x1p-100f;
+        float q[8];
+        if (scaled) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) near = min(near, from_middle(q[i]));
+          for (int i = 0; i < 8; ++i) q[i] = small ? y[i] : 0.875f * p[i];
+          quotients8(q, small ? scale : 0x1p-9f * top, q);
+        }
+        if constexpr (R == 2) {
+          uint32_t closest = ~0u;
+          if (scaled && !small) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) closest = min(closest, from_middle(q[i]));
           }
-          if (__ballot(near <= 2 * kNear)) {
-            // Next to a tie of two codes the quotient's own roundings decide:
-            // there 448 |s w| is compared with the middle times max|s w| (the
-            // row's factor cancels), all with the rests of their sums and
-            // products, and the quotient becomes the middle or a neighbour of it.
-            float p[8], rest[8];  // |s w| is p + rest
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              p[i] = fabsf(s[c][i] * w[c][i]);
-              rest[i] = fmaf(fabsf(s[c][i]), fabsf(w[c][i]), -p[i]);
-            }
+          if (__ballot(closest <= 2 * kNear)) {
+            // Next to a tie of two codes 7/8 |p| is compared with middle / 512 times
+            // max|p|, all with the rests of their sums and products, and the
+            // quotient becomes the middle or a neighbour of it.
+            float low[8];  // |p| is low more
             float x[8], r[8];
             load8_bf16(a.x + t * a.x_stride + j * 8, x);
             load8<true>(a.residual, t * a.residual_stride + j * 8, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float of_x = s[c][i] - r[i], lost = (x[i] - of_x) + (r[i] - (s[c][i] - of_x));
-              rest[i] += copysignf(1.0f, s[c][i]) * lost * fabsf(w[c][i]);
+              low[i] = fmaf(fabsf(s[c][i] * near), fabsf(w[c][i]), -fabsf(p[i])) +
+                       copysignf(1.0f, s[c][i]) * (lost * near) * fabsf(w[c][i]);
             }
-            uint32_t hi = 0;
+            // The maximum's: that of the largest |p| + low, whose |p| may be a
+            // unit below the largest.
+            float top_low = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hi = max(hi, __float_as_uint(p[i]));
-            const float top = __uint_as_float(row16_max(hi));
-            // The maximum's rest: that of the largest p + rest, whose p may be a
-            // unit below the largest p.
-            float top_rest = -INFINITY;
+            for (int i = 0; i < 8; ++i) top_low = fmaxf(top_low, (fabsf(p[i]) - top) + low[i]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top_rest = fmaxf(top_rest, (p[i] - top) + rest[i]);
-#pragma unroll
-            for (int k = 1; k < 16; k <<= 1) top_rest = fmaxf(top_rest, __shfl_xor(top_rest, k, 16));
+            for (int k = 1; k < 16; k <<= 1) top_low = fmaxf(top_low, __shfl_xor(top_low, k, 16));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (!scaled || from_middle(q[i]) > 2 * kNear) continue;
+              if (!scaled || small || from_middle(q[i]) > 2 * kNear) continue;
               const float middle = __uint_as_float((__float_as_uint(fabsf(q[i])) & 0xfff00000u) | 0x80000u);
-              const float h = middle * top;
-              const float d = fmaf(kE4m3Max, p[i], -h) - fmaf(middle, top, -h) +
-                              fmaf(kE4m3Max, rest[i], -middle * top_rest);
+              const float part = 0x1p-9f * middle, h = part * top;
+              const float d = fmaf(0.875f, fabsf(p[i]), -h) - fmaf(part, top, -h) +
+                              fmaf(0.875f, low[i], -part * top_low);
               if (fabsf(q[i]) >= 0x1p-6f)
                 q[i] = copysignf(__uint_as_float(__float_as_uint(middle) + (d > 0.0f ? 1 : d < 0.0f ? -1 : 0)), q[i]);
             }
           }
-          if (scaled) codes = codes8(q);
         }
+        if (scaled) codes = codes8(q);
         store_nt(a.codes + t * a.hidden + j * 8, codes);
         if ((tid & 15) == 0) a.scales[t * (a.hidden >> 7) + (j >> 4)] = scale;
       }
