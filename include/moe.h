@@ -322,9 +322,9 @@ moe_status_t moe_layer_forward_noalloc(moe_layer_t* layer, const void* x, const 
  * moe_layer_forward_noalloc, on the layer's weight tiles, but made for
  * streaming the chosen experts' weights: no staged rows, no compaction, no
  * y rows.  It differs from stage + forward in being more exact: the experts'
- * rows are added in FP32 and not rounded to bfloat16 on the way, FC1 (and
- * with MXFP8 weights FC2) multiplies on the BF16 MFMA, and MXFP8 layers take
- * their BF16 rows as they are.  Every route is held (capacity_factor does not
+ * rows are added in FP32 and not rounded to bfloat16 on the way, FC1 and FC2
+ * multiply on the BF16 MFMA, and MXFP8 layers take their BF16 rows as they
+ * are.  Every route is held (capacity_factor does not
  * drop any).
  *  status_bits  device uint32, may be NULL: receives the call's MOE_DEV_*
  *               bits (moe_read_status does not see them).
