@@ -29,7 +29,10 @@
 //    where every wave reads them.
 //  * router_select_kernel: sums the K parts in order and selects, 16 lanes
 //    per token and four tokens per wave, so that every cross-lane step is a
-//    DPP row operation for four tokens at once.
+//    DPP row operation for four tokens at once.  More than 256 experts take 32
+//    or 64 lanes, so that a lane never holds more than 16: with 32 and 64 of
+//    them it spilled its registers (E=512 H=4096 T=4096 69 us against 49, E=1024
+//    T=1 26 against 13).
 //
 // The ids are those of 64-bit arithmetic: where two choices that matter lie
 // closer than the bounds on their FP32 errors (and, of a sigmoid, on what
@@ -78,6 +81,7 @@ constexpr int kTargetGroups = 256;  // workgroups a split over K aims at
 constexpr int kMaxSplits = 8;
 constexpr int kMaxGroups = 16;
 constexpr int kMaxTopK = 8;
+constexpr int kMaxPerLane = 16;     // experts of a lane of the selection
 constexpr float kStepError = 3.0f, kProductError = 8.0f;  // in units of 2^-24
 
 struct RouterGemmArgs {
@@ -378,23 +382,30 @@ constexpr int kXor1 = 0xb1, kXor2 = 0x4e;              // quad_perm: lane ^ 1, l
 constexpr int kHalfMirror = 0x141, kMirror = 0x140;    // lane ^ 7, lane ^ 15
 constexpr int kNext = 0x101;                           // row_shl:1, the lane after; 0 in the last
 
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+// Over a token's L lanes: a row of 16, two or all four.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   v = max(v, dpp<kXor1>(v));
   v = max(v, dpp<kXor2>(v));
   v = max(v, dpp<kHalfMirror>(v));
-  return max(v, dpp<kMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  if constexpr (L > 16) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  if constexpr (L > 32) v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  return v;
 }
-__device__ __forceinline__ uint32_t row_min(uint32_t v) {
-  v = min(v, dpp<kXor1>(v));
-  v = min(v, dpp<kXor2>(v));
-  v = min(v, dpp<kHalfMirror>(v));
-  return min(v, dpp<kMirror>(v));
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return ~lanes_max<L>(~v);
 }
-__device__ __forceinline__ float row_sum(float v) {
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
   v += dppf<kXor1>(v);
   v += dppf<kXor2>(v);
   v += dppf<kHalfMirror>(v);
-  return v + dppf<kMirror>(v);
+  v += dppf<kMirror>(v);
+  if constexpr (L > 16) v += __shfl_xor(v, 16, 64);
+  if constexpr (L > 32) v += __shfl_xor(v, 32, 64);
+  return v;
 }
 
 // Floats in the order of their values as unsigned integers.  NaN is 1, below
@@ -445,21 +456,25 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
   }
 }
 
-// Where the experts of a token sit: lane q of its 16 belongs to group
-// q / lanes and holds `per_lane` experts of it from (q % lanes) * per_lane on,
-// at most EPL (one group: 16 lanes).  An expert's slot, q EPL + j, rises with
-// its number.
+// Where the experts of a token sit: lane q of its LPT (16, 32 or 64) belongs to
+// group q / lanes and holds `per_lane` experts of it from (q % lanes) *
+// per_lane on, at most EPL (one group: all lanes).  An expert's slot, q EPL +
+// j, rises with its number.
 //
 // A choice known in FP64 is kept as its value rounded to float32 and the rest:
 // key (ordered) then rest.  The rest is 0 for choices known in FP32.
-template <int EPL, bool SPLIT>
+template <int EPL, int LPT, bool SPLIT>
 __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
-  constexpr uint32_t kSlots = 16 * EPL;    // a power of two
+  constexpr uint32_t kSlots = LPT * EPL;   // a power of two
   constexpr uint32_t kSlotMask = kSlots - 1;
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // SPLIT: [4][row]
-  const int lane = threadIdx.x, q = lane & 15, row0 = lane & 48;
-  const int64_t tw = (int64_t)blockIdx.x * 4;  // first of the wave's four tokens
-  const int64_t t = tw + (lane >> 4);
+  constexpr int kTokens = 64 / LPT;        // of a wave
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // SPLIT: [kTokens][row]
+  const int lane = threadIdx.x, q = lane & (LPT - 1), row0 = lane - q;
+  const int64_t tw = (int64_t)blockIdx.x * kTokens;  // the wave's first token
+  const int64_t t = tw + lane / LPT;
+  auto row_max = [](uint32_t v) { return lanes_max<LPT>(v); };
+  auto row_min = [](uint32_t v) { return lanes_min<LPT>(v); };
+  auto row_sum = [](float v) { return lanes_sum<LPT>(v); };
   const bool live = t < a.tokens;
   const int64_t tt = live ? t : a.tokens - 1;
   // this lane's experts
@@ -469,7 +484,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 
   // Squared norms of the row's parts and sums of |partial sum|, the largest of
   // the expert tiles (this half row's): asked for first, wanted last.
-  const int part = q & 7;
+  const int part = lane & 7, odd = lane >> 3 & 1;
   static_assert(kMaxSplits <= 8, "a lane of eight per part");
   const bool has_part = part < a.splits;
   const int64_t at_part = (int64_t)(has_part ? part : 0) * a.tokens + tt;
@@ -479,7 +494,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = a.partial[(int64_t)min(y + 2 * i + (q >> 3), a.tiles - 1) * a.splits * a.tokens + at_part];
+      v[i] = a.partial[(int64_t)min(y + 2 * i + odd, a.tiles - 1) * a.splits * a.tokens + at_part];
     sampled = fmaxf(fmaxf(sampled, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
   }
 
@@ -503,7 +518,7 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   const float* row_logits;
   if constexpr (SPLIT) {
     // the K parts of the wave's tokens, summed in order
-    const int n4 = (int)min((int64_t)4, a.tokens - tw) * (a.row / 4);
+    const int n4 = (int)min((int64_t)kTokens, a.tokens - tw) * (a.row / 4);
     const f32x4* p = reinterpret_cast<const f32x4*>(a.part + tw * a.row);
     const int64_t step = (int64_t)a.tokens * a.row / 4;
     // up to 32 loads of a lane in flight; pieces past the end repeat the last
@@ -537,9 +552,9 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     row_logits = a.part + tt * a.row;
   }
   load_row(row_logits, l);
-  n2 = 0.5f * row_sum(has_part ? n2 : 0.0f);  // both halves of the row hold it
+  n2 = 0.5f * lanes_sum<16>(has_part ? n2 : 0.0f);  // both halves of the row hold it
   sampled = fmaxf(sampled, dppf<0x128>(sampled));  // row_ror:8, the other half's tiles
-  sampled = 0.5f * row_sum(has_part ? sampled : 0.0f);
+  sampled = 0.5f * lanes_sum<16>(has_part ? sampled : 0.0f);
 
   auto choice = [&](float logit, float bias) { return a.sigmoid ? sigmoid_fast(logit) + bias : logit; };
   uint32_t key[EPL], rest[EPL];
@@ -598,8 +613,8 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
   // FP64 logits of two (token row, expert) pairs at a time, in every lane, so
   // that a pair of neighbours costs one trip to memory.
   auto dot2 = [&](int from0, int expert0, int from1, int expert1, double& out0, double& out1) {
-    const uint16_t* rows[4] = {a.x + (tw + (from0 >> 4)) * a.x_stride, a.w + (int64_t)expert0 * a.hidden,
-                               a.x + (tw + (from1 >> 4)) * a.x_stride, a.w + (int64_t)expert1 * a.hidden};
+    const uint16_t* rows[4] = {a.x + (tw + from0 / LPT) * a.x_stride, a.w + (int64_t)expert0 * a.hidden,
+                               a.x + (tw + from1 / LPT) * a.x_stride, a.w + (int64_t)expert1 * a.hidden};
     // Two batches of loads, one on its way while the other is added up.
     constexpr int kBatch = 2;  // pieces of a row per batch: the additions, not the loads, take the time
     double d[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
@@ -717,21 +732,32 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
     if (a.lane_shift > 0) merge(dpp<kXor1>(k1), dpp<kXor1>(k2));
     if (a.lane_shift > 1) merge(dpp<kXor2>(k1), dpp<kXor2>(k2));
     if (a.lane_shift > 2) merge(dpp<kHalfMirror>(k1), dpp<kHalfMirror>(k2));
+    if constexpr (LPT > 16) {
+      if (a.lane_shift > 3) merge(dpp<kMirror>(k1), dpp<kMirror>(k2));
+      if (a.lane_shift > 4) merge(__shfl_xor((int)k1, 16, 64), __shfl_xor((int)k2, 16, 64));
+    }
     const float b1 = unordered(k1), b2 = two ? unordered(k2) : 0.0f;
     const float v = (two ? k2 : k1) > 1u ? b1 + b2 : NAN;
     const bool valid = grp < a.groups;
-    // lanes of groups ahead of this one, by rotating the row
     const uint32_t vk = valid ? ordered(v) : 0u;
     int ahead = 0;
+    if constexpr (LPT == 16) {  // lanes of groups ahead of this one, by rotating the row
 #define MOE_ROT(N)                                                                  \
   {                                                                                 \
     const uint32_t o = dpp<0x120 + N>(vk);                                          \
     ahead += (o > vk || (o == vk && ((q - N) & 15) >> a.lane_shift < grp)) ? 1 : 0; \
   }
-    MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
-    MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
+      MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
+      MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
 #undef MOE_ROT
-    in = valid && ahead < a.top_groups << a.lane_shift;
+      in = valid && ahead < a.top_groups << a.lane_shift;
+    } else {
+      for (int g = 0; g < a.groups; ++g) {
+        const uint32_t o = (uint32_t)__shfl((int)vk, row0 + (g << a.lane_shift), 64);
+        ahead += (o > vk || (o == vk && g < grp)) ? 1 : 0;
+      }
+      in = valid && ahead < a.top_groups;
+    }
     // least that the values that stay can be, most that the others can be
     const float gm = fmaf(ev, fabsf(b1) + fabsf(b2), two ? 2.0f * base : base);
     const bool number = fabsf(v) < INFINITY;
@@ -782,26 +808,16 @@ __global__ __launch_bounds__(64) void router_select_kernel(RouterSelectArgs a) {
 #pragma unroll
   for (int j = 0; j < EPL; ++j)
     pk[j] = in && key[j] ? (max(key[j], kSlots) & ~kSlotMask) | (kSlotMask - (uint32_t)(q * EPL + j)) : 0u;
-  // With up to 16 slots each lane sorts its own first, so that a maximum looks
-  // at one key per lane (T=4096: the selection's instructions halve).
-  if constexpr (EPL <= 16) sort_descending<EPL>(pk);
-  uint32_t mk = 0;  // lane k: the k-th packed key
+  // Each lane sorts its own first, so that a maximum looks at one key per lane
+  // (T=4096: the selection's instructions halve).
+  sort_descending<EPL>(pk);
+  uint32_t mk = 0;  // lane k of the token's first 16: the k-th packed key
   auto take = [&](int k) -> uint32_t {
-    uint32_t m = pk[0];
-    if constexpr (EPL > 16) {
+    const uint32_t m = row_max(pk[0]);
+    const bool hit = pk[0] == m;
 #pragma unroll
-      for (int j = 1; j < EPL; ++j) m = max(m, pk[j]);
-    }
-    m = row_max(m);
-    if constexpr (EPL > 16) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) pk[j] = pk[j] == m ? 0u : pk[j];
-    } else {
-      const bool hit = pk[0] == m;
-#pragma unroll
-      for (int j = 0; j + 1 < EPL; ++j) pk[j] = hit ? pk[j + 1] : pk[j];
-      pk[EPL - 1] = hit ? 0u : pk[EPL - 1];
-    }
+    for (int j = 0; j + 1 < EPL; ++j) pk[j] = hit ? pk[j + 1] : pk[j];
+    pk[EPL - 1] = hit ? 0u : pk[EPL - 1];
     if (q == k) mk = m;
     return m;
   };
@@ -1087,17 +1103,20 @@ Plan plan_for(const moe_router_config_t& c, int64_t tokens) {
 // Floats per logit row: whole blocks of 32 experts.
 int row_of(int experts) { return (experts + 31) / 32 * 32; }
 
-// Lanes of a token's 16 per group, a power of two, and experts per lane.
+// Lanes of a token: 16, or as many more as leave a lane 16 experts at most;
+// those of a group, a power of two, and experts per lane.
 struct Lanes {
-  int groups, lanes, per_lane;
+  int groups, of_token, lanes, per_lane;
 };
 Lanes lanes_for(const moe_router_config_t& c) {
   Lanes r;
   r.groups = c.top_groups == c.num_groups ? 1 : c.num_groups;  // every group stays: none to pick
-  r.lanes = 16;
-  while (r.lanes * r.groups > 16) r.lanes >>= 1;
-  r.per_lane = (c.num_experts / r.groups + r.lanes - 1) / r.lanes;
-  return r;
+  for (r.of_token = 16;; r.of_token *= 2) {
+    r.lanes = r.of_token;
+    while (r.lanes * r.groups > r.of_token) r.lanes >>= 1;
+    r.per_lane = (c.num_experts / r.groups + r.lanes - 1) / r.lanes;
+    if (r.per_lane <= kMaxPerLane || r.of_token == 64) return r;
+  }
 }
 
 struct RouterLayout {
@@ -1145,9 +1164,9 @@ moe_status_t validate(const moe_router_config_t* c, int32_t max_rows) {
   if (c->num_experts / c->num_groups * c->top_groups < c->top_k)
     return fail(MOE_ERR_INVALID_ARG, "top_groups %d hold fewer than top_k %d experts", c->top_groups, c->top_k);
   const Lanes n = lanes_for(*c);
-  if (n.per_lane > 64)
+  if (n.per_lane > kMaxPerLane)
     return fail(MOE_ERR_UNSUPPORTED, "groups of %d experts: %d groups take at most %d each",
-                c->num_experts / c->num_groups, c->num_groups, 64 * n.lanes);
+                c->num_experts / c->num_groups, c->num_groups, kMaxPerLane * n.lanes);
   if (c->renormalize != 0 && c->renormalize != 1)
     return fail(MOE_ERR_INVALID_ARG, "renormalize must be 0 or 1");
   if (!isfinite(c->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
@@ -1185,13 +1204,14 @@ void launch_gemm(const RouterGemmArgs& g, int be, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((router_gemm_kernel<BT, 2, 1>), grid, block, 0, s, g);
 }
 
-template <int EPL>
+template <int EPL, int LPT>
 void launch_select(const RouterSelectArgs& a, hipStream_t s) {
-  const dim3 grid((a.tokens + 3) / 4), block(64);
+  constexpr int kTokens = 64 / LPT;
+  const dim3 grid((a.tokens + kTokens - 1) / kTokens), block(64);
   if (a.splits > 1)
-    hipLaunchKernelGGL((router_select_kernel<EPL, true>), grid, block, 4 * a.row * sizeof(float), s, a);
+    hipLaunchKernelGGL((router_select_kernel<EPL, LPT, true>), grid, block, kTokens * a.row * sizeof(float), s, a);
   else
-    hipLaunchKernelGGL((router_select_kernel<EPL, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((router_select_kernel<EPL, LPT, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -1328,7 +1348,8 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   const moe::Lanes n = moe::lanes_for(c);
   a.groups = n.groups;
   a.group_size = c.num_experts / n.groups;
-  a.lane_shift = n.lanes == 16 ? 4 : n.lanes == 8 ? 3 : n.lanes == 4 ? 2 : n.lanes == 2 ? 1 : 0;
+  a.lane_shift = 0;
+  while (1 << a.lane_shift < n.lanes) ++a.lane_shift;
   a.per_lane = n.per_lane;
   a.top_groups = c.top_groups;
   a.sigmoid = c.score == MOE_SCORE_SIGMOID;
@@ -1340,18 +1361,18 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.idx = topk_idx;
   a.out_w = topk_w;
   a.ids = ids;
-  if (n.per_lane <= 2)
-    moe::launch_select<2>(a, s);
+  if (n.of_token == 64)
+    moe::launch_select<16, 64>(a, s);
+  else if (n.of_token == 32)
+    moe::launch_select<16, 32>(a, s);
+  else if (n.per_lane <= 2)
+    moe::launch_select<2, 16>(a, s);
   else if (n.per_lane <= 4)
-    moe::launch_select<4>(a, s);
+    moe::launch_select<4, 16>(a, s);
   else if (n.per_lane <= 8)
-    moe::launch_select<8>(a, s);
-  else if (n.per_lane <= 16)
-    moe::launch_select<16>(a, s);
-  else if (n.per_lane <= 32)
-    moe::launch_select<32>(a, s);
+    moe::launch_select<8, 16>(a, s);
   else
-    moe::launch_select<64>(a, s);
+    moe::launch_select<16, 16>(a, s);
   if (hipGetLastError() != hipSuccess) return moe::fail(MOE_ERR_HIP, "router launch failed");
   return MOE_OK;
 }

@@ -215,3 +215,18 @@ def test_large_rows(size):
     for groups, top_groups in ((1, 1), (4, 2)):
         got = _ids(x, w, K, score="sigmoid", bias=b, num_groups=groups, top_groups=top_groups)
         assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, b, groups, top_groups))
+
+
+@pytest.mark.parametrize("E,groups,top_groups", [(257, 1, 1), (384, 3, 2), (384, 12, 5), (510, 5, 2), (512, 16, 3),
+                                                 (512, 2, 1), (513, 1, 1), (640, 10, 4), (768, 3, 1), (960, 15, 7),
+                                                 (1000, 8, 4), (1024, 1, 1), (1024, 16, 15)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [1, 3, 131])
+def test_many_experts_close_together(E, groups, top_groups, score, T):
+    """More than 256 experts: a token takes 32 or 64 lanes."""
+    H, K = 512, 8
+    x, _, b = _inputs(T, H, E, E, bias=score == "sigmoid")
+    w = _close_gates(H, E, E)
+    bias = None if b is None else 2e-6 * b
+    got = _ids(x, w, K, score=score, bias=bias, num_groups=groups, top_groups=top_groups)
+    assert np.array_equal(got, ids_64(_logits(x, w), score, K, bias, groups, top_groups))
