@@ -29,10 +29,10 @@
 //    where every wave reads them.
 //  * router_select_kernel: sums the K parts in order and selects, 16 lanes
 //    per token and four tokens per wave, so that every cross-lane step is a
-//    DPP row operation for four tokens at once.  More than 256 experts take 32
-//    or 64 lanes, so that a lane never holds more than 16: with 32 and 64 of
-//    them it spilled its registers (E=512 H=4096 T=4096 69 us against 49, E=1024
-//    T=1 26 against 13).
+//    DPP row operation for four tokens at once.  Smaller batches take 32 or 64
+//    lanes, and more than 256 experts too, so that a lane never holds more than
+//    16: with 32 and 64 of them it spilled its registers (E=512 H=4096 T=4096 69
+//    us against 49, E=1024 T=1 26 against 13).
 //
 // The ids are those of 64-bit arithmetic: where two choices that matter lie
 // closer than the bounds on their FP32 errors (and, of a sigmoid, on what
@@ -1103,19 +1103,25 @@ Plan plan_for(const moe_router_config_t& c, int64_t tokens) {
 // Floats per logit row: whole blocks of 32 experts.
 int row_of(int experts) { return (experts + 31) / 32 * 32; }
 
-// Lanes of a token: 16, or as many more as leave a lane 16 experts at most;
-// those of a group, a power of two, and experts per lane.
+// Lanes of a token: 16, or as many more as leave a lane 16 experts at most, or
+// 4 at least where that makes no more than kSelectWaves waves of the batch (each
+// then has fewer tokens' FP64 logits to wait for; H=7168 E=256, us for the whole
+// call with 16, 32 and 64 lanes: T=1 11.6 / 10.7 / 10.5, 512 29.7 / 25.4 / 24.9,
+// 1024 33.7 / 31.4 / 30.4, 4096 52.2 / 48.1 / 49.0, 8192 76.8 / 78.2 / 82.8; E=32
+// T=509 12.2 / 12.5 / 13.0); those of a group, a power of two, and experts per lane.
+constexpr int64_t kSelectWaves = 2048;
 struct Lanes {
   int groups, of_token, lanes, per_lane;
 };
-Lanes lanes_for(const moe_router_config_t& c) {
+Lanes lanes_for(const moe_router_config_t& c, int64_t tokens) {
   Lanes r;
   r.groups = c.top_groups == c.num_groups ? 1 : c.num_groups;  // every group stays: none to pick
   for (r.of_token = 16;; r.of_token *= 2) {
     r.lanes = r.of_token;
     while (r.lanes * r.groups > r.of_token) r.lanes >>= 1;
     r.per_lane = (c.num_experts / r.groups + r.lanes - 1) / r.lanes;
-    if (r.per_lane <= kMaxPerLane || r.of_token == 64) return r;
+    const bool more = r.per_lane >= 8 && tokens * r.of_token * 2 <= kSelectWaves * 64;
+    if (r.of_token == 64 || (r.per_lane <= kMaxPerLane && !more)) return r;
   }
 }
 
@@ -1163,7 +1169,7 @@ moe_status_t validate(const moe_router_config_t* c, int32_t max_rows) {
     return fail(MOE_ERR_INVALID_ARG, "top_groups %d outside [1, %d]", c->top_groups, c->num_groups);
   if (c->num_experts / c->num_groups * c->top_groups < c->top_k)
     return fail(MOE_ERR_INVALID_ARG, "top_groups %d hold fewer than top_k %d experts", c->top_groups, c->top_k);
-  const Lanes n = lanes_for(*c);
+  const Lanes n = lanes_for(*c, max_rows);
   if (n.per_lane > kMaxPerLane)
     return fail(MOE_ERR_UNSUPPORTED, "groups of %d experts: %d groups take at most %d each",
                 c->num_experts / c->num_groups, c->num_groups, kMaxPerLane * n.lanes);
@@ -1212,6 +1218,18 @@ void launch_select(const RouterSelectArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((router_select_kernel<EPL, LPT, true>), grid, block, kTokens * a.row * sizeof(float), s, a);
   else
     hipLaunchKernelGGL((router_select_kernel<EPL, LPT, false>), grid, block, 0, s, a);
+}
+
+template <int LPT>
+void launch_select_lanes(const RouterSelectArgs& a, hipStream_t s) {
+  if (LPT == 16 && a.per_lane <= 2)  // lanes_for leaves the wider ones four at least
+    launch_select<2, 16>(a, s);
+  else if (a.per_lane <= 4)
+    launch_select<4, LPT>(a, s);
+  else if (a.per_lane <= 8)
+    launch_select<8, LPT>(a, s);
+  else
+    launch_select<16, LPT>(a, s);
 }
 
 }  // namespace
@@ -1345,7 +1363,7 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.row = g.row;
   a.splits = p.splits;
   a.top_k = c.top_k;
-  const moe::Lanes n = moe::lanes_for(c);
+  const moe::Lanes n = moe::lanes_for(c, num_tokens);
   a.groups = n.groups;
   a.group_size = c.num_experts / n.groups;
   a.lane_shift = 0;
@@ -1362,17 +1380,11 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.out_w = topk_w;
   a.ids = ids;
   if (n.of_token == 64)
-    moe::launch_select<16, 64>(a, s);
+    moe::launch_select_lanes<64>(a, s);
   else if (n.of_token == 32)
-    moe::launch_select<16, 32>(a, s);
-  else if (n.per_lane <= 2)
-    moe::launch_select<2, 16>(a, s);
-  else if (n.per_lane <= 4)
-    moe::launch_select<4, 16>(a, s);
-  else if (n.per_lane <= 8)
-    moe::launch_select<8, 16>(a, s);
+    moe::launch_select_lanes<32>(a, s);
   else
-    moe::launch_select<16, 16>(a, s);
+    moe::launch_select_lanes<16>(a, s);
   if (hipGetLastError() != hipSuccess) return moe::fail(MOE_ERR_HIP, "router launch failed");
   return MOE_OK;
 }
