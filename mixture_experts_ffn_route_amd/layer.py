@@ -37,8 +37,8 @@ class MoELayer:
         self.ws_bytes = L.moe_workspace_query(self.cfg, expected_m, max_rows, capacity_factor)
         if workspace is None:
             workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=w13.device)
-        elif workspace.numel() < self.ws_bytes:
-            raise ValueError("workspace too small")
+        elif workspace.numel() < self.ws_bytes or not workspace.is_contiguous():
+            raise ValueError("workspace too small, or not contiguous")
         self.workspace = workspace
         self._keep = (w13, w13_scale, w2, w2_scale)  # the handle reads these in place
         with torch.cuda.device(workspace.device):

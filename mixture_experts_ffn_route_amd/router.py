@@ -47,8 +47,9 @@ class MoERouter:
         self.ws_bytes = L.moe_router_workspace_query(self.cfg, max_rows)
         if workspace is None:
             workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-        elif workspace.numel() * workspace.element_size() < self.ws_bytes or workspace.device != self.device:
-            raise ValueError("workspace too small, or on another device")
+        elif (workspace.numel() * workspace.element_size() < self.ws_bytes or workspace.device != self.device
+              or not workspace.is_contiguous()):
+            raise ValueError("workspace too small, on another device, or not contiguous")
         self.workspace = workspace
         self._keep = (weight, bias)  # the handle reads the weight in place; the bias until its copy is made
         with torch.cuda.device(self.device):
