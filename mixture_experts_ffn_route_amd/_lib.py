@@ -19,7 +19,6 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 SLOT_TIMERS = os.environ.get("MOE_SLOT_TIMERS", "0") == "1"
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x_slot_timers.so" if SLOT_TIMERS else "libmoe_mi355x.so")
 MOE_SLOT_TIMER_WORDS = 32
-DECODE_TOKENS = 16  # most tokens moe_layer_decode takes
 
 # moe_status_t
 MOE_OK = 0

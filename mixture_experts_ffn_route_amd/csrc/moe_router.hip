@@ -109,7 +109,7 @@ struct RouterSelectArgs {
   int64_t x_stride;
   const uint16_t* w;  // [E, H] as the caller holds it
   const float* bias;    // [row]: zeros where there is none
-  int32_t tokens, hidden, experts, row, splits;
+  int32_t tokens, hidden, row, splits;
   int32_t top_k, groups, group_size, top_groups;
   int32_t lane_shift, per_lane;  // log2 of the lanes per group; see router_select_kernel
   int32_t sigmoid, renormalize;
@@ -1359,7 +1359,6 @@ extern "C" moe_status_t moe_router_forward(moe_router_t* r, const void* x, int64
   a.bias = reinterpret_cast<const float*>(r->ws + r->L.bias);
   a.tokens = num_tokens;
   a.hidden = c.hidden;
-  a.experts = c.num_experts;
   a.row = g.row;
   a.splits = p.splits;
   a.top_k = c.top_k;

@@ -18,9 +18,6 @@ from ._args import check, current_raw_stream, empty_rows, ptr
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
-def _ptr(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
-
 
 class MoELayer:
     def __init__(self, hidden: int, intermediate: int, num_experts: int, top_k: int,
@@ -42,8 +39,8 @@ class MoELayer:
         self.workspace = workspace
         self._keep = (w13, w13_scale, w2, w2_scale)  # the handle reads these in place
         with torch.cuda.device(workspace.device):
-            self.handle = L.moe_layer_create(self.cfg, expected_m, max_rows, capacity_factor, _ptr(w13),
-                                             _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(workspace),
+            self.handle = L.moe_layer_create(self.cfg, expected_m, max_rows, capacity_factor, ptr(w13),
+                                             ptr(w13_scale), ptr(w2), ptr(w2_scale), ptr(workspace),
                                              self.ws_bytes, self._stream())
         self._staged = None
 
@@ -67,7 +64,7 @@ class MoELayer:
         for t in (x, topk_idx, topk_w, out) + ((x_scale,) if x_scale is not None else ()):
             if not t.is_contiguous():
                 raise ValueError("inputs must be contiguous")
-        L.moe_stage_inputs(self.handle, _ptr(x), _ptr(x_scale), _ptr(topk_idx), _ptr(topk_w), T, _ptr(out),
+        L.moe_stage_inputs(self.handle, ptr(x), ptr(x_scale), ptr(topk_idx), ptr(topk_w), T, ptr(out),
                            self._stream())
         self._staged = (x, topk_idx, topk_w, x_scale, out)  # keep alive until forward
         return out
@@ -89,8 +86,8 @@ class MoELayer:
         for t in (x, topk_idx, topk_w, out) + tuple(t for t in (x_scale, status) if t is not None):
             if not t.is_contiguous():
                 raise ValueError("inputs must be contiguous")
-        L.moe_layer_forward_noalloc(self.handle, _ptr(x), _ptr(x_scale), _ptr(topk_idx), _ptr(topk_w), x.shape[0],
-                                    _ptr(out), _ptr(status), self._stream())
+        L.moe_layer_forward_noalloc(self.handle, ptr(x), ptr(x_scale), ptr(topk_idx), ptr(topk_w), x.shape[0],
+                                    ptr(out), ptr(status), self._stream())
 
     def decode(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                x_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -128,8 +125,8 @@ class MoELayer:
 
     def region(self, name: str, dtype: torch.dtype, shape=None) -> torch.Tensor:
         """A device view of a workspace region (no copy)."""
-        ptr, nbytes = L.moe_layer_region(self.handle, L.REGIONS[name])
-        off = ptr - self.workspace.data_ptr()
+        address, nbytes = L.moe_layer_region(self.handle, L.REGIONS[name])
+        off = address - self.workspace.data_ptr()
         view = self.workspace[off:off + nbytes].view(dtype)
         return view if shape is None else view[: int(torch.tensor(shape).prod())].view(*shape)
 
