@@ -17,15 +17,19 @@ from .layer import MoELayer
 from .norm import rms_norm_quant
 from .router import MoERouter
 
-# Batches of up to this many tokens take the few-token layer, which is faster
-# than stage + forward up to there (us, 32 experts, all here).  FP8 rows,
-# H=7168 I=2048 K=8: T=1 66 against 84, T=8 201 against 203, T=10 216 against
-# 217, T=12 222 against 221; H=2048 I=768 K=6: T=1 18 against 33, T=8 37
-# against 40, T=10 41 against 40.  MXFP8 weights: T=5 183 against 185, T=6 196
-# against 193, T=8 215 against 205; at the smaller sizes T=5 31 against 36, T=8
-# 39 against 40.
-FEW_TOKENS = 8
-FEW_TOKENS_MX = 5
+# Batches of up to so many tokens, expected to have so many routes here (tokens
+# top_k local_experts / num_experts), take the few-token layer, which is faster
+# than stage + forward up to there.  us, few-token / stage + forward:
+#   all experts here   FP8 H=7168 I=2048 K=8    T=1 66/84, 6 195/201, 8 212/206
+#                      FP8 H=2048 I=768 K=6     T=1 18/34, 8 38/40, 10 43/41
+#                      MXFP8, the first sizes   T=1 68/88, 4 163/175, 6 201/201, 8 219/209
+#                      MXFP8, the second        T=8 38/40, 10 42/40
+#   an eighth of them  FP8, the first           T=1 15/34, 8 62/87, 16 94/105
+#                      FP8, the second          T=16 24/35
+#                      MXFP8, the first         T=8 60/87, 12 100/104, 16 124/116
+#                      MXFP8, the second        T=16 25/35
+FEW_TOKENS, FEW_ROUTES = 16, 48
+FEW_TOKENS_MX, FEW_ROUTES_MX = 12, 40
 
 
 class MoEBlock:
@@ -44,7 +48,8 @@ class MoEBlock:
             raise ValueError(f"router on device {router.device}, layer on {layer.workspace.device}")
         self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
-        self.few = FEW_TOKENS if self.fp8 else FEW_TOKENS_MX
+        tokens, routes = (FEW_TOKENS, FEW_ROUTES) if self.fp8 else (FEW_TOKENS_MX, FEW_ROUTES_MX)
+        self.few = min(tokens, routes * router.cfg.num_experts // (router.top_k * router.cfg.local_experts))
         if layer.capacity_factor < 1.0:
             self.few = 0  # the few-token layer drops no routes
 

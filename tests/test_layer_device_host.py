@@ -38,6 +38,7 @@ def _layer():
     layer = object.__new__(MoELayer)
     layer.hidden, layer.top_k, layer.max_rows, layer.handle = 128, 2, 32, None
     layer.workspace = types.SimpleNamespace(device=torch.device("cuda", 1))
+    layer.capacity_factor = 1.0
     layer.cfg = types.SimpleNamespace(num_experts=4, act_format=block_module.L.MOE_ACT_E4M3_1X128)
     return layer
 
@@ -65,3 +66,17 @@ def test_block_refuses_a_router_on_another_device():
                                    cfg=types.SimpleNamespace(local_experts=4))
     with pytest.raises(ValueError, match="device"):
         MoEBlock(None, router, _layer())
+
+
+@pytest.mark.parametrize("fp8,top_k,experts,here,few", [
+    (True, 8, 32, 32, 6), (True, 6, 32, 32, 8), (True, 8, 256, 32, 16), (True, 1, 4, 4, 16),
+    (False, 8, 32, 32, 5), (False, 8, 256, 32, 12), (False, 8, 64, 32, 10)])
+def test_few_token_limit_goes_by_the_routes_expected_here(fp8, top_k, experts, here, few):
+    layer = _layer()
+    layer.top_k, layer.cfg.num_experts = top_k, here
+    layer.cfg.act_format = block_module.L.MOE_ACT_E4M3_1X128 if fp8 else block_module.L.MOE_ACT_BF16
+    router = types.SimpleNamespace(hidden=128, top_k=top_k, device=layer.workspace.device,
+                                   cfg=types.SimpleNamespace(local_experts=here, num_experts=experts, top_k=top_k))
+    assert MoEBlock(None, router, layer).few == few
+    layer.capacity_factor = 0.5
+    assert MoEBlock(None, router, layer).few == 0
