@@ -13,6 +13,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
+from ._args import check
 from .layer import MoELayer
 from .norm import rms_norm_quant
 from .router import MoERouter
@@ -59,6 +60,8 @@ class MoEBlock:
         output (bfloat16 [T, H]) and x + residual.  The optional int32
         ``status`` word ([1]) receives the call's MOE_DEV_* bits
         (``layer.status()`` has those of stage + forward only)."""
+        if status is not None:
+            check(status, "status", (1,), (torch.int32,), self.router.device)
         n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8, bf16=True)
         idx, w = self.router.route(n.y)
         rows, scale = (n.codes, n.scale) if self.fp8 else (n.y, None)

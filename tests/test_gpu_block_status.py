@@ -47,3 +47,37 @@ def test_a_layer_that_may_drop_routes(T):
     want = small.stage(n.codes, idx, w, x_scale=n.scale)
     small.forward()
     assert torch.equal(out, want) and int(status) == small.status() == L.MOE_DEV_CAPACITY
+
+
+@pytest.mark.parametrize("T", [4, 30])
+def test_status_word_of_a_captured_call(T):
+    _, _, _, _, block, x, r = _make(T, False, base=0, seed=T)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good, bad = x.clone(), x.clone()
+    bad[0, 3] = float("inf")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block.forward(x, r, status=status)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out, _ = block.forward(x, r, status=status)
+    torch.cuda.synchronize()
+    for rows, bits in ((good, 0), (bad, L.MOE_DEV_NONFINITE), (good, 0), (bad, L.MOE_DEV_NONFINITE)):
+        x.copy_(rows)
+        eager = torch.full_like(status, -1)
+        want, _ = block.forward(x, r, status=eager)
+        out.zero_()
+        status.fill_(-1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[1:], want[1:]) and int(status) == int(eager) == bits
+
+
+def test_status_word_is_checked():
+    _, _, _, _, block, x, r = _make(20, False)
+    for bad in (torch.zeros(1, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            block.forward(x, r, status=bad)
