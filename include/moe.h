@@ -329,8 +329,9 @@ moe_status_t moe_layer_forward_noalloc(moe_layer_t* layer, const void* x, const 
  *  status_bits  device uint32, may be NULL: receives the call's MOE_DEV_*
  *               bits (moe_read_status does not see them).
  * It is faster than stage + forward up to about 48 routes to this layer's
- * experts (FP8 weights) or 40 and 12 tokens (MXFP8); with all routes of 16
- * tokens it is up to 10 and 22 % slower.
+ * experts (FP8 weights; 16 and 8 with H above 7168 and 10240) or 40 and 12
+ * tokens (MXFP8); from there to 16 tokens with all routes it is up to 12 and
+ * 22 % slower, with the longer rows up to 40.
  * The layer's flags other than CHECK_ROUTES choose among forms of stage +
  * forward and do not matter here.  The handle's staged batch is left as it was;
  * the call uses regions of the workspace of its own, so calls on one handle

@@ -29,7 +29,11 @@ from .router import MoERouter
 #                      FP8, the second          T=16 24/35
 #                      MXFP8, the first         T=8 60/87, 12 100/104, 16 124/116
 #                      MXFP8, the second        T=16 25/35
+# Longer FP8 rows keep more of the token operand in registers, or spill it (I=1536
+# K=4 of 16, all here: H=10240 T=4 108/113, 8 140/126; H=12288 T=1 73/97, 4 145/126;
+# H=16384 T=1 90/120, 4 183/157).
 FEW_TOKENS, FEW_ROUTES = 16, 48
+FEW_ROUTES_LONG = ((10240, 8), (7168, 16))   # (rows longer than, routes)
 FEW_TOKENS_MX, FEW_ROUTES_MX = 12, 40
 
 
@@ -49,7 +53,10 @@ class MoEBlock:
             raise ValueError(f"router on device {router.device}, layer on {layer.workspace.device}")
         self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
-        tokens, routes = (FEW_TOKENS, FEW_ROUTES) if self.fp8 else (FEW_TOKENS_MX, FEW_ROUTES_MX)
+        tokens, routes = FEW_TOKENS_MX, FEW_ROUTES_MX
+        if self.fp8:
+            tokens = FEW_TOKENS
+            routes = next((r for hidden, r in FEW_ROUTES_LONG if layer.hidden > hidden), FEW_ROUTES)
         self.few = min(tokens, routes * router.cfg.num_experts // (router.top_k * router.cfg.local_experts))
         if layer.capacity_factor < 1.0:
             self.few = 0  # the few-token layer drops no routes

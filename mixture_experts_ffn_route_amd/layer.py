@@ -95,8 +95,9 @@ class MoELayer:
         """The whole layer for at most 16 tokens in two launches
         (moe_layer_decode): x bfloat16 [T, H], or e4m3 codes with x_scale.
         Faster than stage + forward up to about 48 routes to this layer's
-        experts (FP8 weights) or 40 and 12 tokens (MXFP8); from there to 16
-        tokens with all routes up to 10 and 22 % slower.
+        experts (FP8 weights; 16 and 8 with rows longer than 7168 and 10240) or
+        40 and 12 tokens (MXFP8); from there to 16 tokens with all routes up to
+        12 and 22 % slower, with the longer rows up to 40.
         The optional int32 ``status`` word receives the call's MOE_DEV_*
         bits."""
         dev = self.workspace.device

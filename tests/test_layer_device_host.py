@@ -68,14 +68,16 @@ def test_block_refuses_a_router_on_another_device():
         MoEBlock(None, router, _layer())
 
 
-@pytest.mark.parametrize("fp8,top_k,experts,here,few", [
-    (True, 8, 32, 32, 6), (True, 6, 32, 32, 8), (True, 8, 256, 32, 16), (True, 1, 4, 4, 16),
-    (False, 8, 32, 32, 5), (False, 8, 256, 32, 12), (False, 8, 64, 32, 10)])
-def test_few_token_limit_goes_by_the_routes_expected_here(fp8, top_k, experts, here, few):
+@pytest.mark.parametrize("fp8,hidden,top_k,experts,here,few", [
+    (True, 7168, 8, 32, 32, 6), (True, 2048, 6, 32, 32, 8), (True, 7168, 8, 256, 32, 16), (True, 128, 1, 4, 4, 16),
+    (True, 7296, 4, 16, 16, 4), (True, 10368, 4, 16, 16, 2), (True, 16384, 8, 256, 32, 8),
+    (False, 7168, 8, 32, 32, 5), (False, 16384, 8, 256, 32, 12), (False, 2048, 8, 64, 32, 10)])
+def test_few_token_limit_goes_by_the_routes_expected_here(fp8, hidden, top_k, experts, here, few):
     layer = _layer()
+    layer.hidden = hidden
     layer.top_k, layer.cfg.num_experts = top_k, here
     layer.cfg.act_format = block_module.L.MOE_ACT_E4M3_1X128 if fp8 else block_module.L.MOE_ACT_BF16
-    router = types.SimpleNamespace(hidden=128, top_k=top_k, device=layer.workspace.device,
+    router = types.SimpleNamespace(hidden=hidden, top_k=top_k, device=layer.workspace.device,
                                    cfg=types.SimpleNamespace(local_experts=here, num_experts=experts, top_k=top_k))
     assert MoEBlock(None, router, layer).few == few
     layer.capacity_factor = 0.5
