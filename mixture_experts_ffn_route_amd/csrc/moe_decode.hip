@@ -17,8 +17,8 @@
 //    few experts still make several hundred workgroups.  The waves' sums meet
 //    in LDS.
 //  * BF16 rows for FP8 weights are quantised by every FC1 workgroup for itself
-//    (T=16 H=7168: 229 KB of rows, from L2, each block by eight lanes; 235 us
-//    for the call against 226 with e4m3 rows given).
+//    (T=16 H=7168: 229 KB of rows, from L2, each block by eight lanes; 242 us
+//    for the call against 223 with e4m3 rows given).
 //  * h is quantised per 128 columns.  A workgroup makes whole blocks where the
 //    chosen experts have enough of them; the tasks of the others go to several
 //    workgroups, which store FP32 columns, and the last to arrive quantises
@@ -26,8 +26,8 @@
 //  * FC2 adds the experts' rows in FP32 with the routing weights applied to
 //    the partial sums, so there are no y rows and no combine.
 // The whole call, FP8 weights and e4m3 rows, H=7168 I=2048 K=8 of 32 experts:
-// T=1 66 us, 2 111, 4 165, 8 208, 16 226 (5.3 to 6.2 TB/s; FC1 takes two
-// thirds); MXFP8 66, 102, 162, 218, 269.  H=2048 I=768 K=6: T=1 18 us, 5 33,
+// T=1 67 us, 2 108, 4 160, 8 205, 16 223 (5.3 to 6.2 TB/s; FC1 takes two
+// thirds); MXFP8 67, 105, 163, 219, 282.  H=2048 I=768 K=6: T=1 18 us, 5 33,
 // 16 44, where the two launches' starts and ends, about 10 us, are what is
 // left beside the stream.
 #include <hip/hip_runtime.h>

@@ -18,9 +18,10 @@
 // one chunk of 16 consecutive lanes, a DPP row, so the block maximum never
 // leaves the wave.  The outputs are stored non-temporally: T=8192 H=2048 24.2
 // us against 30.8 with plain stores of codes and BF16 rows, T=4096 H=7168
-// 48.3 against 50.8.  At T=4096 H=7168 with a BF16 residual and every output
-// a call moves 265 MB in 48.3 us, 5.5 TB/s (a 2 GiB copy: 4.9); T=32768
-// without the BF16 rows 1652 MB in 295 us, 5.6 TB/s; T=1 takes 4.1 us.
+// 48.3 against 50.8 (before the quotients came from p: 2 to 3 % more now).  At
+// T=4096 H=7168 with a BF16 residual and every output a call moves 265 MB in 50.6
+// to 51.1 us, 5.2 TB/s (a 2 GiB copy: 4.9); T=32768 without the BF16 rows 1652 MB
+// in 314 to 322 us, 5.2 TB/s; T=1 takes 4.2 us.
 #include <hip/hip_runtime.h>
 #include <math.h>
 

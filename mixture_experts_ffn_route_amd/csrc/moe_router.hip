@@ -13,12 +13,13 @@
 // every number.
 //
 // Its floor is the token rows read once and the product on the MFMA: T=4096
-// H=7168 E=256 9 and 11 us, T=32768 68 and 89.  A call takes 10 us (T=1), 24
-// (512), 42 (4096), 163 (32768), of which the product 4, 8, 22 and 127 and the
-// 64-bit decisions about 10 from T=512 on: two FP64 logits take a wave 4 us (2
-// x 7168 products, converted and added one by one), a token whose groups or
-// experts lie close needs two to six of them, and the launch waits for the
-// slowest.
+// H=7168 E=256 9 and 11 us, T=32768 68 and 89.  A call takes 10.5 us (T=1), 26
+// (512), 47 (4096), 180 (32768), of which the product 5, 9, 23 and 135 (1 and 5
+// for sampling its partial sums at the last two) and the 64-bit decisions about
+// 10 from T=512 on, 20 at the last: two FP64 logits take a wave 4 us (2 x 7168
+// products, converted and added one by one), a token whose groups or experts lie
+// close needs two to six of them, and the launch waits for the slowest.  With a
+// tenth of the bound below a call would take 44 (4096) and 170 us.
 //
 // Two launches:
 //  * router_gemm_kernel: FP32 logits on the BF16 MFMA, split over K where a
@@ -53,7 +54,9 @@
 // between at most S / 2 partial sums (and the half of its own) and their
 // sample, and sum |x_k| |w_k| <= |x| |w|:
 //   sum_k |p_k| <= S sum |samples| + (S / 2 + 1 / 2) |x| |w|.
-// So rows of large terms that cancel are covered like any other.
+// So rows of large terms that cancel are covered like any other.  For rows and
+// gates of random signs, H = 7168, the bound is 1.4e-4 (T=4096, two K parts) to
+// 2.1e-4 (one part, 8 accumulators a wave) of a logit's size |x| |w| / sqrt(H).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <string.h>

@@ -82,7 +82,8 @@ def _expected(x, inp, mx, left=None):
 
 
 @pytest.mark.parametrize("T,H,I,E,K", [(1, 512, 256, 8, 2), (5, 2048, 768, 16, 6), (16, 1024, 384, 16, 8),
-                                       (8, 256, 2048, 4, 2), (3, 7168, 256, 8, 4)])
+                                       (8, 256, 2048, 4, 2), (3, 7168, 256, 8, 4), (5, 10496, 256, 4, 2),
+                                       (8, 16384, 128, 4, 2)])
 @pytest.mark.parametrize("form", ["codes", "e4m3", "e5m2"])
 def test_every_element(T, H, I, E, K, form):
     if form == "codes":
