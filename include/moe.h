@@ -380,7 +380,7 @@ typedef struct {
  * Strides are at least H and whole 16-byte pieces (of no account for one
  * row); pointers are 16-byte aligned (codes 8, scales 4).  A row is read
  * before any of it is written, so residual_out may be residual with the same
- * stride, and y_bf16 may be x with stride H.  A block of y with a NaN or an
+ * stride, and y_bf16 may be x with stride H (other strides are refused there).  A block of y with a NaN or an
  * infinity gets a NaN or infinite scale and NaN codes; an all-zero block
  * scale 0 and zero codes.  num_tokens 0 launches nothing. */
 moe_status_t moe_rms_norm_quant(const moe_norm_config_t* cfg, const void* x, int64_t x_stride, const void* residual,

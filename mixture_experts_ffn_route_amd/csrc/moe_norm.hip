@@ -309,6 +309,12 @@ extern "C" moe_status_t moe_rms_norm_quant(const moe_norm_config_t* cfg, const v
       return moe::fail(MOE_ERR_INVALID_ARG, "residual_stride %lld", (long long)residual_stride);
     if (residual_out && (residual_out_stride < H || residual_out_stride % per16))
       return moe::fail(MOE_ERR_INVALID_ARG, "residual_out_stride %lld", (long long)residual_out_stride);
+    // an output over its input: row over row, which the row's workgroup has read
+    if (residual_out && residual_out == residual && residual_out_stride != residual_stride)
+      return moe::fail(MOE_ERR_INVALID_ARG, "residual_out over residual with strides %lld and %lld",
+                       (long long)residual_out_stride, (long long)residual_stride);
+    if (y_bf16 && y_bf16 == x && x_stride != H)
+      return moe::fail(MOE_ERR_INVALID_ARG, "y over x with x_stride %lld", (long long)x_stride);
   }
   moe::NormArgs a;
   a.x = static_cast<const uint16_t*>(x);
