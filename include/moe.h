@@ -440,6 +440,8 @@ moe_status_t moe_router_workspace_query(const moe_router_config_t* cfg, int32_t 
  *             expert's bias, infinite or NaN too, concerns that expert alone
  *             (-inf switches it off while top_k others are left).
  *  workspace  device, 256-byte aligned, ws_bytes >= the query's.
+ *  stream     the weights' transform is launched on it: calls on another
+ *             stream have to wait for it.
  * The launches of one handle must not overlap on the device (its workspace
  * holds the logits of the call in progress). */
 moe_status_t moe_router_create(const moe_router_config_t* cfg, int32_t max_rows, const void* weight,

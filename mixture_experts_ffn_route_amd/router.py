@@ -24,7 +24,7 @@ class MoERouter:
     [expert_base, expert_base + local_experts) are this GPU's (all of them by
     default); routes to others come out as -1.  The weight is read in place
     while the router exists, the bias is copied; one router's calls must not
-    overlap on the device."""
+    overlap on the device, nor with its creation (on the stream current then)."""
 
     def __init__(self, weight: torch.Tensor, top_k: int, *, max_rows: int, score: str = "softmax",
                  bias: Optional[torch.Tensor] = None, num_groups: int = 1, top_groups: int = 1,
