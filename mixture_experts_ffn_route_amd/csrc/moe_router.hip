@@ -423,16 +423,23 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 
 // A choice known in FP64 is a float and a rest: the difference in units of
 // 2^-53 of the float's binade (FP64's own steps there, or halves of them), as
-// an ordered integer.  It is below 2^30.
+// an ordered integer.  It is below 2^30.  Where the float is subnormal or 0 the
+// rest is the FP64 value's upper half, which orders it to 2^-20 of itself.
 constexpr uint32_t kNoRest = 0x80000000u;
-__device__ __forceinline__ int rest_exponent(float hi) { return max(ilogbf(hi), -126) - 53; }
 __device__ __forceinline__ uint32_t rest_of(double c) {
   const float hi = (float)c;
-  return kNoRest + (uint32_t)(int)ldexp(c - (double)hi, -rest_exponent(hi));
+  if (fabsf(hi) < 0x1p-126f) {
+    const uint32_t up = (uint32_t)(__double_as_longlong(fabs(c)) >> 32);
+    return c < 0.0 ? kNoRest - up : kNoRest + up;
+  }
+  return kNoRest + (uint32_t)(int)ldexp(c - (double)hi, 53 - ilogbf(hi));
 }
 __device__ __forceinline__ double with_rest(uint32_t key, uint32_t rest) {
   const float hi = unordered(key);
-  return rest == kNoRest ? (double)hi : (double)hi + ldexp((double)(int)(rest - kNoRest), rest_exponent(hi));
+  const int r = (int)(rest - kNoRest);
+  if (r == 0) return (double)hi;
+  if (fabsf(hi) < 0x1p-126f) return copysign(__longlong_as_double((int64_t)abs(r) << 32), (double)r);
+  return (double)hi + ldexp((double)r, ilogbf(hi) - 53);
 }
 
 __device__ __forceinline__ float sigmoid_fast(float l) {

@@ -230,3 +230,18 @@ def test_many_experts_close_together(E, groups, top_groups, score, T):
     bias = None if b is None else 2e-6 * b
     got = _ids(x, w, K, score=score, bias=bias, num_groups=groups, top_groups=top_groups)
     assert np.array_equal(got, ids_64(_logits(x, w), score, K, bias, groups, top_groups))
+
+
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("E", [24, 40, 320])
+def test_scores_below_float32(E, groups, top_groups):
+    """Sigmoids of logits from -100 to -600 are all 0 in float32, not in
+    float64."""
+    T, H, K = 5, 256, 8
+    x = torch.zeros(T, H, device="cuda", dtype=torch.bfloat16)
+    x[:, 7] = torch.tensor([-1.0, -2.0, -1.25, -1.5, -1.75], device="cuda").bfloat16()
+    w = torch.zeros(E, H, device="cuda", dtype=torch.bfloat16)
+    w[:, 7] = (100 + torch.randperm(E, generator=torch.Generator().manual_seed(E)) % 128).cuda().bfloat16()
+    x[:, 9], w[:, 9] = 2.0 ** -7, torch.arange(E, device="cuda").bfloat16()  # and experts 2^-7 apart
+    got = _ids(x, w, K, score="sigmoid", num_groups=groups, top_groups=top_groups)
+    assert np.array_equal(got, ids_64(_logits(x, w), "sigmoid", K, None, groups, top_groups))
