@@ -461,6 +461,90 @@ moe_status_t moe_router_forward(moe_router_t* router, const void* x, int64_t x_s
 /* Release the handle (host memory only).  NULL is a no-op. */
 moe_status_t moe_router_destroy(moe_router_t* router);
 
+/* Matrix product of e4m3 rows with one scale per block of 128:
+ *   out[i, j] = bf16(sum_kb x_scale[i, kb] w_scale[j / 128, kb] sum_{c in kb} x[i, c] w[j, c] + add[i, j])
+ * over the K-blocks kb of 128 columns -- the dense projections beside the
+ * experts, in the block scaling of MOE_WEIGHT_E4M3_BLOCK128; x and x_scale are
+ * what moe_rms_norm_quant writes.  The last block of n and of k may be short.
+ *  x          device e4m3 [m, k], rows x_stride apart; x_scale float32
+ *             [m, ceil(k/128)], contiguous.
+ *  w          device e4m3 [n, k], rows w_stride apart; w_scale float32
+ *             [ceil(n/128), ceil(k/128)], contiguous.
+ *  add        device bfloat16 [m, n], rows add_stride apart, or NULL; may be
+ *             out itself (same stride).
+ *  out        device bfloat16 [m, n], rows out_stride apart; shares no memory
+ *             with the other inputs.
+ *  workspace  device, 256-byte aligned, at least the query's bytes (0 for many
+ *             sizes: then it may be NULL), of this call alone until it is done.
+ * k is a multiple of 16 and at most 65536, n at most 262144; the rows of x and
+ * w are 16-byte aligned, with strides of whole 16 bytes below 2^21.  m 0
+ * launches nothing.
+ *
+ * Sums over blocks are FP32, rounded once.  Up to 64 rows a block's sum is FP32
+ * too; above, it is one FP8 MFMA's, whose error is at most 2^-10 of the block's
+ * largest product.  A NaN code or scale makes its own row's (or weight's) results
+ * NaN.  A scale product outside of float32's normal range loses bits as such a
+ * number does. */
+moe_status_t moe_fp8_matmul_workspace_query(int32_t m, int32_t n, int32_t k, size_t* ws_bytes);
+moe_status_t moe_fp8_matmul(const uint8_t* x, int64_t x_stride, const float* x_scale, const uint8_t* w,
+                            int64_t w_stride, const float* w_scale, int32_t m, int32_t n, int32_t k,
+                            const void* add_bf16, int64_t add_stride, void* out_bf16, int64_t out_stride,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* Shared expert: the gated feed-forward block that every token takes beside its
+ * routed experts, with the layer's arithmetic:
+ *   g | u = x w13^T in FP32 (as moe_fp8_matmul), h = silu(g) u,
+ *   per 128 columns of h: scale = max|h| / 448, code = e4m3 RNE_sat(h / scale),
+ *   out = bf16(codes and scales times w2^T + add).
+ *  x, x_scale       as moe_fp8_matmul's, [T, H].
+ *  w13, w13_scale   device e4m3 [2 I, H] (gate rows, then up rows) and float32
+ *                   [2 I / 128, H / 128], contiguous.
+ *  w2, w2_scale     device e4m3 [H, I] and float32 [H / 128, I / 128].
+ *  add, out         as above, [T, H]: with both the routed experts' output, that
+ *                   output becomes the layer's.
+ * H and I are multiples of 128, at most 65536.  A row of h with a NaN or an
+ * infinity gives NaNs in its token's output. */
+moe_status_t moe_ffn_fp8_workspace_query(int32_t num_tokens, int32_t hidden, int32_t intermediate, size_t* ws_bytes);
+moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const float* x_scale, const uint8_t* w13,
+                         const float* w13_scale, const uint8_t* w2, const float* w2_scale, int32_t num_tokens,
+                         int32_t hidden, int32_t intermediate, const void* add_bf16, int64_t add_stride,
+                         void* out_bf16, int64_t out_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same block in bfloat16, with its gradients (before quantisation, and to
+ * train it):
+ *   g | u = x w13^T, h = silu(g) u, out = h w2^T.
+ *  x          device bfloat16 [T, H], rows x_stride apart.
+ *  w13, w2    device bfloat16 [2 I, H] (gate rows, then up rows) and [H, I].
+ *  gate_up    device float32 [T, 2 I]: g | u, for moe_ffn_backward; NULL: not
+ *             wanted.
+ *  h          device bfloat16 [T, I]: scratch, and for moe_ffn_backward.
+ *  out        device bfloat16 [T, H], rows out_stride apart.
+ * H and I are multiples of 8, at most 65536; pointers are 16-byte aligned and
+ * strides whole 16 bytes, below 2^20; outputs share memory with nothing else.
+ * Sums are FP32; h is rounded to bfloat16 between the products.  num_tokens 0
+ * launches nothing. */
+moe_status_t moe_ffn_workspace_query(int32_t num_tokens, int32_t hidden, int32_t intermediate,
+                                     size_t* forward_ws_bytes, size_t* backward_ws_bytes);
+moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const void* w13, const void* w2, int32_t num_tokens,
+                             int32_t hidden, int32_t intermediate, void* gate_up, void* h, void* out,
+                             int64_t out_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients from dy = d out (bfloat16 [T, H], rows dy_stride apart) and the
+ * forward's gate_up and h:
+ *   dh = dy w2, du = dh silu(g), dg = dh u s (1 + g (1 - s)), s = sigmoid(g),
+ *   dx = (dg | du) w13, dw13 = (dg | du)^T x, dw2 = dy^T h.
+ *  dx          device bfloat16 [T, H], rows dx_stride apart, or NULL.
+ *  dw13, dw2   device [2 I, H] and [H, I] of dw_type (MOE_TYPE_*), each or NULL.
+ *              accumulate 1 (float32 only): they are added to what is there.
+ * Inputs that the wanted gradients do not need may be NULL (x without dw13, w13
+ * without dx, h without dw2, w2 and gate_up with dw2 alone).  dg and du are
+ * rounded to bfloat16 between the products; sums are FP32, in an order that
+ * depends on the sizes alone.  With no tokens the weight gradients are zero. */
+moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* w13,
+                              const void* w2, const void* gate_up, const void* h, int32_t num_tokens, int32_t hidden,
+                              int32_t intermediate, void* dx, int64_t dx_stride, void* dw13, void* dw2,
+                              int32_t dw_type, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
 /* Optional per-kernel timing with HIP events recorded around the launches
  * of the selected kernel classes on the launch stream.  kernel_mask: bit
  * (1 << MOE_KERNEL_*) per class to time, MOE_PROFILE_ALL for all of them,

@@ -11,4 +11,6 @@ from ._lib import MoEError  # noqa: F401
 from .layer import MoELayer  # noqa: F401
 from .norm import NormOutput, rms_norm_quant  # noqa: F401
 from .router import MoERouter  # noqa: F401
+from .linear import MoESharedExpert, fp8_matmul  # noqa: F401
+from .ffn import gated_ffn, gated_ffn_backward, gated_ffn_forward  # noqa: F401
 from .block import MoEBlock  # noqa: F401

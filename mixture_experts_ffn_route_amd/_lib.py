@@ -10,6 +10,7 @@ importing this module raises ``ImportError`` -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
@@ -67,6 +68,8 @@ EXPORTS = (
     "moe_profile_read", "moe_layer_destroy", "moe_token_bucket", "moe_status_string",
     "moe_last_error", "moe_debug_slot_timers", "moe_rms_norm_quant",
     "moe_layer_decode", "moe_router_workspace_query", "moe_router_create", "moe_router_forward", "moe_router_destroy",
+    "moe_fp8_matmul_workspace_query", "moe_fp8_matmul", "moe_ffn_fp8_workspace_query", "moe_ffn_fp8",
+    "moe_ffn_workspace_query", "moe_ffn_forward", "moe_ffn_backward",
 )
 
 
@@ -123,7 +126,7 @@ def _load() -> ctypes.CDLL:
     # are valid handles here.
     import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
-    i32, vp = c_int32, c_void_p
+    i32, i64, vp = c_int32, c_int64, c_void_p
     sig = {
         "moe_workspace_query": (i32, [POINTER(moe_config_t), i32, i32, c_float, POINTER(c_size_t)]),
         "moe_layer_create": (i32, [POINTER(moe_config_t), i32, i32, c_float, POINTER(moe_weights_t), vp, c_size_t,
@@ -145,6 +148,14 @@ def _load() -> ctypes.CDLL:
         "moe_router_create": (i32, [POINTER(moe_router_config_t), i32, vp, vp, vp, c_size_t, vp, POINTER(vp)]),
         "moe_router_forward": (i32, [vp, vp, c_int64, i32, vp, vp, vp, vp]),
         "moe_router_destroy": (i32, [vp]),
+        "moe_fp8_matmul_workspace_query": (i32, [i32, i32, i32, POINTER(c_size_t)]),
+        "moe_fp8_matmul": (i32, [vp, i64, vp, vp, i64, vp, i32, i32, i32, vp, i64, vp, i64, vp, c_size_t, vp]),
+        "moe_ffn_fp8_workspace_query": (i32, [i32, i32, i32, POINTER(c_size_t)]),
+        "moe_ffn_fp8": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp, c_size_t, vp]),
+        "moe_ffn_workspace_query": (i32, [i32, i32, i32, POINTER(c_size_t), POINTER(c_size_t)]),
+        "moe_ffn_forward": (i32, [vp, i64, vp, vp, i32, i32, i32, vp, vp, vp, i64, vp, c_size_t, vp]),
+        "moe_ffn_backward": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i32, i32, vp,
+                                   c_size_t, vp]),
         "moe_token_bucket": (i32, [i32]),
         "moe_status_string": (c_char_p, [i32]),
         "moe_last_error": (c_char_p, []),
@@ -296,3 +307,54 @@ def moe_router_forward(router: int, x: int, x_stride: int, num_tokens: int, topk
 
 def moe_router_destroy(router: int) -> None:
     _check(_lib.moe_router_destroy(router))
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_fp8_matmul_workspace_query(m: int, n: int, k: int) -> int:
+    b = c_size_t(0)
+    _check(_lib.moe_fp8_matmul_workspace_query(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def moe_fp8_matmul(x: int, x_stride: int, x_scale: int, w: int, w_stride: int, w_scale: int, m: int, n: int, k: int,
+                   add: int, add_stride: int, out: int, out_stride: int, workspace: int, ws_bytes: int,
+                   stream: int = 0) -> None:
+    _check(_lib.moe_fp8_matmul(x, x_stride, x_scale, w, w_stride, w_scale, m, n, k, add or None, add_stride, out,
+                               out_stride, workspace or None, ws_bytes, stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_ffn_fp8_workspace_query(num_tokens: int, hidden: int, intermediate: int) -> int:
+    b = c_size_t(0)
+    _check(_lib.moe_ffn_fp8_workspace_query(num_tokens, hidden, intermediate, ctypes.byref(b)))
+    return b.value
+
+
+def moe_ffn_fp8(x: int, x_stride: int, x_scale: int, w13: int, w13_scale: int, w2: int, w2_scale: int, num_tokens: int,
+                hidden: int, intermediate: int, add: int, add_stride: int, out: int, out_stride: int, workspace: int,
+                ws_bytes: int, stream: int = 0) -> None:
+    _check(_lib.moe_ffn_fp8(x, x_stride, x_scale, w13, w13_scale, w2, w2_scale, num_tokens, hidden, intermediate,
+                            add or None, add_stride, out, out_stride, workspace or None, ws_bytes, stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_ffn_workspace_query(num_tokens: int, hidden: int, intermediate: int):
+    """Bytes of a forward's workspace and of a backward's."""
+    f, b = c_size_t(0), c_size_t(0)
+    _check(_lib.moe_ffn_workspace_query(num_tokens, hidden, intermediate, ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def moe_ffn_forward(x: int, x_stride: int, w13: int, w2: int, num_tokens: int, hidden: int, intermediate: int,
+                    gate_up: int, h: int, out: int, out_stride: int, workspace: int, ws_bytes: int,
+                    stream: int = 0) -> None:
+    _check(_lib.moe_ffn_forward(x, x_stride, w13, w2, num_tokens, hidden, intermediate, gate_up or None, h, out,
+                                out_stride, workspace or None, ws_bytes, stream))
+
+
+def moe_ffn_backward(dy: int, dy_stride: int, x: int, x_stride: int, w13: int, w2: int, gate_up: int, h: int,
+                     num_tokens: int, hidden: int, intermediate: int, dx: int, dx_stride: int, dw13: int, dw2: int,
+                     dw_type: int, accumulate: int, workspace: int, ws_bytes: int, stream: int = 0) -> None:
+    _check(_lib.moe_ffn_backward(dy, dy_stride, x or None, x_stride, w13 or None, w2 or None, gate_up or None,
+                                 h or None, num_tokens, hidden, intermediate, dx or None, dx_stride, dw13 or None,
+                                 dw2 or None, dw_type, accumulate, workspace or None, ws_bytes, stream))

@@ -40,6 +40,8 @@ SOURCES = [
     "moe_decode.hip",
     "moe_norm.hip",
     "moe_router.hip",
+    "moe_linear.hip",
+    "moe_ffn.hip",
 ]
 
 # Packed FP32 VALU ops are disabled for all device code.

@@ -1,0 +1,370 @@
+// Dense products on 128 x 128 (or 64 x 256) tiles: the simple form, for mid-size
+// batches, and the sums of products split over K.
+//
+// Four waves, 2 (n) x 2 (m); a K-block of 128 bytes is one stage of a ring of
+// two, and two workgroups share a CU, so that one's loads run beside the
+// other's MFMAs.
+#pragma once
+
+#include "moe_dense_dev.h"
+
+namespace moe {
+namespace dense {
+
+// What becomes of a tile's results.
+enum {
+  kOut,       // out = bf16(acc + add)
+  kOutF32,    // outf = acc, or outf + acc
+  kPart,      // part[split] = acc
+  kSwiglu,    // R = gate rows, then up rows: out = h = bf16(silu(g) u), gu = g | u where wanted
+  kSwigluQ,   // the same, h as e4m3 with a scale per 128 columns
+  kDswiglu,   // acc = dh: out = bf16(dg | du) from gu
+  kSwigluF32  // outf = h (few tokens)
+};
+
+struct Args {
+  const uint8_t* l;  // m side; strides in bytes between memory lines
+  int64_t l_stride;
+  const uint8_t* r;  // n side
+  int64_t r_stride;
+  const float* ls;   // e4m3: [m, kbs]
+  const float* rs;   // e4m3: [ceil(n / 128), kbs]
+  int32_t m, n, k;   // n: columns of the result (SwiGLU: of h)
+  int32_t kbs;       // K-blocks of 128 bytes (bfloat16: 64 values)
+  int32_t m_tiles, n_tiles, kb_per_split;
+  uint16_t* out;
+  int64_t out_stride;  // values
+  const uint16_t* add;  // null: none
+  int64_t add_stride;
+  float* outf;  // kOutF32: [m, n]; kPart: [splits, m, n]; kSwigluF32: [m, n]
+  int32_t accumulate;
+  int32_t vec;  // results of 4 columns may be stored at once
+  float* gu;  // [m, 2 n]
+  uint8_t* hq;
+  float* hs;
+};
+
+__device__ __forceinline__ void unpack4(u32x2 v, float f[4]) {
+  f[0] = bf16_to_f32(v[0] & 0xffffu);
+  f[1] = bf16_to_f32(v[0] >> 16);
+  f[2] = bf16_to_f32(v[1] & 0xffffu);
+  f[3] = bf16_to_f32(v[1] >> 16);
+}
+__device__ __forceinline__ u32x2 pack4(const float f[4]) { return u32x2{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])}; }
+
+// Four results of row m, columns [c, c + 4) (those below n exist).
+__device__ __forceinline__ void store_out(const Args& a, int64_t m, int c, const float v[4]) {
+  uint16_t* o = a.out + m * a.out_stride + c;
+  const uint16_t* d = a.add ? a.add + m * a.add_stride + c : nullptr;
+  if (a.vec && c + 4 <= a.n) {
+    float f[4] = {v[0], v[1], v[2], v[3]};
+    if (d) {
+      float e[4];
+      unpack4(*reinterpret_cast<const u32x2*>(d), e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] += e[i];
+    }
+    *reinterpret_cast<u32x2*>(o) = pack4(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < a.n) o[i] = (uint16_t)f32_to_bf16_rne(d ? v[i] + bf16_to_f32(d[i]) : v[i]);
+  }
+}
+__device__ __forceinline__ void store_f32(float* o, int c, int n, int vec, bool accumulate, const float v[4]) {
+  if (vec && c + 4 <= n) {
+    v4f f = {v[0], v[1], v[2], v[3]};
+    if (accumulate) f += *reinterpret_cast<const v4f*>(o);
+    *reinterpret_cast<v4f*>(o) = f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < n) o[i] = accumulate ? o[i] + v[i] : v[i];
+  }
+}
+// h, and g | u where wanted; n is a multiple of 4
+__device__ __forceinline__ void store_swiglu(const Args& a, int64_t m, int c, const float g[4], const float u[4]) {
+  if (c >= a.n) return;
+  float h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = swiglu(g[i], u[i]);
+  *reinterpret_cast<u32x2*>(a.out + m * a.out_stride + c) = pack4(h);
+  if (a.gu) {
+    float* p = a.gu + m * 2 * (int64_t)a.n + c;
+    *reinterpret_cast<v4f*>(p) = v4f{g[0], g[1], g[2], g[3]};
+    *reinterpret_cast<v4f*>(p + a.n) = v4f{u[0], u[1], u[2], u[3]};
+  }
+}
+__device__ __forceinline__ void store_dswiglu(const Args& a, int64_t m, int c, const float dh[4]) {
+  if (c >= a.n) return;
+  const float* p = a.gu + m * 2 * (int64_t)a.n + c;
+  const v4f g = *reinterpret_cast<const v4f*>(p), u = *reinterpret_cast<const v4f*>(p + a.n);
+  float dg[4], du[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dswiglu(g[i], u[i], dh[i], dg[i], du[i]);
+  uint16_t* o = a.out + m * a.out_stride + c;
+  *reinterpret_cast<u32x2*>(o) = pack4(dg);
+  *reinterpret_cast<u32x2*>(o + a.n) = pack4(du);
+}
+
+template <bool FP8, int LL, int LR, int BM, int BN, int EPI>
+__global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
+  constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
+  static_assert(!FP8 || (LL == kKin && LR == kKin), "e4m3 has no transposing read here");
+  constexpr int NB = BN / 32, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
+  constexpr int NP = (BN + BM) / 32;                      // DMA pieces per wave and K-block
+  constexpr int STAGE = (BN + BM) * kLine;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[2 * STAGE];
+  __shared__ uint32_t top_s[EPI == kSwigluQ ? 2 * BM : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
+  int mt, nt;
+  if (!tile_of(blockIdx.x, a.m_tiles, a.n_tiles, 8, mt, nt)) return;
+  const int m0 = mt * BM, n0 = nt * (kPair ? HN : BN);
+  const int kb0 = blockIdx.y * a.kb_per_split, kb1 = min(kb0 + a.kb_per_split, a.kbs);
+  constexpr int ES = FP8 ? 1 : 2;
+
+  // operands: two halves of R (gate and up rows, or rows that follow), L
+  Operand op[3];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int row = kPair ? n0 + h * a.n : n0 + h * HN;
+    int rows = kPair ? a.n - n0 : a.n - n0 - h * HN;
+    if (rows <= 0) {  // nothing there: half 0 again, not stored
+      row = n0;
+      rows = a.n - n0;
+    }
+    op[h] = Operand{a.r + (LR == kKin ? row * a.r_stride : (int64_t)row * ES), a.r_stride, min(rows, HN)};
+  }
+  op[2] = Operand{a.l + (LL == kKin ? m0 * a.l_stride : (int64_t)m0 * ES), a.l_stride, min(a.m - m0, BM)};
+  uint32_t off[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int p = i * 4 + wave;
+    if (i < HN / 32)
+      off[i] = piece_offset<LR>(op[0], p, lane);
+    else if (i < BN / 32)
+      off[i] = piece_offset<LR>(op[1], p - HN / 8, lane);
+    else
+      off[i] = piece_offset<LL>(op[2], p - BN / 8, lane);
+  }
+  auto issue = [&](int kb) {
+    const lds_u8* st = (const lds_u8*)ring_lds + (kb & 1) * STAGE;
+    const int64_t radv = LR == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.r_stride;
+    const int64_t ladv = LL == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.l_stride;
+    const int kleft = a.k - kb * (kLine / ES);  // values of K from here on
+    if (kleft >= kLine / ES) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const bool is_r = i < BN / 32;
+        dma16(is_r ? op[i < HN / 32 ? 0 : 1].base + radv : op[2].base + ladv, off[i], st + (i * 4 + wave) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const bool is_r = i < BN / 32;
+        const int p = i * 4 + wave - (is_r ? (i < HN / 32 ? 0 : HN / 8) : BN / 8);
+        const uint8_t* src = (is_r ? op[i < HN / 32 ? 0 : 1].base + radv : op[2].base + ladv) + off[i];
+        const bool ok = is_r ? piece_valid<LR>(p, lane, LR == kKin ? kleft * ES : kleft)
+                             : piece_valid<LL>(p, lane, LL == kKin ? kleft * ES : kleft);
+        dma16_at(ok ? src : (const uint8_t*)&kZeros, st + (i * 4 + wave) * 1024);
+      }
+    }
+  };
+
+  // e4m3: scales of this lane's tokens and of the two halves' weight blocks
+  const float* sx_p[TB];
+  const float* sw_p[2];
+  float sx[TB], sw[2];
+  if constexpr (FP8) {
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+      sx_p[t] = a.ls + (int64_t)min(m0 + wm * (BM / 2) + t * 16 + (lane & 15), a.m - 1) * a.kbs;
+    const int blocks = ((kPair ? 2 * a.n : a.n) + 127) / 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      sw_p[h] = a.rs + (int64_t)min((kPair ? n0 + h * a.n : n0 + h * HN) / 128, blocks - 1) * a.kbs;
+  }
+  auto scales = [&](int kb) {
+    if constexpr (FP8) {
+#pragma unroll
+      for (int t = 0; t < TB; ++t) sx[t] = sx_p[t][kb];
+      sw[0] = sw_p[0][kb];
+      sw[1] = sw_p[1][kb];
+    }
+  };
+
+  v4f acc[NB][TB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  // block of R's fragment i within the half: (half, block)
+  auto r_tile = [&](const lds_u8* st, int i) { return st + (i < NB / 2 ? 0 : HN * kLine); };
+  auto r_block = [&](int i) { return wn * (NB / 2) + (i < NB / 2 ? i : i - NB / 2); };
+
+  if (kb0 < kb1) {  // (no tokens: no K-block)
+    scales(kb0);
+    issue(kb0);
+  }
+  for (int kb = kb0; kb < kb1; ++kb) {
+    wait_vm<0>();
+    wait_lds();
+    barrier();
+    const lds_u8* st = (const lds_u8*)ring_lds + (kb & 1) * STAGE;
+    const lds_u8* lt = st + BN * kLine;
+    float f0[TB], f1[TB];
+    if constexpr (FP8) {
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        f0[t] = sx[t] * sw[0];
+        f1[t] = sx[t] * sw[1];
+      }
+    }
+    if (kb + 1 < kb1) {
+      scales(kb + 1);
+      issue(kb + 1);
+    }
+    if constexpr (FP8) {
+      v8i rf[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) rf[i] = frag_fp8(r_tile(st, i), r_block(i), lane);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const v8i lf = frag_fp8(lt, wm * TB + t, lane);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rf[i], lf, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
+                                                                         127, 0, 127);
+          const float f = i < NB / 2 ? f0[t] : f1[t];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(p[e], f, acc[i][t][e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        v8bf rf[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) rf[i] = frag_bf16<LR>(r_tile(st, i), r_block(i), s, lane);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const v8bf lf = frag_bf16<LL>(lt, wm * TB + t, s, lane);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rf[i], lf, acc[i][t], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  const int lm = m0 + wm * (BM / 2) + (lane & 15);  // this lane's row of block t: + 16 t
+  const int lc = 4 * (lane >> 4);
+  if constexpr (EPI == kSwigluQ) {
+    static_assert(EPI != kSwigluQ || HN == 128, "one scale block of h per tile");
+    float h[NB / 2][TB][4];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      uint32_t top = 0;  // max |h| as bits: a NaN is larger than every number
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[i][t][e] = swiglu(acc[i][t][e], acc[NB / 2 + i][t][e]);
+          top = max(top, __float_as_uint(h[i][t][e]) & 0x7fffffffu);
+        }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      if (lane < 16) top_s[wn * BM + wm * (BM / 2) + t * 16 + lane] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int r = wm * (BM / 2) + t * 16 + (lane & 15), m = m0 + r;
+      if (m >= a.m) continue;
+      const float s = __uint_as_float(max(top_s[r], top_s[BM + r])) / kE4m3Max;
+      if (wn == 0 && lane < 16) a.hs[(int64_t)m * (a.n / 128) + nt] = s;
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i)
+        *reinterpret_cast<uint32_t*>(a.hq + (int64_t)m * a.n + n0 + wn * (HN / 2) + i * 16 + lc) = quant4(h[i][t], s);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int64_t m = lm + t * 16;
+      if (m >= a.m) continue;
+#pragma unroll
+      for (int i = 0; i < (kPair ? NB / 2 : NB); ++i) {
+        const int c = n0 + (i < NB / 2 ? 0 : HN) + r_block(i) * 16 + lc;
+        const v4f v = acc[i][t];
+        const float f[4] = {v[0], v[1], v[2], v[3]};
+        if constexpr (EPI == kOut) {
+          store_out(a, m, c, f);
+        } else if constexpr (EPI == kOutF32) {
+          store_f32(a.outf + m * a.n + c, c, a.n, a.vec, a.accumulate, f);
+        } else if constexpr (EPI == kPart) {
+          store_f32(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.n + c, c, a.n, a.vec, false, f);
+        } else if constexpr (EPI == kSwiglu) {
+          const v4f w = acc[NB / 2 + i][t];
+          const float u[4] = {w[0], w[1], w[2], w[3]};
+          store_swiglu(a, m, c, f, u);
+        } else {
+          store_dswiglu(a, m, c, f);
+        }
+      }
+    }
+  }
+}
+
+// Sums of kPart results over the splits, in ascending order, and what becomes
+// of them; a thread takes 4 columns of one row.  kSwigluQ: 32 lanes hold a scale
+// block.  part: [splits, a.m, cols].
+template <int EPI>
+__global__ __launch_bounds__(256) void join_kernel(Args a, const float* part, int splits, int cols) {
+  constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
+  const int quads = (a.n + 3) / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = at / quads;
+  const int c = (int)(at - m * quads) * 4;
+  if (m >= a.m) return;  // kSwigluQ: whole groups of 32 lanes
+  const int64_t plane = (int64_t)a.m * cols;
+  const bool whole = cols % 4 == 0;
+  float v[kPair ? 2 : 1][4] = {};
+#pragma unroll
+  for (int h = 0; h < (kPair ? 2 : 1); ++h) {
+    const float* p = part + m * cols + c + h * a.n;
+    for (int s = 0; s < splits; ++s, p += plane) {
+      if (whole) {
+        const v4f w = *reinterpret_cast<const v4f*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[h][i] += w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < cols) v[h][i] += p[i];
+      }
+    }
+  }
+  if constexpr (EPI == kOut) {
+    store_out(a, m, c, v[0]);
+  } else if constexpr (EPI == kDswiglu) {
+    store_dswiglu(a, m, c, v[0]);
+  } else if constexpr (EPI == kSwiglu) {
+    store_swiglu(a, m, c, v[0], v[1]);
+  } else {
+    float h[4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = swiglu(v[0][i], v[1][i]);
+      top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, w, 32));
+    const float s = __uint_as_float(top) / kE4m3Max;
+    *reinterpret_cast<uint32_t*>(a.hq + m * a.n + c) = quant4(h, s);
+    if (c % 128 == 0) a.hs[m * (a.n / 128) + c / 128] = s;
+  }
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,271 @@
+// The BF16 gated feed-forward block with its gradients (moe_ffn_forward,
+// moe_ffn_backward).
+//
+//   g | u = x w13^T, h = silu(g) u, y = h w2^T
+//   dh = dy w2, du = dh silu(g), dg = dh u s (1 + g (1 - s)), s = sigmoid(g)
+//   dx = (dg | du) w13, dw13 = (dg | du)^T x, dw2 = dy^T h
+//
+// Sums are FP32.  Rounded to bfloat16 between the products are h and dg | du,
+// which the MFMA takes.  g | u stay float32 for the gradients: as bfloat16 they
+// would save 16 T I bytes of traffic (1.5 % of a step at T=4096 H=7168 I=2048) and
+// double the error that dx and dw13 have beside their own rounding (0.0030 in
+// place of 0.0024 of their root mean square, of which that rounding is 0.0017).
+#include <hip/hip_runtime.h>
+
+#include "moe_dense_few.h"
+#include "moe_dense_host.h"
+#include "moe_dense_tile.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+using namespace dense;
+
+constexpr int kFewTokens = 64;  // up to here the few-token form
+
+size_t parts_bytes(int m, int n, int kbs) {
+  const int s = splits_for(m, n, kbs);
+  return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
+}
+
+template <int EPI>
+void launch_few(const Args& a, hipStream_t s) {
+  const dim3 grid(cdiv(a.n, EPI == kSwiglu ? 16 : 32));
+  if (a.m <= 16)
+    hipLaunchKernelGGL((few_kernel<kBf16, 2, 1, 2, 16, EPI>), grid, dim3(1024), 0, s, a);
+  else if (a.m <= 32)
+    hipLaunchKernelGGL((few_kernel<kBf16, 2, 2, 2, 8, EPI>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((few_kernel<kBf16, 2, 4, 2, 8, EPI>), grid, dim3(512), 0, s, a);
+}
+
+// n: columns of the product (SwiGLU: of h).
+template <int LL, int LR, int EPI>
+void launch_tile(Args a, int splits, hipStream_t s) {
+  a.m_tiles = cdiv(a.m, 128);
+  a.n_tiles = cdiv(a.n, EPI == kSwiglu ? 64 : 128);
+  a.kb_per_split = splits > 1 ? cdiv(a.kbs, splits) : a.kbs;
+  hipLaunchKernelGGL((tile_kernel<false, LL, LR, 128, 128, EPI>), dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles), splits),
+                     dim3(256), 0, s, a);
+}
+
+// A product whose result has n columns, of L (K inside) and R, into EPI; with
+// SwiGLU h has half of the columns.
+template <int LR, int EPI>
+void product(Args a, int n, float* parts, hipStream_t s) {
+  const int splits = splits_for(a.m, n, a.kbs);
+  if (splits == 1) return launch_tile<kKin, LR, EPI>(a, 1, s);
+  Args p = a;
+  p.n = n;
+  p.outf = parts;
+  p.vec = 1;
+  launch_tile<kKin, LR, kPart>(p, splits, s);
+  launch_join<EPI>(a, parts, splits, n, s);
+}
+
+moe_status_t check_sizes(int32_t m, int32_t hidden, int32_t inter) {
+  if (m < 0 || hidden <= 0 || inter <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "num_tokens %d, hidden %d, intermediate %d", m, hidden, inter);
+  if (hidden % 8 || inter % 8 || hidden > 65536 || inter > 65536)
+    return fail(MOE_ERR_UNSUPPORTED, "hidden (%d) and intermediate (%d) must be multiples of 8, at most 65536", hidden,
+                inter);
+  return MOE_OK;
+}
+moe_status_t check_rows(const char* name, const void* p, int64_t stride, int64_t rows, int64_t cols) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "%s must be non-NULL", name);
+  if ((uintptr_t)p & 15) return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (rows > 1 && (stride < cols || stride % 8 || stride > kMaxStride / 2))
+    return fail(MOE_ERR_INVALID_ARG, "%s_stride %lld: %lld at least, a multiple of 8, at most %lld", name,
+                (long long)stride, (long long)cols, (long long)(kMaxStride / 2));
+  return MOE_OK;
+}
+
+struct Area {
+  const void* p;
+  int64_t bytes;
+};
+// Outputs share memory with no other area.
+moe_status_t check_apart(const Area* outs, int n_outs, const Area* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+        return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return fail(MOE_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  return MOE_OK;
+}
+
+size_t forward_bytes(int m, int hidden, int inter) {
+  if (m <= kFewTokens) return 0;
+  const size_t a = parts_bytes(m, 2 * inter, cdiv(hidden, 64)), b = parts_bytes(m, hidden, cdiv(inter, 64));
+  return a > b ? a : b;
+}
+// dg | du, then parts
+size_t backward_bytes(int m, int hidden, int inter, size_t* first) {
+  *first = pad256((size_t)m * 2 * inter * 2);
+  const size_t a = parts_bytes(m, inter, cdiv(hidden, 64)), b = parts_bytes(m, hidden, cdiv(2 * inter, 64));
+  return *first + (a > b ? a : b);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_ffn_workspace_query(int32_t num_tokens, int32_t hidden, int32_t intermediate,
+                                                size_t* forward_ws_bytes, size_t* backward_ws_bytes) {
+  using namespace moe;
+  clear_error();
+  if (!forward_ws_bytes || !backward_ws_bytes) return fail(MOE_ERR_INVALID_ARG, "ws_bytes is NULL");
+  const moe_status_t st = check_sizes(num_tokens, hidden, intermediate);
+  if (st != MOE_OK) return st;
+  size_t first;
+  *forward_ws_bytes = num_tokens == 0 ? 0 : forward_bytes(num_tokens, hidden, intermediate);
+  *backward_ws_bytes = num_tokens == 0 ? 0 : backward_bytes(num_tokens, hidden, intermediate, &first);
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const void* w13, const void* w2,
+                                        int32_t num_tokens, int32_t hidden, int32_t intermediate, void* gate_up,
+                                        void* h, void* out, int64_t out_stride, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+  using namespace moe;
+  clear_error();
+  const int32_t m = num_tokens;
+  moe_status_t st = check_sizes(m, hidden, intermediate);
+  if (st != MOE_OK) return st;
+  if (m == 0) return MOE_OK;
+  if ((st = check_rows("x", x, x_stride, m, hidden)) != MOE_OK) return st;
+  if ((st = check_rows("out", out, out_stride, m, hidden)) != MOE_OK) return st;
+  if ((st = check_rows("w13", w13, hidden, 1, hidden)) != MOE_OK) return st;
+  if ((st = check_rows("w2", w2, intermediate, 1, intermediate)) != MOE_OK) return st;
+  if ((st = check_rows("h", h, intermediate, 1, intermediate)) != MOE_OK) return st;
+  if ((uintptr_t)gate_up & 15) return fail(MOE_ERR_INVALID_ARG, "gate_up must be 16-byte aligned");
+  const int64_t weights = (int64_t)hidden * intermediate * 2, rows = (int64_t)m * intermediate * 2;
+  const Area outs[] = {{out, span(m, out_stride, hidden, 2)}, {h, rows}, {gate_up, 4 * rows}};
+  const Area ins[] = {{x, span(m, x_stride, hidden, 2)}, {w13, 2 * weights}, {w2, weights}};
+  if ((st = check_apart(outs, 3, ins, 3)) != MOE_OK) return st;
+  if ((st = check_workspace(workspace, ws_bytes, forward_bytes(m, hidden, intermediate))) != MOE_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  Args a = {};
+  a.l = static_cast<const uint8_t*>(x);
+  a.l_stride = m == 1 ? (int64_t)hidden * 2 : x_stride * 2;
+  a.r = static_cast<const uint8_t*>(w13);
+  a.r_stride = (int64_t)hidden * 2;
+  a.m = m;
+  a.n = intermediate;
+  a.k = hidden;
+  a.kbs = cdiv(hidden, 64);
+  a.out = static_cast<uint16_t*>(h);
+  a.out_stride = intermediate;
+  a.gu = static_cast<float*>(gate_up);
+  Args b = {};
+  b.l = static_cast<const uint8_t*>(h);
+  b.l_stride = (int64_t)intermediate * 2;
+  b.r = static_cast<const uint8_t*>(w2);
+  b.r_stride = (int64_t)intermediate * 2;
+  b.m = m;
+  b.n = hidden;
+  b.k = intermediate;
+  b.kbs = cdiv(intermediate, 64);
+  set_out(b, nullptr, 0, out, out_stride);
+  if (m <= kFewTokens) {
+    launch_few<kSwiglu>(a, s);
+    launch_few<kOut>(b, s);
+  } else {
+    float* parts = static_cast<float*>(workspace);
+    product<kKin, kSwiglu>(a, 2 * intermediate, parts, s);
+    product<kKin, kOut>(b, hidden, parts, s);
+  }
+  return launched("gated ffn");
+}
+
+extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                         const void* w13, const void* w2, const void* gate_up, const void* h,
+                                         int32_t num_tokens, int32_t hidden, int32_t intermediate, void* dx,
+                                         int64_t dx_stride, void* dw13, void* dw2, int32_t dw_type, int32_t accumulate,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  clear_error();
+  const int32_t m = num_tokens;
+  moe_status_t st = check_sizes(m, hidden, intermediate);
+  if (st != MOE_OK) return st;
+  if (dw_type != MOE_TYPE_BF16 && dw_type != MOE_TYPE_F32) return fail(MOE_ERR_INVALID_ARG, "unknown dw_type %d", dw_type);
+  if (accumulate != 0 && accumulate != 1) return fail(MOE_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  if (accumulate && dw_type != MOE_TYPE_F32)
+    return fail(MOE_ERR_UNSUPPORTED, "accumulate needs float32 weight gradients");
+  if ((((uintptr_t)dw13 | (uintptr_t)dw2) & 15)) return fail(MOE_ERR_INVALID_ARG, "dw13 and dw2 must be 16-byte aligned");
+  size_t first = 0;
+  if (m > 0) {
+    if ((st = check_rows("dy", dy, dy_stride, m, hidden)) != MOE_OK) return st;
+    if ((dw13 && (st = check_rows("x", x, x_stride, m, hidden)) != MOE_OK)) return st;
+    if (dx && (st = check_rows("dx", dx, dx_stride, m, hidden)) != MOE_OK) return st;
+    if (dx && (st = check_rows("w13", w13, hidden, 1, hidden)) != MOE_OK) return st;
+    if ((dx || dw13) && (st = check_rows("w2", w2, intermediate, 1, intermediate)) != MOE_OK) return st;
+    if ((dx || dw13) && (st = check_rows("gate_up", gate_up, intermediate, 1, intermediate)) != MOE_OK) return st;
+    if (dw2 && (st = check_rows("h", h, intermediate, 1, intermediate)) != MOE_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, backward_bytes(m, hidden, intermediate, &first))) != MOE_OK) return st;
+  }
+  const int64_t weights = (int64_t)hidden * intermediate, rows = (int64_t)m * intermediate * 2;
+  const int size = dw_type == MOE_TYPE_F32 ? 4 : 2;
+  const Area outs[] = {{dx, span(m, dx_stride, hidden, 2)}, {dw13, 2 * weights * size}, {dw2, weights * size}};
+  const Area ins[] = {{dy, span(m, dy_stride, hidden, 2)}, {x, span(m, x_stride, hidden, 2)}, {w13, 4 * weights},
+                      {w2, 2 * weights}, {gate_up, 4 * rows}, {h, rows}};
+  if ((st = check_apart(outs, 3, ins, 6)) != MOE_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* dgu = static_cast<uint8_t*>(workspace);
+  float* parts = reinterpret_cast<float*>(dgu + first);
+  const int64_t dys = m == 1 ? hidden : dy_stride, xs = m == 1 ? hidden : x_stride;
+  if (m > 0 && (dx || dw13)) {
+    Args a = {};  // dh, and from it dg | du
+    a.l = static_cast<const uint8_t*>(dy);
+    a.l_stride = dys * 2;
+    a.r = static_cast<const uint8_t*>(w2);
+    a.r_stride = (int64_t)intermediate * 2;
+    a.m = m;
+    a.n = intermediate;
+    a.k = hidden;
+    a.kbs = cdiv(hidden, 64);
+    a.gu = const_cast<float*>(static_cast<const float*>(gate_up));
+    a.out = reinterpret_cast<uint16_t*>(dgu);
+    a.out_stride = 2 * (int64_t)intermediate;
+    product<kKout, kDswiglu>(a, intermediate, parts, s);
+  }
+  if (m > 0 && dx) {
+    Args a = {};
+    a.l = dgu;
+    a.l_stride = (int64_t)intermediate * 4;
+    a.r = static_cast<const uint8_t*>(w13);
+    a.r_stride = (int64_t)hidden * 2;
+    a.m = m;
+    a.n = hidden;
+    a.k = 2 * intermediate;
+    a.kbs = cdiv(2 * intermediate, 64);
+    set_out(a, nullptr, 0, dx, dx_stride);
+    product<kKout, kOut>(a, hidden, parts, s);
+  }
+  for (int which = 0; which < 2; ++which) {  // dw13 [2 I, H], dw2 [H, I]
+    void* dw = which ? dw2 : dw13;
+    if (!dw) continue;
+    Args a = {};
+    a.l = which ? static_cast<const uint8_t*>(dy) : dgu;
+    a.l_stride = which ? dys * 2 : (int64_t)intermediate * 4;
+    a.r = static_cast<const uint8_t*>(which ? h : x);
+    a.r_stride = which ? (int64_t)intermediate * 2 : xs * 2;
+    a.m = which ? hidden : 2 * intermediate;
+    a.n = which ? intermediate : hidden;
+    a.k = m;
+    a.kbs = cdiv(m, 64);
+    a.accumulate = accumulate;
+    if (dw_type == MOE_TYPE_F32) {
+      a.outf = static_cast<float*>(dw);
+      a.vec = 1;
+      launch_tile<kKout, kKout, kOutF32>(a, 1, s);
+    } else {
+      set_out(a, nullptr, 0, dw, a.n);
+      launch_tile<kKout, kKout, kOut>(a, 1, s);
+    }
+  }
+  return launched("gated ffn backward");
+}

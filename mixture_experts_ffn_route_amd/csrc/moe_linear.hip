@@ -1,0 +1,245 @@
+// The e4m3 matrix product with block scales (moe_fp8_matmul) and the shared
+// expert on it (moe_ffn_fp8).
+//
+//   out[m, n] = bf16(sum_kb sx[m, kb] sw[n / 128, kb] sum_{k in kb} x[m, k] w[n, k] + add[m, n])
+//   shared expert: g | u = x w13^T in float32, h = silu(g) u, per 128 columns of h
+//   hs = max|h| / 448 and e4m3 codes, out = the product of those with w2
+#include <hip/hip_runtime.h>
+
+#include "moe_dense_few.h"
+#include "moe_dense_host.h"
+#include "moe_dense_tile.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+using namespace dense;
+
+constexpr int kFewTokens = 64;  // up to here the few-token form
+constexpr int kFewQuant = 16;   // up to here the shared expert's second product quantises h as it reads it
+
+size_t parts_bytes(int m, int n, int kbs) {
+  if (m <= kFewTokens) return 0;
+  const int s = splits_for(m, n, kbs);
+  return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
+}
+
+template <int L, int RB, int EPI>
+void launch_few(const Args& a, hipStream_t s) {
+  const dim3 grid(cdiv(a.n, EPI == kSwigluF32 ? 16 : 16 * RB));
+  if (a.m <= 16)
+    hipLaunchKernelGGL((few_kernel<L, RB, 1, 2, 16, EPI>), grid, dim3(1024), 0, s, a);
+  else if (a.m <= 32)
+    hipLaunchKernelGGL((few_kernel<L, RB, 2, 2, 8, EPI>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((few_kernel<L, RB, 4, 2, 8, EPI>), grid, dim3(512), 0, s, a);
+}
+
+// One product of e4m3 rows, n columns, into `parts` where K is split.
+void tile_parts(Args a, int splits, float* parts, hipStream_t s) {
+  a.outf = parts;
+  a.vec = a.n % 4 == 0;
+  a.m_tiles = cdiv(a.m, 128);
+  a.n_tiles = cdiv(a.n, 128);
+  a.kb_per_split = cdiv(a.kbs, splits);
+  hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 128, 128, kPart>),
+                     dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles), splits), dim3(256), 0, s, a);
+}
+
+void product(Args a, float* parts, hipStream_t s) {
+  if (a.m <= kFewTokens) return launch_few<kCodes, 2, kOut>(a, s);
+  const int splits = splits_for(a.m, a.n, a.kbs);
+  if (splits > 1) {
+    tile_parts(a, splits, parts, s);
+    return launch_join<kOut>(a, parts, splits, a.n, s);
+  }
+  a.m_tiles = cdiv(a.m, 128);
+  a.n_tiles = cdiv(a.n, 128);
+  a.kb_per_split = a.kbs;
+  hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 128, 128, kOut>), dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles)),
+                     dim3(256), 0, s, a);
+}
+
+moe_status_t check_rows(const char* name, const void* x, int64_t stride, int64_t rows, int64_t k) {
+  if (!x) return fail(MOE_ERR_INVALID_ARG, "%s must be non-NULL", name);
+  if ((uintptr_t)x & 15) return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (rows > 1 && (stride < k || stride % 16 || stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_ARG, "%s_stride %lld: %lld at least, a multiple of 16, at most %lld", name,
+                (long long)stride, (long long)k, (long long)kMaxStride);
+  return MOE_OK;
+}
+
+moe_status_t check_sizes(int32_t m, int32_t n, int32_t k) {
+  if (m < 0 || n <= 0 || k <= 0) return fail(MOE_ERR_INVALID_ARG, "m %d, n %d, k %d", m, n, k);
+  if (k % 16 || k > 65536 || n > 262144)
+    return fail(MOE_ERR_UNSUPPORTED, "k (%d) must be a multiple of 16, at most 65536; n (%d) at most 262144", k, n);
+  return MOE_OK;
+}
+moe_status_t check_ffn(int32_t m, int32_t hidden, int32_t inter) {
+  if (m < 0 || hidden <= 0 || inter <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "num_tokens %d, hidden %d, intermediate %d", m, hidden, inter);
+  if (hidden % 128 || inter % 128 || hidden > 65536 || inter > 65536)
+    return fail(MOE_ERR_UNSUPPORTED, "hidden (%d) and intermediate (%d) must be multiples of 128, at most 65536",
+                hidden, inter);
+  return MOE_OK;
+}
+
+// The shared expert's workspace: `first` bytes of float32 h, gate/up or parts,
+// then h's codes and scales.
+struct FfnLayout {
+  size_t first, codes, scales;
+  size_t total() const { return first + codes + scales; }
+};
+FfnLayout ffn_layout(int32_t m, int32_t hidden, int32_t inter) {
+  FfnLayout l{0, 0, 0};
+  if (m <= kFewQuant) {
+    l.first = pad256((size_t)m * inter * 4);
+    return l;
+  }
+  l.first = m <= kFewTokens ? pad256((size_t)m * 2 * inter * 4) : parts_bytes(m, 2 * inter, hidden / 128);
+  const size_t second = parts_bytes(m, hidden, inter / 128);
+  if (second > l.first) l.first = second;
+  l.codes = pad256((size_t)m * inter);
+  l.scales = pad256((size_t)m * (inter / 128) * 4);
+  return l;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_fp8_matmul_workspace_query(int32_t m, int32_t n, int32_t k, size_t* ws_bytes) {
+  moe::clear_error();
+  if (!ws_bytes) return moe::fail(MOE_ERR_INVALID_ARG, "ws_bytes is NULL");
+  const moe_status_t st = moe::check_sizes(m, n, k);
+  if (st != MOE_OK) return st;
+  *ws_bytes = m == 0 ? 0 : moe::parts_bytes(m, n, moe::cdiv(k, 128));
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_fp8_matmul(const uint8_t* x, int64_t x_stride, const float* x_scale, const uint8_t* w,
+                                       int64_t w_stride, const float* w_scale, int32_t m, int32_t n, int32_t k,
+                                       const void* add_bf16, int64_t add_stride, void* out_bf16, int64_t out_stride,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  clear_error();
+  moe_status_t st = check_sizes(m, n, k);
+  if (st != MOE_OK) return st;
+  if (m == 0) return MOE_OK;  // tensors of no rows have no address
+  if ((st = check_rows("x", x, x_stride, m, k)) != MOE_OK) return st;
+  if ((st = check_rows("w", w, w_stride, n, k)) != MOE_OK) return st;
+  if (!x_scale || !w_scale || (((uintptr_t)x_scale | (uintptr_t)w_scale) & 3))
+    return fail(MOE_ERR_INVALID_ARG, "x_scale and w_scale must be non-NULL and 4-byte aligned");
+  if ((st = check_out(m, n, add_bf16, add_stride, out_bf16, out_stride)) != MOE_OK) return st;
+  const int64_t out_bytes = span(m, out_stride, n, 2), kbs = cdiv(k, 128);
+  if (overlap(x, span(m, x_stride, k, 1), out_bf16, out_bytes) || overlap(w, span(n, w_stride, k, 1), out_bf16, out_bytes) ||
+      overlap(x_scale, m * kbs * 4, out_bf16, out_bytes) || overlap(w_scale, cdiv(n, 128) * kbs * 4, out_bf16, out_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+  if ((st = check_workspace(workspace, ws_bytes, parts_bytes(m, n, (int)kbs))) != MOE_OK) return st;
+  Args a = {};
+  a.l = x;
+  a.l_stride = m == 1 ? k : x_stride;
+  a.r = w;
+  a.r_stride = n == 1 ? k : w_stride;
+  a.ls = x_scale;
+  a.rs = w_scale;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.kbs = (int32_t)kbs;
+  set_out(a, add_bf16, add_stride, out_bf16, out_stride);
+  product(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
+  return launched("fp8 matmul");
+}
+
+extern "C" moe_status_t moe_ffn_fp8_workspace_query(int32_t num_tokens, int32_t hidden, int32_t intermediate,
+                                                    size_t* ws_bytes) {
+  moe::clear_error();
+  if (!ws_bytes) return moe::fail(MOE_ERR_INVALID_ARG, "ws_bytes is NULL");
+  const moe_status_t st = moe::check_ffn(num_tokens, hidden, intermediate);
+  if (st != MOE_OK) return st;
+  *ws_bytes = num_tokens == 0 ? 0 : moe::ffn_layout(num_tokens, hidden, intermediate).total();
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const float* x_scale, const uint8_t* w13,
+                                    const float* w13_scale, const uint8_t* w2, const float* w2_scale,
+                                    int32_t num_tokens, int32_t hidden, int32_t intermediate, const void* add_bf16,
+                                    int64_t add_stride, void* out_bf16, int64_t out_stride, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  using namespace moe;
+  clear_error();
+  const int32_t m = num_tokens;
+  moe_status_t st = check_ffn(m, hidden, intermediate);
+  if (st != MOE_OK) return st;
+  if (m == 0) return MOE_OK;
+  if ((st = check_rows("x", x, x_stride, m, hidden)) != MOE_OK) return st;
+  if ((st = check_rows("w13", w13, hidden, 2 * intermediate, hidden)) != MOE_OK) return st;
+  if ((st = check_rows("w2", w2, intermediate, hidden, intermediate)) != MOE_OK) return st;
+  if (!x_scale || !w13_scale || !w2_scale || (((uintptr_t)x_scale | (uintptr_t)w13_scale | (uintptr_t)w2_scale) & 3))
+    return fail(MOE_ERR_INVALID_ARG, "the scales must be non-NULL and 4-byte aligned");
+  if ((st = check_out(m, hidden, add_bf16, add_stride, out_bf16, out_stride)) != MOE_OK) return st;
+  const int64_t out_bytes = span(m, out_stride, hidden, 2), weights = (int64_t)hidden * intermediate;
+  if (overlap(x, span(m, x_stride, hidden, 1), out_bf16, out_bytes) || overlap(w13, 2 * weights, out_bf16, out_bytes) ||
+      overlap(w2, weights, out_bf16, out_bytes) || overlap(x_scale, (int64_t)m * (hidden / 128) * 4, out_bf16, out_bytes) ||
+      overlap(w13_scale, weights / 8192 * 4, out_bf16, out_bytes) ||
+      overlap(w2_scale, weights / 16384 * 4, out_bf16, out_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+  const FfnLayout lay = ffn_layout(m, hidden, intermediate);
+  if ((st = check_workspace(workspace, ws_bytes, lay.total())) != MOE_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* first = reinterpret_cast<float*>(ws);
+  Args a = {};
+  a.l = x;
+  a.l_stride = m == 1 ? hidden : x_stride;
+  a.r = w13;
+  a.r_stride = hidden;
+  a.ls = x_scale;
+  a.rs = w13_scale;
+  a.m = m;
+  a.n = intermediate;
+  a.k = hidden;
+  a.kbs = hidden / 128;
+  a.hq = ws + lay.first;
+  a.hs = reinterpret_cast<float*>(ws + lay.first + lay.codes);
+  Args b = a;  // the second product
+  b.l = a.hq;
+  b.l_stride = intermediate;
+  b.ls = a.hs;
+  b.r = w2;
+  b.r_stride = intermediate;
+  b.rs = w2_scale;
+  b.n = hidden;
+  b.k = intermediate;
+  b.kbs = intermediate / 128;
+  set_out(b, add_bf16, add_stride, out_bf16, out_stride);
+  if (m <= kFewQuant) {
+    a.outf = first;
+    launch_few<kCodes, 2, kSwigluF32>(a, s);
+    b.l = ws;
+    b.l_stride = (int64_t)intermediate * 4;
+    hipLaunchKernelGGL((few_kernel<kQuant, 2, 1, 2, 16, kOut>), dim3(cdiv(hidden, 32)), dim3(1024), 0, s, b);
+    return launched("shared expert");
+  }
+  const int splits = m <= kFewTokens ? 1 : splits_for(m, 2 * intermediate, a.kbs);
+  if (m <= kFewTokens || splits > 1) {
+    Args p = a;
+    p.n = 2 * intermediate;
+    p.outf = first;
+    p.vec = 1;
+    if (m <= kFewTokens)
+      launch_few<kCodes, 2, kPart>(p, s);
+    else
+      tile_parts(p, splits, first, s);
+    launch_join<kSwigluQ>(a, first, splits, 2 * intermediate, s);
+  } else {
+    a.m_tiles = cdiv(m, 64);
+    a.n_tiles = intermediate / 128;
+    a.kb_per_split = a.kbs;
+    hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 64, 256, kSwigluQ>),
+                       dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles)), dim3(256), 0, s, a);
+  }
+  product(b, first, s);
+  return launched("shared expert");
+}

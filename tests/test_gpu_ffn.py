@@ -1,0 +1,226 @@
+"""The BF16 gated feed-forward block and its gradients, against 64-bit
+arithmetic."""
+
+import pytest
+import torch
+
+from tests import dense_util as D
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_ffn_route_amd as pkg
+    return pkg
+
+
+SIZES = [(1, 8, 8), (1, 7168, 2048), (3, 72, 40), (16, 1000, 136), (17, 128, 64), (50, 520, 264), (64, 2048, 768),
+         (65, 8, 8), (65, 72, 200), (127, 136, 128), (301, 2040, 776), (640, 1024, 1096)]
+
+
+@pytest.mark.parametrize("t,h,i", SIZES)
+def test_forward_and_gradients(m, t, h, i):
+    x, w13, w2, dy = D.ffn_inputs(t, h, i, t + h + i)
+    want = D.ffn64(x, w13, w2, dy)
+    D.assert_within(m.gated_ffn(x, w13, w2), *want["y"], "y without gradients")
+    for v in (x, w13, w2):
+        v.requires_grad_(True)
+    y = m.gated_ffn(x, w13, w2)
+    dx, dw13, dw2 = torch.autograd.grad(y, (x, w13, w2), dy)
+    got = {"y": y.detach(), "dx": dx, "dw13": dw13, "dw2": dw2}
+    for name, g in got.items():
+        value, bound = want[name] if name in ("y", "dx") else D.rounded(*want[name])
+        assert g.dtype == torch.bfloat16
+        D.assert_within(g, value, bound, name)
+    # Two roundings count in each: of h (y, dw2) or dg | du (dx, dw13), and of the
+    # result.  Errors of half a step are at most 2^-8 / sqrt(3) each in the mean.
+    half = D.HALF_BF16 / 3 ** 0.5
+    if t * h * i > 10 ** 6:
+        for name in got:
+            assert D.rel_rms(got[name], want[name][0]) < 2 ** 0.5 * half, name
+
+
+@pytest.mark.parametrize("t,h,i", [(5, 72, 40), (130, 264, 136)])
+def test_float32_weight_gradients_and_accumulation(m, t, h, i):
+    x, w13, w2, dy = D.ffn_inputs(t, h, i, 9)
+    want = D.ffn64(x, w13, w2, dy)
+    y, gu, hid = m.gated_ffn_forward(x, w13, w2)
+    D.assert_within(y, *want["y"], "y")
+    dx = torch.empty_like(x)
+    dw13, dw2 = torch.empty(2 * i, h, device="cuda"), torch.empty(h, i, device="cuda")
+    m.gated_ffn_backward(dy, x, w13, w2, gu, hid, dx=dx, dw13=dw13, dw2=dw2)
+    D.assert_within(dx, *want["dx"], "dx")
+    D.assert_within(dw13, *want["dw13"], "dw13")
+    D.assert_within(dw2, *want["dw2"], "dw2")
+    a13, a2 = torch.ones_like(dw13), torch.full_like(dw2, 2.0)
+    m.gated_ffn_backward(dy, x, w13, w2, gu, hid, dw13=a13, dw2=a2, accumulate=True)
+    assert torch.equal(a13, dw13 + 1.0) and torch.equal(a2, dw2 + 2.0)
+
+
+def test_each_gradient_alone(m):
+    x, w13, w2, dy = D.ffn_inputs(90, 136, 72, 4)
+    leaves = [v.clone().requires_grad_(True) for v in (x, w13, w2)]
+    want = torch.autograd.grad(m.gated_ffn(*leaves), leaves, dy)
+    for k in range(3):
+        args = [x, w13, w2]
+        args[k] = args[k].clone().requires_grad_(True)
+        (got,) = torch.autograd.grad(m.gated_ffn(*args), (args[k],), dy)
+        assert torch.equal(got, want[k])
+
+
+def test_gradients_against_differences(m):
+    """Directional differences of the 64-bit forward, step 1e-5: their error is
+    1e-10 of third derivatives and 1e-16 / 1e-5 of the loss, far below the
+    roundings of the kernel's gradients, whose bounds are summed."""
+    t, h, i = 70, 72, 40
+    x, w13, w2, dy = D.ffn_inputs(t, h, i, 21)
+    want = D.ffn64(x, w13, w2, dy)
+    leaves = [v.clone().requires_grad_(True) for v in (x, w13, w2)]
+    grads = torch.autograd.grad(m.gated_ffn(*leaves), leaves, dy)
+
+    def loss(*p):
+        g, u = (p[0] @ p[1].T).split(i, 1)
+        return ((g * torch.sigmoid(g) * u) @ p[2].T * dy.double()).sum()
+
+    base = [v.double() for v in (x, w13, w2)]
+    for k, name in enumerate(("dx", "dw13", "dw2")):
+        step = torch.randn_like(base[k])
+        plus, minus = list(base), list(base)
+        plus[k], minus[k] = base[k] + 1e-5 * step, base[k] - 1e-5 * step
+        difference = (loss(*plus) - loss(*minus)) / 2e-5
+        bound = (D.rounded(*want[name])[1] * step.abs()).sum() + 1e-6 * difference.abs() + 1e-6
+        assert (grads[k].double() * step).sum().sub(difference).abs() <= bound, name
+
+
+def test_broadcast_and_strided_gradient_of_the_output(m):
+    x, w13, w2, _ = D.ffn_inputs(70, 72, 40, 6)
+    x.requires_grad_(True)
+    ones = torch.ones(70, 72, device="cuda").bfloat16()
+    (want,) = torch.autograd.grad(m.gated_ffn(x, w13, w2), (x,), ones)
+    (got,) = torch.autograd.grad(m.gated_ffn(x, w13, w2).sum(), (x,))  # dy has strides of zero
+    assert torch.equal(got, want)
+    (got,) = torch.autograd.grad(m.gated_ffn(x, w13, w2), (x,), ones.t().contiguous().t())
+    assert torch.equal(got, want)
+    wide = torch.ones(70, 80, device="cuda").bfloat16()
+    (got,) = torch.autograd.grad(m.gated_ffn(x, w13, w2), (x,), wide[:, 4:76])
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("t", [3, 100])
+def test_strided_rows(m, t):
+    x, w13, w2, dy = D.ffn_inputs(t, 72, 40, 7)
+    wide = torch.full((t, 96), float("nan"), device="cuda").bfloat16()
+    wide[:, 16:88] = x
+    view = wide[:, 16:88]
+    assert torch.equal(m.gated_ffn(view, w13, w2), m.gated_ffn(x, w13, w2))
+    out = torch.zeros(t, 104, device="cuda").bfloat16()
+    y, gu, h = m.gated_ffn_forward(view, w13, w2, out=out[:, 8:80])
+    assert torch.equal(out[:, 8:80], m.gated_ffn(x, w13, w2)) and not out[:, :8].any() and not out[:, 80:].any()
+    a, b = torch.empty_like(w13), torch.empty_like(w13)
+    m.gated_ffn_backward(dy, view, w13, w2, gu, h, dw13=a)
+    m.gated_ffn_backward(dy, x, w13, w2, gu, h, dw13=b)
+    assert torch.equal(a, b)
+
+
+def test_no_tokens(m):
+    x, w13, w2, dy = D.ffn_inputs(1, 72, 40, 8)
+    leaves = [x[:0].clone().requires_grad_(True), w13.requires_grad_(True), w2.requires_grad_(True)]
+    y = m.gated_ffn(*leaves)
+    assert y.shape == (0, 72)
+    dx, dw13, dw2 = torch.autograd.grad(y, leaves, dy[:0])
+    assert dx.shape == (0, 72) and not dw13.any() and not dw2.any()
+
+
+@pytest.mark.parametrize("t", [3, 80])
+def test_large_gates(m, t):
+    """silu and its slope at gates in the hundreds and thousands, both signs."""
+    x, w13, w2, dy = D.ffn_inputs(t, 72, 40, 14)
+    x = (x.float() * 400).bfloat16()
+    want = D.ffn64(x, w13, w2, dy)
+    leaves = [v.clone().requires_grad_(True) for v in (x, w13, w2)]
+    y = m.gated_ffn(*leaves)
+    got = dict(zip(("dx", "dw13", "dw2"), torch.autograd.grad(y, leaves, dy)), y=y.detach())
+    for name, g in got.items():
+        assert g.isfinite().all()
+        D.assert_within(g, *(want[name] if name in ("y", "dx") else D.rounded(*want[name])), name)
+
+
+@pytest.mark.parametrize("t", [3, 90])
+def test_nan_stays_in_its_row(m, t):
+    x, w13, w2, dy = D.ffn_inputs(t, 72, 40, 15)
+    y = m.gated_ffn(x, w13, w2)
+    x[1, 5] = float("nan")
+    got = m.gated_ffn(x, w13, w2)
+    assert got[1].isnan().all()
+    keep = torch.arange(t, device="cuda") != 1
+    assert torch.equal(got[keep], y[keep])
+
+
+@pytest.mark.parametrize("t", [20, 100])
+def test_captured_step(m, t):
+    x, w13, w2, dy = D.ffn_inputs(t, 264, 136, 16)
+    leaves = [v.requires_grad_(True) for v in (x, w13, w2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(m.gated_ffn(*leaves), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = m.gated_ffn(*leaves)
+        grads = torch.autograd.grad(y, leaves, dy)
+    y = y.detach()
+    for seed in range(3):
+        with torch.no_grad():
+            x.copy_(torch.randn(x.shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda"))
+        want_y = m.gated_ffn(*leaves)
+        want = torch.autograd.grad(want_y, leaves, dy)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y)
+        assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+@pytest.mark.parametrize("t", [20, 100])
+def test_captured_step_beside_an_eager_graph(m, t):
+    """Through autograd it is refused before anything is launched; the two calls
+    without autograd are captured, into graphs that share no memory."""
+    x, w13, w2, dy = D.ffn_inputs(t, 264, 136, 16)
+    leaves = [v.requires_grad_(True) for v in (x, w13, w2)]
+    eager = m.gated_ffn(*leaves)  # its graph stays alive over the capture
+    torch.cuda.synchronize()
+    refused = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="eager graph"):
+        with torch.cuda.graph(refused):
+            m.gated_ffn(*leaves)
+    graphs = []
+    with torch.no_grad():
+        for _ in range(2):
+            grads = [torch.empty_like(v) for v in leaves]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                y, gu, h = m.gated_ffn_forward(*leaves)
+                m.gated_ffn_backward(dy, *leaves, gu, h, dx=grads[0], dw13=grads[1], dw2=grads[2])
+            graphs.append((graph, y, grads))
+        want = torch.autograd.grad(eager, leaves, dy)
+        for _ in range(3):
+            for graph, y, grads in graphs:
+                graph.replay()
+            torch.cuda.synchronize()
+            for graph, y, grads in graphs:
+                assert torch.equal(y, eager)
+                assert all(torch.equal(a, b) for a, b in zip(grads, want))
+                y.zero_()
+                for v in grads:
+                    v.zero_()
+
+
+def test_in_place_change_of_a_saved_weight_is_refused(m):
+    x, w13, w2, dy = D.ffn_inputs(4, 72, 40, 17)
+    x.requires_grad_(True)
+    y = m.gated_ffn(x, w13, w2)
+    w13.add_(1.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward(dy)
