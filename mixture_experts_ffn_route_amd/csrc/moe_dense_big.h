@@ -1,0 +1,226 @@
+// BF16 products on 256 x 256 (256 x 128, 128 x 256) tiles.
+//
+// Four waves, one a SIMD, 2 (n) x 2 (m), each with a quarter of the tile in its
+// accumulators (128 x 128: 256 registers).  A wave that large reads an operand
+// value from LDS once for 128 results: 128 KB of reads and 64 KB of DMA a K-block
+// of 64, 1536 of LDS's cycles beside 2048 of the MFMA's; with eight waves of 64 x
+// 128 the reads alone would take 1536.
+//
+// With one wave a SIMD nothing but the wave itself hides a latency: the
+// fragments are double-buffered in registers (those of half a K-block, 32 k, are
+// read while the other half's MFMAs run), the K-blocks in LDS (two stages), and
+// reads and DMA are spread between the MFMAs.  One barrier a K-block, between
+// its halves: there every wave holds the second half's fragments, so the stage
+// can take the next K-block but one, and the next K-block has landed.
+//
+// Workgroups stay: a tile's last K-blocks already load the next tile's first.
+#pragma once
+
+#include <type_traits>
+
+#include "moe_dense_tile.h"
+
+namespace moe {
+namespace dense {
+
+// acc += r l^T in accumulation registers: with 256 of them the compiler, left to
+// choose, keeps some in the other half of the file and copies them to and fro.
+// What it does not know of an MFMA in asm: results are read only after the wait
+// behind the K loop, an accumulator is used again NB TB MFMAs later, and
+// operands come from LDS reads, for which it waits.
+__device__ __forceinline__ void mfma(v4f& acc, const v8bf& r, const v8bf& l) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(r), "v"(l));
+}
+
+// CUT: K is no multiple of 64.
+template <int LL, int LR, int BM, int BN, int EPI, bool CUT>
+__global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
+  constexpr bool kPair = EPI == kSwiglu;
+  constexpr int NB = BN / 32, TB = BM / 32, HN = BN / 2;
+  constexpr int NP = (BN + BM) / 32;
+  constexpr int STAGE = (BN + BM) * kLine;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
+  const int total = a.m_tiles * a.n_tiles, kbs = a.kbs;
+
+  // The tile whose loads are being issued: scalars only (a lane's offsets are
+  // computed again for each piece, three instructions beside the MFMAs, in place
+  // of a register each).
+  const uint8_t* base[3];
+  int rows[3];
+  auto setup = [&](int mt, int nt) {
+    const int m0 = mt * BM, n0 = nt * (kPair ? HN : BN);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int row = kPair ? n0 + h * a.n : n0 + h * HN, left = kPair ? a.n - n0 : a.n - n0 - h * HN;
+      if (left <= 0) {  // nothing there: half 0 again, not stored
+        row = n0;
+        left = a.n - n0;
+      }
+      base[h] = a.r + (LR == kKin ? row * a.r_stride : (int64_t)row * 2);
+      rows[h] = min(left, HN);
+    }
+    base[2] = a.l + (LL == kKin ? m0 * a.l_stride : (int64_t)m0 * 2);
+    rows[2] = min(a.m - m0, BM);
+  };
+  // Pieces 4 i + wave (see piece_offset): kKin rows 32 i + in_row, chunk in_c;
+  // kKout k = 32 (i % 2) + out_k, rows 64 (i / 2) + out_n.
+  const int in_row = 8 * wave + (lane >> 3), in_c = ((lane & 7) ^ swz(in_row & 15)) * 16;
+  const int out_k = 8 * (2 * (wave & 1) + ((lane >> 3) & 1)) + 4 * (wave >> 1) + ((lane >> 1) & 3);
+  const int out_n = 16 * (lane >> 4) + 8 * (lane & 1);
+  // Piece i of K-block kb into a stage; k_left: values of K from there on.
+  auto issue_piece = [&](int stage, int kb, int i) {
+    const lds_u8* to = (const lds_u8*)ring_lds + stage * STAGE + (i * 4 + wave) * 1024;
+    const bool is_r = i < BN / 32;
+    const int o = is_r ? (i < HN / 32 ? 0 : 1) : 2, j = i - (is_r ? o * (HN / 32) : BN / 32);
+    const int layout = is_r ? LR : LL;
+    const int64_t stride = is_r ? a.r_stride : a.l_stride;
+    const uint8_t* from = base[o] + (layout == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * stride);
+    const uint32_t off = layout == kKin
+                             ? __umul24(min(32 * j + in_row, rows[o] - 1), (uint32_t)stride) + in_c
+                             : __umul24(32 * (j & 1) + out_k, (uint32_t)stride) + 2 * min(64 * (j >> 1) + out_n, rows[o] - 8);
+    if constexpr (!CUT) {
+      dma16(from, off, to);
+    } else {
+      const int left = a.k - kb * 64;
+      const bool ok = layout == kKin ? in_c < 2 * left : 32 * (j & 1) + out_k < left;
+      dma16_at(ok ? from + off : (const uint8_t*)&kZeros, to);
+    }
+  };
+
+  v8bf rf[2][NB], lf[2][TB];
+  // fragment f (R's, then L's) of half s of the K-block in a stage
+  auto read = [&](int stage, int s, int f) {
+    const lds_u8* st = (const lds_u8*)ring_lds + stage * STAGE;
+    if (f < NB)
+      rf[s][f] = frag_bf16<LR>(st + (f < NB / 2 ? 0 : HN * kLine), wn * (NB / 2) + (f < NB / 2 ? f : f - NB / 2), s, lane);
+    else
+      lf[s][f - NB] = frag_bf16<LL>(st + BN * kLine, wm * TB + f - NB, s, lane);
+  };
+
+  // The K-block to load next is kb_in of tile v_in.  After the last tile its last
+  // K-block is loaded again, into stages that nothing reads.
+  const int ids = (total + 7) / 8 * 8;  // grid is a multiple of 8: a workgroup keeps its XCD
+  int mt = 0, nt = 0;
+  auto next = [&](int id) {  // the next tile from id on, in mt and nt
+    while (id < ids && !tile_of(id, a.m_tiles, a.n_tiles, 8, mt, nt)) id += gridDim.x;
+    return id;
+  };
+  int v = next(blockIdx.x), kb_in = 0;
+  if (v >= ids) return;
+  int v_in = v, mt_cur = mt, nt_cur = nt;
+  setup(mt, nt);
+  auto advance = [&]() {
+    if (++kb_in < kbs) return;
+    const int id = v_in < ids ? next(v_in + gridDim.x) : ids;
+    v_in = id;
+    kb_in = 0;
+    if (id < ids)
+      setup(mt, nt);
+    else
+      kb_in = kbs - 1;
+  };
+  int stage = 0;
+#pragma unroll
+  for (int pre = 0; pre < 2; ++pre) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) issue_piece(pre, kb_in, i);
+    advance();
+  }
+  wait_vm<0>();
+  barrier();
+#pragma unroll
+  for (int f = 0; f < NB + TB; ++f) read(0, 0, f);
+
+  while (true) {
+    v4f acc[NB][TB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    // written by VALU instructions, and next read by MFMAs that the compiler does not know
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) asm volatile("" : "+a"(acc[i][t]));
+    asm volatile("s_nop 7" ::: "memory");
+    constexpr int GROUPS = NB * TB / 4, READS = NB + TB;
+    // half s of a K-block: its MFMAs; the fragments of half s ^ 1 (of the next
+    // K-block if s is 1) from stage `from`; with s = 1 the loads of a K-block
+    // into stage `into`
+    auto half = [&](auto s_, int from, int into) {
+      constexpr int s = decltype(s_)::value;
+#pragma unroll
+      for (int q = 0; q < GROUPS; ++q) {
+#pragma unroll
+        for (int f = q * READS * 3 / 2 / GROUPS; f < (q + 1) * READS * 3 / 2 / GROUPS; ++f)
+          if (f < READS) read(from, s ^ 1, f);
+        if constexpr (s == 1) {
+#pragma unroll
+          for (int i = q * NP / GROUPS; i < (q + 1) * NP / GROUPS; ++i)
+            issue_piece(into, kb_in, i);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (q * 4 + e) % NB, t = (q * 4 + e) / NB;
+          mfma(acc[i][t], rf[s][i], lf[s][t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int kb = 0; kb < kbs; ++kb) {
+      half(std::integral_constant<int, 0>{}, stage, 0);
+      wait_lds();
+      wait_vm<0>();
+      barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      half(std::integral_constant<int, 1>{}, stage ^ 1, stage);
+      advance();
+      stage ^= 1;
+    }
+    // the MFMAs' results are there 18 wait states after the last
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) asm volatile("" : "+a"(acc[i][t]));
+
+    const int m0 = mt_cur * BM, n0 = nt_cur * (kPair ? HN : BN);
+    const int lm = m0 + wm * (BM / 2) + (lane & 15), lc = n0 + wn * (HN / 2) + 4 * (lane >> 4);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int64_t m = lm + t * 16;
+      if (m < a.m) {
+#pragma unroll
+        for (int i = 0; i < (kPair ? NB / 2 : NB); ++i) {
+          const int c = lc + (i < NB / 2 ? i * 16 : HN + (i - NB / 2) * 16);
+          if (c >= a.n) continue;
+          const v4f r = acc[i][t];
+          const float f[4] = {r[0], r[1], r[2], r[3]};
+          if constexpr (EPI == kOut) {
+            *reinterpret_cast<u32x2*>(a.out + m * a.out_stride + c) = pack4(f);
+          } else if constexpr (EPI == kOutF32) {
+            v4f* o = reinterpret_cast<v4f*>(a.outf + m * a.n + c);
+            *o = a.accumulate ? *o + r : r;
+          } else if constexpr (EPI == kSwiglu) {
+            const v4f w = acc[NB / 2 + i][t];
+            const float u[4] = {w[0], w[1], w[2], w[3]};
+            store_swiglu(a, m, c, f, u);
+          } else {
+            store_dswiglu(a, m, c, f);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    v = next(v + gridDim.x);
+    if (v >= ids) break;
+    mt_cur = mt;
+    nt_cur = nt;
+  }
+  wait_vm<0>();  // no load into LDS outlives the workgroup
+}
+
+}  // namespace dense
+}  // namespace moe

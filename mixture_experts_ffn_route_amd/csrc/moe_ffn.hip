@@ -12,6 +12,7 @@
 // place of 0.0024 of their root mean square, of which that rounding is 0.0017).
 #include <hip/hip_runtime.h>
 
+#include "moe_dense_big.h"
 #include "moe_dense_few.h"
 #include "moe_dense_host.h"
 #include "moe_dense_tile.h"
@@ -50,10 +51,25 @@ void launch_tile(Args a, int splits, hipStream_t s) {
                      dim3(256), 0, s, a);
 }
 
+template <int LL, int LR, int EPI, int BM, int BN>
+void launch_big(Args a, hipStream_t s) {
+  a.m_tiles = cdiv(a.m, BM);
+  a.n_tiles = cdiv(a.n, EPI == kSwiglu ? BN / 2 : BN);
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256);
+  if (a.k % 64 == 0)
+    hipLaunchKernelGGL((big_kernel<LL, LR, BM, BN, EPI, false>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((big_kernel<LL, LR, BM, BN, EPI, true>), grid, dim3(256), 0, s, a);
+}
+
+bool use_big(int64_t m, int64_t n) { return (int64_t)cdiv(m, 256) * cdiv(n, 256) >= 96; }
+
 // A product whose result has n columns, of L (K inside) and R, into EPI; with
 // SwiGLU h has half of the columns.
 template <int LR, int EPI>
 void product(Args a, int n, float* parts, hipStream_t s) {
+  if (use_big(a.m, n)) return launch_big<kKin, LR, EPI, 256, 256>(a, s);
   const int splits = splits_for(a.m, n, a.kbs);
   if (splits == 1) return launch_tile<kKin, LR, EPI>(a, 1, s);
   Args p = a;
@@ -261,10 +277,16 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
     if (dw_type == MOE_TYPE_F32) {
       a.outf = static_cast<float*>(dw);
       a.vec = 1;
-      launch_tile<kKout, kKout, kOutF32>(a, 1, s);
+      if (m > 0 && use_big(a.m, a.n))
+        launch_big<kKout, kKout, kOutF32, 256, 256>(a, s);
+      else
+        launch_tile<kKout, kKout, kOutF32>(a, 1, s);
     } else {
       set_out(a, nullptr, 0, dw, a.n);
-      launch_tile<kKout, kKout, kOut>(a, 1, s);
+      if (m > 0 && use_big(a.m, a.n))
+        launch_big<kKout, kKout, kOut, 256, 256>(a, s);
+      else
+        launch_tile<kKout, kKout, kOut>(a, 1, s);
     }
   }
   return launched("gated ffn backward");

@@ -16,7 +16,8 @@ def m():
 
 
 SIZES = [(1, 8, 8), (1, 7168, 2048), (3, 72, 40), (16, 1000, 136), (17, 128, 64), (50, 520, 264), (64, 2048, 768),
-         (65, 8, 8), (65, 72, 200), (127, 136, 128), (301, 2040, 776), (640, 1024, 1096)]
+         (65, 8, 8), (65, 72, 200), (127, 136, 128), (301, 2040, 776), (640, 1024, 1096),
+         (2341, 2312, 1288), (4200, 1032, 1800), (1000, 6400, 1992)]
 
 
 @pytest.mark.parametrize("t,h,i", SIZES)
