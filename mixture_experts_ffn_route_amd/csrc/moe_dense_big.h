@@ -65,9 +65,9 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
     rows[2] = min(a.m - m0, BM);
   };
   // Pieces 4 i + wave (see piece_offset): kKin rows 32 i + in_row, chunk in_c;
-  // kKout k = 32 (i % 2) + out_k, rows 64 (i / 2) + out_n.
+  // kKout k = 8 (i % 2) + out_k, rows 64 (i / 2) + out_n.
   const int in_row = 8 * wave + (lane >> 3), in_c = ((lane & 7) ^ swz(in_row & 15)) * 16;
-  const int out_k = 8 * (2 * (wave & 1) + ((lane >> 3) & 1)) + 4 * (wave >> 1) + ((lane >> 1) & 3);
+  const int out_k = 16 * (2 * (wave & 1) + ((lane >> 3) & 1)) + 4 * (wave >> 1) + ((lane >> 1) & 3);
   const int out_n = 16 * (lane >> 4) + 8 * (lane & 1);
   // Piece i of K-block kb into a stage; k_left: values of K from there on.
   auto issue_piece = [&](int stage, int kb, int i) {
@@ -79,12 +79,12 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
     const uint8_t* from = base[o] + (layout == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * stride);
     const uint32_t off = layout == kKin
                              ? __umul24(min(32 * j + in_row, rows[o] - 1), (uint32_t)stride) + in_c
-                             : __umul24(32 * (j & 1) + out_k, (uint32_t)stride) + 2 * min(64 * (j >> 1) + out_n, rows[o] - 8);
+                             : __umul24(8 * (j & 1) + out_k, (uint32_t)stride) + 2 * min(64 * (j >> 1) + out_n, rows[o] - 8);
     if constexpr (!CUT) {
       dma16(from, off, to);
     } else {
       const int left = a.k - kb * 64;
-      const bool ok = layout == kKin ? in_c < 2 * left : 32 * (j & 1) + out_k < left;
+      const bool ok = layout == kKin ? in_c < 2 * left : 8 * (j & 1) + out_k < left;
       dma16_at(ok ? from + off : (const uint8_t*)&kZeros, to);
     }
   };

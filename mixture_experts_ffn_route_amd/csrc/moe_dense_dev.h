@@ -8,14 +8,16 @@
 //
 // K inside (kKin): a row's K-block is 128 consecutive bytes.  In LDS chunk c (16
 // bytes) of row r sits at position 8 r + (c ^ swz(r)) of 16 bytes: one DMA
-// instruction fetches 8 whole lines, and every 16 lanes that read one chunk
-// number of 16 rows meet distinct banks.
+// instruction fetches 8 whole lines.  Lane l reads row l % 16, chunk 2 (l / 16) + s
+// for the halves s of the K-block: a 16-byte read is served in groups of lanes
+// like 0-3, 12-15, 20-23, 24-27, which then meet distinct banks (with chunk
+// 4 s + l / 16 they do not: 4 cycles more a read of 8).
 //
 // K outside (kKout, bfloat16): rows are consecutive in memory, one line of
 // memory a k.  LDS-transposing reads (ds_read_b64_tr_b16) turn it: 16 lanes
 // that read a 4 (k) x 16 (rows) block get a row's 4 values each.  Lane l of the
-// MFMA holds k = 32 s + 8 (l / 16) + [0, 8) of row l % 16, so one block is
-// k = 32 s + 8 g + 4 h + [0, 4), and the reads h of the four lane groups g
+// MFMA holds k = 16 (l / 16) + 8 s + [0, 8) of row l % 16, as above, so one block
+// is k = 16 g + 8 s + 4 h + [0, 4), and the reads h of the four lane groups g
 // together take 512 bytes.  DMA instruction (s, q, h, j) fetches the 8 lines
 // g = 2 j, 2 j + 1 of rows [64 q, 64 q + 64) and lays them down so that each of
 // its 4 blocks of 16 rows has 256 consecutive bytes.
@@ -100,7 +102,7 @@ __device__ __forceinline__ uint32_t piece_offset(const Operand& o, int p, int la
   } else {
     const int j = p & 1, h = (p >> 1) & 1, s = (p >> 2) & 1, q = p >> 3;
     const int b = lane >> 4, g = 2 * j + ((lane >> 3) & 1), r = (lane >> 1) & 3, c = lane & 1;
-    const int k = 32 * s + 8 * g + 4 * h + r, n = 64 * q + 16 * b + 8 * c;
+    const int k = 16 * g + 8 * s + 4 * h + r, n = 64 * q + 16 * b + 8 * c;
     return (uint32_t)k * (uint32_t)o.stride + (uint32_t)min(n, o.rows - 8) * 2u;
   }
 }
@@ -113,7 +115,7 @@ __device__ __forceinline__ bool piece_valid(int p, int lane, int k_valid) {
   } else {
     const int j = p & 1, h = (p >> 1) & 1, s = (p >> 2) & 1;
     const int g = 2 * j + ((lane >> 3) & 1), r = (lane >> 1) & 3;
-    return 32 * s + 8 * g + 4 * h + r < k_valid;
+    return 16 * g + 8 * s + 4 * h + r < k_valid;
   }
 }
 
@@ -124,11 +126,11 @@ __device__ __forceinline__ u32x4 lds16(const lds_u8* p) {
   return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(p);
 }
 
-// Fragment of 16 rows [16 b, 16 b + 16) of a bfloat16 tile, k = 32 s + 8 (l / 16) + [0, 8).
+// Fragment of 16 rows [16 b, 16 b + 16) of a bfloat16 tile, k = 16 (l / 16) + 8 s + [0, 8).
 template <int LAYOUT>
 __device__ __forceinline__ v8bf frag_bf16(const lds_u8* tile, int b, int s, int lane) {
   if constexpr (LAYOUT == kKin) {
-    return __builtin_bit_cast(v8bf, lds16(tile + b * 2048 + chunk_at(lane & 15, 4 * s + (lane >> 4))));
+    return __builtin_bit_cast(v8bf, lds16(tile + b * 2048 + chunk_at(lane & 15, 2 * (lane >> 4) + s)));
   } else {
     typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
     const lds_u8* p = tile + (b >> 2) * 8192 + s * 4096 + (b & 3) * 256 + (lane >> 5) * 1024 + ((lane >> 4) & 1) * 128 +
