@@ -20,6 +20,12 @@
 
 #include "moe_dense_tile.h"
 
+#ifndef MOE_RD
+#define MOE_RD 3
+#endif
+#ifndef MOE_FRONT
+#define MOE_FRONT 1
+#endif
 namespace moe {
 namespace dense {
 
@@ -37,20 +43,21 @@ template <int LL, int LR, int BM, int BN, int EPI, bool CUT>
 __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu;
   constexpr int NB = BN / 32, TB = BM / 32, HN = BN / 2;
-  constexpr int NP = (BN + BM) / 32;
-  constexpr int STAGE = (BN + BM) * kLine;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[2 * STAGE];
+  constexpr int NPR = BN / 32, NPL = BM / 32;               // DMA pieces per wave and K-block
+  constexpr int R_BYTES = BN * kLine, L_BYTES = BM * kLine;  // a K-block of each
+  __shared__ __attribute__((aligned(1024))) uint8_t r_lds[3 * R_BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t l_lds[2 * L_BYTES];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
   const int total = a.m_tiles * a.n_tiles, kbs = a.kbs;
 
-  // The tile whose loads are being issued: scalars only (a lane's offsets are
-  // computed again for each piece, three instructions beside the MFMAs, in place
-  // of a register each).
+  // The tiles whose loads are being issued, R's and L's: scalars only (a lane's
+  // offsets are computed again for each piece, three instructions beside the
+  // MFMAs, in place of a register each).
   const uint8_t* base[3];
   int rows[3];
-  auto setup = [&](int mt, int nt) {
-    const int m0 = mt * BM, n0 = nt * (kPair ? HN : BN);
+  auto setup_r = [&](int nt) {
+    const int n0 = nt * (kPair ? HN : BN);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       int row = kPair ? n0 + h * a.n : n0 + h * HN, left = kPair ? a.n - n0 : a.n - n0 - h * HN;
@@ -61,6 +68,9 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
       base[h] = a.r + (LR == kKin ? row * a.r_stride : (int64_t)row * 2);
       rows[h] = min(left, HN);
     }
+  };
+  auto setup_l = [&](int mt) {
+    const int m0 = mt * BM;
     base[2] = a.l + (LL == kKin ? m0 * a.l_stride : (int64_t)m0 * 2);
     rows[2] = min(a.m - m0, BM);
   };
@@ -69,11 +79,11 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   const int in_row = 8 * wave + (lane >> 3), in_c = ((lane & 7) ^ swz(in_row & 15)) * 16;
   const int out_k = 16 * (2 * (wave & 1) + ((lane >> 3) & 1)) + 4 * (wave >> 1) + ((lane >> 1) & 3);
   const int out_n = 16 * (lane >> 4) + 8 * (lane & 1);
-  // Piece i of K-block kb into a stage; k_left: values of K from there on.
-  auto issue_piece = [&](int stage, int kb, int i) {
-    const lds_u8* to = (const lds_u8*)ring_lds + stage * STAGE + (i * 4 + wave) * 1024;
-    const bool is_r = i < BN / 32;
-    const int o = is_r ? (i < HN / 32 ? 0 : 1) : 2, j = i - (is_r ? o * (HN / 32) : BN / 32);
+  // Piece i of K-block kb of R or L into a stage of its own.
+  auto issue_piece = [&](bool is_r, int stage, int kb, int i) {
+    const lds_u8* to = (is_r ? (const lds_u8*)r_lds + stage * R_BYTES : (const lds_u8*)l_lds + stage * L_BYTES) +
+                       (i * 4 + wave) * 1024;
+    const int o = is_r ? (i < HN / 32 ? 0 : 1) : 2, j = is_r ? i - o * (HN / 32) : i;
     const int layout = is_r ? LR : LL;
     const int64_t stride = is_r ? a.r_stride : a.l_stride;
     const uint8_t* from = base[o] + (layout == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * stride);
@@ -90,48 +100,59 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   };
 
   v8bf rf[2][NB], lf[2][TB];
-  // fragment f (R's, then L's) of half s of the K-block in a stage
-  auto read = [&](int stage, int s, int f) {
-    const lds_u8* st = (const lds_u8*)ring_lds + stage * STAGE;
+  // fragment f (R's, then L's) of half s of the K-block in these stages
+  auto read = [&](int sr, int sl, int s, int f) {
     if (f < NB)
-      rf[s][f] = frag_bf16<LR>(st + (f < NB / 2 ? 0 : HN * kLine), wn * (NB / 2) + (f < NB / 2 ? f : f - NB / 2), s, lane);
+      rf[s][f] = frag_bf16<LR>((const lds_u8*)r_lds + sr * R_BYTES + (f < NB / 2 ? 0 : HN * kLine),
+                               wn * (NB / 2) + (f < NB / 2 ? f : f - NB / 2), s, lane);
     else
-      lf[s][f - NB] = frag_bf16<LL>(st + BN * kLine, wm * TB + f - NB, s, lane);
+      lf[s][f - NB] = frag_bf16<LL>((const lds_u8*)l_lds + sl * L_BYTES, wm * TB + f - NB, s, lane);
   };
 
-  // The K-block to load next is kb_in of tile v_in.  After the last tile its last
-  // K-block is loaded again, into stages that nothing reads.
+  // The K-blocks to load next are r.kb of tile r.v and l.kb of l.v.  After the
+  // last tile its last K-block is loaded again, into stages that nothing reads.
   const int ids = (total + 7) / 8 * 8;  // grid is a multiple of 8: a workgroup keeps its XCD
   int mt = 0, nt = 0;
   auto next = [&](int id) {  // the next tile from id on, in mt and nt
     while (id < ids && !tile_of(id, a.m_tiles, a.n_tiles, 8, mt, nt)) id += gridDim.x;
     return id;
   };
-  int v = next(blockIdx.x), kb_in = 0;
-  if (v >= ids) return;
-  int v_in = v, mt_cur = mt, nt_cur = nt;
-  setup(mt, nt);
-  auto advance = [&]() {
-    if (++kb_in < kbs) return;
-    const int id = v_in < ids ? next(v_in + gridDim.x) : ids;
-    v_in = id;
-    kb_in = 0;
-    if (id < ids)
-      setup(mt, nt);
-    else
-      kb_in = kbs - 1;
+  struct Cursor {
+    int v, kb;
   };
-  int stage = 0;
+  int v = next(blockIdx.x);
+  if (v >= ids) return;
+  int mt_cur = mt, nt_cur = nt;
+  setup_r(nt);
+  setup_l(mt);
+  Cursor cr{v, 0}, cl{v, 0};
+  auto advance = [&](Cursor& c) {  // true: another tile, in mt and nt
+    if (++c.kb < kbs) return false;
+    if (c.v < ids) c.v = next(c.v + gridDim.x);
+    c.kb = c.v < ids ? 0 : kbs - 1;
+    return c.v < ids;
+  };
+  auto advance_r = [&]() {
+    if (advance(cr)) setup_r(nt);
+  };
+  auto advance_l = [&]() {
+    if (advance(cl)) setup_l(mt);
+  };
 #pragma unroll
   for (int pre = 0; pre < 2; ++pre) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) issue_piece(pre, kb_in, i);
-    advance();
+    for (int i = 0; i < NPR; ++i) issue_piece(true, pre, cr.kb, i);
+    advance_r();
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) issue_piece(false, pre, cl.kb, i);
+    advance_l();
   }
+  int sr = 0, sl = 0;  // stages of the K-block at hand
+  auto after = [](int stage, int n) { return stage + n >= 3 ? stage + n - 3 : stage + n; };
   wait_vm<0>();
   barrier();
 #pragma unroll
-  for (int f = 0; f < NB + TB; ++f) read(0, 0, f);
+  for (int f = 0; f < NB + TB; ++f) read(0, 0, 0, f);
 
   while (true) {
     v4f acc[NB][TB];
@@ -147,20 +168,18 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
     asm volatile("s_nop 7" ::: "memory");
     constexpr int GROUPS = NB * TB / 4, READS = NB + TB;
     // half s of a K-block: its MFMAs; the fragments of half s ^ 1 (of the next
-    // K-block if s is 1) from stage `from`; with s = 1 the loads of a K-block
-    // into stage `into`
-    auto half = [&](auto s_, int from, int into) {
-      constexpr int s = decltype(s_)::value;
+    // K-block if s is 1) from stages fr and fl; the loads of R (s = 0) or L into
+    // a stage
+    auto half = [&](auto s_, int fr, int fl, int into) {
+      constexpr int s = decltype(s_)::value, NP = s == 0 ? NPR : NPL;
 #pragma unroll
       for (int q = 0; q < GROUPS; ++q) {
 #pragma unroll
-        for (int f = q * READS * 3 / 2 / GROUPS; f < (q + 1) * READS * 3 / 2 / GROUPS; ++f)
-          if (f < READS) read(from, s ^ 1, f);
-        if constexpr (s == 1) {
+        for (int f = q * READS * MOE_RD / 2 / GROUPS; f < (q + 1) * READS * MOE_RD / 2 / GROUPS; ++f)
+          if (f < READS) read(fr, fl, s ^ 1, f);
 #pragma unroll
-          for (int i = q * NP / GROUPS; i < (q + 1) * NP / GROUPS; ++i)
-            issue_piece(into, kb_in, i);
-        }
+        for (int i = q * NP * MOE_FRONT / GROUPS; i < (q + 1) * NP * MOE_FRONT / GROUPS; ++i)
+          if (i < NP) issue_piece(s == 0, into, s == 0 ? cr.kb : cl.kb, i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (q * 4 + e) % NB, t = (q * 4 + e) / NB;
@@ -170,14 +189,16 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
       }
     };
     for (int kb = 0; kb < kbs; ++kb) {
-      half(std::integral_constant<int, 0>{}, stage, 0);
+      half(std::integral_constant<int, 0>{}, sr, sl, after(sr, 2));
+      advance_r();
       wait_lds();
-      wait_vm<0>();
+      wait_vm<NPR>();  // all but the pieces just issued: the next K-block is there
       barrier();
       __builtin_amdgcn_sched_barrier(0);
-      half(std::integral_constant<int, 1>{}, stage ^ 1, stage);
-      advance();
-      stage ^= 1;
+      half(std::integral_constant<int, 1>{}, after(sr, 1), sl ^ 1, sl);
+      advance_l();
+      sr = after(sr, 1);
+      sl ^= 1;
     }
     // the MFMAs' results are there 18 wait states after the last
     asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
