@@ -61,6 +61,10 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, const lds_
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(off), "s"(uniform_ptr(base)), "s"(lds_addr(to)) : "memory", "m0");
 }
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, const lds_u8* to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(off), "s"(uniform_ptr(base)), "s"(lds_addr(to)) : "memory", "m0");
+}
 // from a per-lane address
 __device__ __forceinline__ void dma16_at(const void* src, const lds_u8* to) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"

@@ -6,6 +6,7 @@
 //   hs = max|h| / 448 and e4m3 codes, out = the product of those with w2
 #include <hip/hip_runtime.h>
 
+#include "moe_dense_big8.h"
 #include "moe_dense_few.h"
 #include "moe_dense_host.h"
 #include "moe_dense_tile.h"
@@ -47,8 +48,28 @@ void tile_parts(Args a, int splits, float* parts, hipStream_t s) {
                      dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles), splits), dim3(256), 0, s, a);
 }
 
+bool use_big(int64_t m, int64_t n) { return (int64_t)cdiv(m, 256) * cdiv(n, 256) >= 96; }
+
+template <int EPI>
+void launch_big(Args a, hipStream_t s) {
+  a.m_tiles = cdiv(a.m, 256);
+  a.n_tiles = cdiv(a.n, EPI == kSwigluQ ? 128 : 256);
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256), block(512);
+  const bool cut = a.k % 128 != 0, vec = EPI == kSwigluQ || (a.vec && a.n % 4 == 0);
+  if (EPI == kSwigluQ || (!cut && vec))
+    hipLaunchKernelGGL((big8_kernel<EPI, false, true>), grid, block, 0, s, a);
+  else if (vec)
+    hipLaunchKernelGGL((big8_kernel<kOut, true, true>), grid, block, 0, s, a);
+  else if (cut)
+    hipLaunchKernelGGL((big8_kernel<kOut, true, false>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((big8_kernel<kOut, false, false>), grid, block, 0, s, a);
+}
+
 void product(Args a, float* parts, hipStream_t s) {
   if (a.m <= kFewTokens) return launch_few<kCodes, 2, kOut>(a, s);
+  if (use_big(a.m, a.n)) return launch_big<kOut>(a, s);
   const int splits = splits_for(a.m, a.n, a.kbs);
   if (splits > 1) {
     tile_parts(a, splits, parts, s);
@@ -233,6 +254,8 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
     else
       tile_parts(p, splits, first, s);
     launch_join<kSwigluQ>(a, first, splits, 2 * intermediate, s);
+  } else if (use_big(m, 2 * (int64_t)intermediate)) {
+    launch_big<kSwigluQ>(a, s);
   } else {
     a.m_tiles = cdiv(m, 64);
     a.n_tiles = intermediate / 128;

@@ -17,7 +17,8 @@ def m():
 
 SIZES = [(1, 1, 16), (1, 7168, 2048), (5, 130, 144), (16, 1003, 2000), (17, 64, 128), (33, 257, 1040), (64, 512, 4096),
          (65, 1, 16), (65, 130, 144), (100, 1003, 2000), (128, 128, 128), (129, 640, 7168), (300, 257, 400),
-         (513, 1027, 2064), (1100, 2304, 640)]
+         (513, 1027, 2064), (1100, 2304, 640),
+         (2500, 2500, 400), (2341, 2563, 1040), (3000, 2304, 128), (4100, 1541, 256)]
 
 
 @pytest.mark.parametrize("rows,n,k", SIZES)
@@ -30,7 +31,7 @@ def test_product(m, rows, n, k, with_add):
     D.assert_within(got, want, bound, f"{rows}x{n}x{k}")
 
 
-@pytest.mark.parametrize("rows", [3, 40, 200])
+@pytest.mark.parametrize("rows", [3, 40, 200, 13000])
 def test_strided_rows_and_output_over_add(m, rows):
     n, k = 260, 272
     x, xs, w, ws = D.fp8_inputs(rows, n, k, rows)
@@ -50,7 +51,7 @@ def test_strided_rows_and_output_over_add(m, rows):
     assert torch.equal(left, wide)  # nothing beside the rows was written
 
 
-@pytest.mark.parametrize("rows", [2, 30, 150])
+@pytest.mark.parametrize("rows", [2, 30, 150, 13000])
 def test_scales_of_far_apart_blocks(m, rows):
     n, k = 300, 1024
     x, xs, w, ws = D.fp8_inputs(rows, n, k, 11)
@@ -63,7 +64,7 @@ def test_scales_of_far_apart_blocks(m, rows):
     assert not got[0].any()
 
 
-@pytest.mark.parametrize("rows", [3, 40, 130, 700])
+@pytest.mark.parametrize("rows", [3, 40, 130, 700, 13000])
 def test_nan_stays_in_its_row_and_column(m, rows):
     n, k = 384, 400
     x, xs, w, ws = D.fp8_inputs(rows, n, k, 12)
@@ -93,7 +94,7 @@ def test_no_rows(m):
     assert m.fp8_matmul(x[:0], xs[:0], w, ws).shape == (0, 64)
 
 
-@pytest.mark.parametrize("rows,n,k", [(40, 512, 512), (90, 700, 2048), (520, 512, 256)])
+@pytest.mark.parametrize("rows,n,k", [(40, 512, 512), (90, 700, 2048), (520, 512, 256), (4096, 2048, 1024)])
 def test_repeats_give_the_same_bits(m, rows, n, k):
     x, xs, w, ws = D.fp8_inputs(rows, n, k, 3)
     first = m.fp8_matmul(x, xs, w, ws)
@@ -102,7 +103,8 @@ def test_repeats_give_the_same_bits(m, rows, n, k):
 
 
 SHARED = [(1, 256, 128), (1, 7168, 2048), (16, 1280, 640), (17, 512, 384), (48, 2048, 768), (64, 256, 128),
-          (65, 256, 128), (77, 2048, 768), (301, 1152, 896), (1200, 512, 1024)]
+          (65, 256, 128), (77, 2048, 768), (301, 1152, 896), (1200, 512, 1024),
+          (2341, 2560, 1280), (700, 7168, 8192 - 128)]
 
 
 @pytest.mark.parametrize("t,h,i", SHARED)
@@ -122,7 +124,7 @@ def test_shared_expert(m, t, h, i, with_add):
         assert torch.equal(shared.forward(x, xs, add=add, out=add), got)
 
 
-@pytest.mark.parametrize("t", [2, 30, 70, 1100])
+@pytest.mark.parametrize("t", [2, 30, 70, 1100, 12500])
 def test_shared_expert_rows_that_are_not_finite(m, t):
     h, i = 512, 256
     x, xs, w13, s13 = D.fp8_inputs(t, 2 * i, h, 1)
