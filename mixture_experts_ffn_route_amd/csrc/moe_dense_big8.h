@@ -20,11 +20,6 @@
 namespace moe {
 namespace dense {
 
-// A float that no wave writes, through the scalar cache.
-__device__ __forceinline__ float scalar_f32(const float* p) {
-  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
-}
-
 // CUT: K is no multiple of 128.  VEC: four columns are stored at once (kOut).
 template <int EPI, bool CUT, bool VEC>
 __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {

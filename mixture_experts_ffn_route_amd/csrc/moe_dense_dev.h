@@ -61,6 +61,11 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, const lds_
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(off), "s"(uniform_ptr(base)), "s"(lds_addr(to)) : "memory", "m0");
 }
+// the same of lines that are read once
+__device__ __forceinline__ void dma16_nt(const void* base, uint32_t off, const lds_u8* to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+               :: "v"(off), "s"(uniform_ptr(base)), "s"(lds_addr(to)) : "memory", "m0");
+}
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, const lds_u8* to) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :: "v"(off), "s"(uniform_ptr(base)), "s"(lds_addr(to)) : "memory", "m0");
@@ -77,6 +82,12 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// A float at a wave-uniform address that no wave writes, through the scalar cache
+// (and so not counted among the loads in flight).
+__device__ __forceinline__ float scalar_f32(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)uniform_ptr(p);
+}
 
 // 16 bytes of zeros that lanes past the end of K read instead
 __device__ const u32x4 kZeros = {0, 0, 0, 0};

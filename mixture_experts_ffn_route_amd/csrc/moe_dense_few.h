@@ -1,15 +1,19 @@
 // Dense products for a few tokens, where the weights' bytes are what counts: a
-// workgroup takes 16 RB rows of R and all of L, its waves take the K-blocks in
-// turn and hold both operands in registers, straight from memory (no LDS: no
-// two waves share a weight), and their sums are joined through LDS.
-//
-// e4m3 products are made on the BF16 MFMA, whose operands hold every code and
-// whose sums keep float32: these sizes wait for memory, and the wider product
-// costs nothing.
+// workgroup takes 16 RB rows of R and up to 64 of L, its waves take the K-blocks in
+// turn, each through a ring of its own in LDS, filled by DMA (no two waves share a
+// weight, so they never wait for each other), and their sums are joined through
+// LDS.
 #pragma once
 
 #include "moe_dense_tile.h"
 
+#ifndef MOE_NARROW
+#define MOE_NARROW 200
+#endif
+#ifndef MOE_W1
+#define MOE_W1 8
+#define MOE_D1 2
+#endif
 namespace moe {
 namespace dense {
 
@@ -25,28 +29,9 @@ __device__ __forceinline__ v8bf widen_fp8(uint32_t lo, uint32_t hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One lane's 32 bytes of a K-block: [at, at + 32) bytes of a row, whose last 16
-// are read again past its end (trim makes those zeros).  Weights, which one
-// workgroup reads once, are loaded non-temporally.
 struct Line {
   u32x4 c[2];
 };
-template <bool NT>
-__device__ __forceinline__ Line load_line(const uint8_t* row, int at, int bytes) {
-  Line v;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(row + min(at + 16 * i, bytes - 16));
-    v.c[i] = NT ? __builtin_nontemporal_load(p) : *p;
-  }
-  return v;
-}
-__device__ __forceinline__ void trim(Line& v, int at, int bytes) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (at + 16 * i >= bytes) v.c[i] = u32x4{0, 0, 0, 0};
-}
-
 // e4m3 codes and scale of 32 float32 values of a row, the other 96 of whose block
 // the lanes l ^ 16, l ^ 32 and l ^ 48 hold.
 __device__ __forceinline__ Line quant_line(const float* row, float& scale) {
@@ -70,109 +55,199 @@ __device__ __forceinline__ Line quant_line(const float* row, float& scale) {
   return r;
 }
 
-// U: K-blocks in flight per wave.
-template <int L, int RB, int MT, int U, int WAVES, int EPI>
+// RB: blocks of 16 rows of R (SwiGLU: 2, gate rows and up rows, or 1, 8 of each);
+// MT: blocks of 16 rows of L, blockIdx.y the part of L.  DEPTH: K-blocks in a
+// wave's own ring in LDS.
+//
+// With one block of L rows an e4m3 product is made on the BF16 MFMA, whose
+// operands hold every code and whose sums keep float32: the conversions are
+// nothing beside the weights' bytes.  With more it is made on the FP8 MFMA.
+template <int L, int RB, int MT, int WAVES, int DEPTH, int EPI>
 __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
-  constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluF32, kFp8 = L != kBf16;
-  static_assert(!kPair || RB == 2, "gate and up rows");
-  __shared__ __attribute__((aligned(16))) v4f part[WAVES][RB][MT][64];
+  constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluF32, kFp8 = L != kBf16, kHalves = kPair && RB == 1;
+  static_assert(!kPair || RB <= 2, "gate and up rows");
+  constexpr int COLS = kHalves ? 8 : kPair ? 16 : 16 * RB;  // of the result, per workgroup
+  constexpr int LT = L == kQuant ? 0 : MT;                  // blocks of L in a slot
+  constexpr int SLOT = (RB + LT) * 2048 + (L == kCodes ? 256 : 0);
+  constexpr int LOADS = 2 * (RB + LT) + (L == kCodes ? 1 : 0);
+  constexpr int RING = WAVES * DEPTH * SLOT, PART = WAVES * RB * MT * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[RING > PART ? RING : PART];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g = lane >> 4, n0 = blockIdx.x * (kPair ? 16 : 16 * RB);
+  const int g = lane >> 4, n0 = blockIdx.x * COLS, m0 = blockIdx.y * 16 * MT;
   const int bytes = a.k * (kFp8 ? 1 : 2);
-  const uint8_t* rp[RB];
-  const float* sw[RB];
+  lds_u8* ring = (lds_u8*)lds + wave * DEPTH * SLOT;
+
+  // DMA instruction h of a block fetches 8 rows; this lane's row and chunk
+  const int dr = lane >> 3;
+  uint32_t roff[RB][2], loff[LT ? LT : 1][2], soff = 0;
+  auto chunk = [&](int h) { return ((lane & 7) ^ swz(8 * h + dr)) * 16; };
+  // row r of the workgroup's block b of R
+  auto r_row = [&](int b, int r) {
+    return kHalves ? min(n0 + (r & 7), a.n - 1) + (r >> 3) * a.n
+                   : kPair ? min(n0 + r, a.n - 1) + b * a.n : min(n0 + 16 * b + r, a.n - 1);
+  };
+  const uint8_t* rbase[RB][2];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int first = r_row(b, 8 * h);  // wave-uniform
+      rbase[b][h] = a.r + first * a.r_stride;
+      roff[b][h] = __umul24(r_row(b, 8 * h + dr) - first, (uint32_t)a.r_stride) + chunk(h);
+    }
+  const uint8_t* lbase = a.l + m0 * a.l_stride;
+  const int rows = min(a.m - m0, 16 * MT);
+#pragma unroll
+  for (int t = 0; t < LT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      loff[t][h] = __umul24(min(16 * t + 8 * h + dr, rows - 1), (uint32_t)a.l_stride) + chunk(h);
+  if constexpr (L == kCodes) soff = __umul24(min(lane, rows - 1), (uint32_t)a.kbs) * 4u;
+  const bool once = gridDim.y == 1;  // no other workgroup reads these weights
+  auto issue = [&](int kb, int slot) {
+    lds_u8* to = ring + slot * SLOT;
+    const int64_t at = (int64_t)kb * kLine;
+    if ((kb + 1) * kLine <= bytes) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (once)
+            dma16_nt(rbase[b][h] + at, roff[b][h], to + b * 2048 + h * 1024);
+          else
+            dma16(rbase[b][h] + at, roff[b][h], to + b * 2048 + h * 1024);
+        }
+#pragma unroll
+      for (int t = 0; t < LT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dma16(lbase + at, loff[t][h], to + (RB + t) * 2048 + h * 1024);
+    } else {  // the last K-block, cut: zeros beyond K
+      auto from = [&](const uint8_t* base, uint32_t off, int h) {
+        return chunk(h) < bytes - kb * kLine ? base + at + off : (const uint8_t*)&kZeros;
+      };
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dma16_at(from(rbase[b][h], roff[b][h], h), to + b * 2048 + h * 1024);
+#pragma unroll
+      for (int t = 0; t < LT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dma16_at(from(lbase, loff[t][h], h), to + (RB + t) * 2048 + h * 1024);
+    }
+    if constexpr (L == kCodes) dma4(a.ls + (int64_t)m0 * a.kbs + kb, soff, to + (RB + LT) * 2048);
+  };
+
+  // The weight scales of each block of R, which lies in one scale block (kHalves:
+  // rows 0-7 and 8-15 in two; a lane's results are rows 4 g and up).
+  const float *sw[RB], *sw_up = nullptr;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
-    const int row = kPair ? min(n0 + (lane & 15), a.n - 1) + b * a.n : min(n0 + 16 * b + (lane & 15), a.n - 1);
-    rp[b] = a.r + row * a.r_stride;
-    // a block of 16 rows lies in one scale block
     const int first = kPair ? n0 + b * a.n : min(n0 + 16 * b, a.n - 1);
-    if constexpr (kFp8) sw[b] = a.rs + (int64_t)(first / 128) * a.kbs;
+    sw[b] = kFp8 ? a.rs + (int64_t)(first / 128) * a.kbs : nullptr;
   }
-  const uint8_t* lp[MT];
-  const float* sx[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = min(t * 16 + (lane & 15), a.m - 1);
-    lp[t] = a.l + m * a.l_stride;
-    if constexpr (L == kCodes) sx[t] = a.ls + (int64_t)m * a.kbs;
-  }
+  if constexpr (kFp8 && kHalves) sw_up = a.rs + (int64_t)((n0 + a.n) / 128) * a.kbs;
   v4f acc[RB][MT];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[b][t] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  for (int kb = wave; kb < a.kbs; kb += WAVES * U) {
-    Line w[U][RB], x[U][MT];
-    float fw[U][RB], fx[U][MT];
+  const int count = wave < a.kbs ? (a.kbs - wave + WAVES - 1) / WAVES : 0;  // this wave's K-blocks
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = kb + u * WAVES, at = k * kLine + 32 * g;
-      if (u > 0 && k >= a.kbs) break;  // wave-uniform
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        w[u][b] = load_line<true>(rp[b], at, bytes);
-        if constexpr (kFp8) fw[u][b] = sw[b][k];
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if constexpr (L != kQuant) x[u][t] = load_line<false>(lp[t], at, bytes);
-        if constexpr (L == kCodes) fx[u][t] = sx[t][k];
-      }
+  for (int i = 0; i < DEPTH; ++i)
+    if (i < count) issue(wave + i * WAVES, i);
+  int slot = 0;
+  for (int i = 0; i < count; ++i) {
+    const int kb = wave + i * WAVES;
+    Line xq;
+    float xs = 0.f;
+    if constexpr (L == kQuant) {
+      const int m = min(m0 + (lane & 15), a.m - 1);
+      xq = quant_line(reinterpret_cast<const float*>(a.l + m * a.l_stride) + kb * kLine + 32 * g, xs);
     }
+    if (i + DEPTH <= count)
+      wait_vm<LOADS * (DEPTH - 1)>();
+    else
+      wait_vm<0>();
+    const lds_u8* st = ring + slot * SLOT;
+    if constexpr (kFp8) {
+      float fw[RB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = kb + u * WAVES;
-      if (u > 0 && k >= a.kbs) break;
-      if ((k + 1) * kLine > bytes) {  // the last K-block, cut
-#pragma unroll
-        for (int b = 0; b < RB; ++b) trim(w[u][b], k * kLine + 32 * g, bytes);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) trim(x[u][t], k * kLine + 32 * g, bytes);
+      for (int b = 0; b < RB; ++b) fw[b] = scalar_f32(sw[b] + kb);
+      if constexpr (kHalves) {
+        const float up = scalar_f32(sw_up + kb);
+        fw[0] = g >= 2 ? up : fw[0];
       }
+      v8i w[RB];
+#pragma unroll
+      for (int b = 0; b < RB; ++b) w[b] = frag_fp8(st, b, lane);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        if constexpr (L == kQuant)
-          x[u][t] = quant_line(reinterpret_cast<const float*>(lp[t]) + k * kLine + 32 * g, fx[u][t]);
+        v8i x;
+        float fx;
+        if constexpr (L == kQuant) {
+          x = __builtin_bit_cast(v8i, xq);
+          fx = xs;
+        } else {
+          x = frag_fp8(st, RB + t, lane);
+          fx = ((const __attribute__((address_space(3))) float*)(st + (RB + LT) * 2048))[16 * t + (lane & 15)];
+        }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          if constexpr (kFp8) {
-            v4f p = {0.f, 0.f, 0.f, 0.f};
+          v4f p = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (MT == 1) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  widen_fp8(w[u][b].c[s >> 1][2 * (s & 1)], w[u][b].c[s >> 1][2 * (s & 1) + 1]),
-                  widen_fp8(x[u][t].c[s >> 1][2 * (s & 1)], x[u][t].c[s >> 1][2 * (s & 1) + 1]), p, 0, 0, 0);
-            const float f = fw[u][b] * fx[u][t];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(p[e], f, acc[b][t][e]);
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_fp8((uint32_t)w[b][2 * s], (uint32_t)w[b][2 * s + 1]),
+                                                          widen_fp8((uint32_t)x[2 * s], (uint32_t)x[2 * s + 1]), p, 0, 0, 0);
           } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(v8bf, w[u][b].c[s]), __builtin_bit_cast(v8bf, x[u][t].c[s]), acc[b][t], 0, 0, 0);
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[b], x, p, 0, 0, 0, 0, 0, 0);
           }
+          const float f = fw[b] * fx;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(p[e], f, acc[b][t][e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        v8bf w[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) w[b] = frag_bf16<kKin>(st, b, s, lane);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const v8bf x = frag_bf16<kKin>(st, RB + t, s, lane);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[b], x, acc[b][t], 0, 0, 0);
         }
       }
     }
+    if (i + DEPTH < count) {
+      wait_lds();  // the slot has been read
+      issue(kb + DEPTH * WAVES, slot);
+    }
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
   }
+  __syncthreads();  // every ring has been read
+  typedef __attribute__((address_space(3))) v4f lds_v4f;
+  lds_v4f* part = (lds_v4f*)lds;  // [WAVES][RB][MT][64]
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) part[wave][b][t][lane] = acc[b][t];
+    for (int t = 0; t < MT; ++t) part[((wave * RB + b) * MT + t) * 64 + lane] = acc[b][t];
   __syncthreads();
-  constexpr int kJobs = (kPair ? 1 : RB) * MT;  // blocks of 16 x 16 results, one wave each
+  constexpr int kJobs = (kPair ? 1 : RB) * MT;  // blocks of 16 x 16 results (kHalves: 8 x 16), one wave each
   for (int job = wave; job < kJobs; job += WAVES) {
     const int b = job / MT, t = job % MT;
-    const int m = t * 16 + (lane & 15), c = n0 + 16 * b + 4 * g;
-    if (m >= a.m || c >= a.n) continue;
+    const int m = m0 + t * 16 + (lane & 15), c = n0 + 16 * b + 4 * g;
+    if (m >= a.m || c >= a.n || (kHalves && g >= 2)) continue;
     float v[kPair ? 2 : 1][4] = {};
 #pragma unroll
     for (int h = 0; h < (kPair ? 2 : 1); ++h)
+#pragma unroll
       for (int w = 0; w < WAVES; ++w) {
-        const v4f p = part[w][kPair ? h : b][t][lane];
+        const v4f p = part[((w * RB + (kHalves ? 0 : kPair ? h : b)) * MT + t) * 64 + (kHalves ? lane + 32 * h : lane)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[h][e] += p[e];
       }
@@ -189,6 +264,27 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
       store_f32(a.outf + (int64_t)m * a.n + c, c, a.n, 1, false, h);
     }
   }
+}
+
+template <int L, int EPI, int RB, int MT, int WAVES, int DEPTH>
+void launch_few_as(const Args& a, hipStream_t s) {
+  constexpr int cols = EPI == kSwiglu || EPI == kSwigluF32 ? 8 * RB : 16 * RB;
+  hipLaunchKernelGGL((few_kernel<L, RB, MT, WAVES, DEPTH, EPI>),
+                     dim3((a.n + cols - 1) / cols, (a.m + 16 * MT - 1) / (16 * MT)), dim3(WAVES * 64), 0, s, a);
+}
+// MAX_MT 1: one block of L rows only (a.m <= 16).
+template <int L, int EPI, int MAX_MT = 4>
+void launch_few(const Args& a, hipStream_t s) {
+  const int blocks = (a.m + 15) / 16, parts = (blocks + 3) / 4, mt = (blocks + parts - 1) / parts;
+  // 16 columns a workgroup, 8 with SwiGLU, where twice as many would leave CUs idle
+  const int wide = EPI == kSwiglu || EPI == kSwigluF32 ? 16 : 32;
+  const bool narrow = (int64_t)((a.n + wide - 1) / wide) * parts < MOE_NARROW;
+  if constexpr (MAX_MT > 1) {
+    if (mt == 2) return narrow ? launch_few_as<L, EPI, 1, 2, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 2, 8, 2>(a, s);
+    if (mt == 3) return narrow ? launch_few_as<L, EPI, 1, 3, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 3, 4, 3>(a, s);
+    if (mt == 4) return narrow ? launch_few_as<L, EPI, 1, 4, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 4, 4, 3>(a, s);
+  }
+  return narrow ? launch_few_as<L, EPI, 1, 1, MOE_W1, MOE_D1>(a, s) : launch_few_as<L, EPI, 2, 1, MOE_W1, MOE_D1>(a, s);
 }
 
 }  // namespace dense

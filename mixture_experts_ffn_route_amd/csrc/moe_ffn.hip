@@ -23,25 +23,16 @@ namespace {
 
 using namespace dense;
 
-constexpr int kFewTokens = 64;  // up to here the few-token form
+#ifndef MOE_FEW_MAX
+#define MOE_FEW_MAX 64
+#endif
+constexpr int kFewTokens = MOE_FEW_MAX;  // up to here the few-token form
 
 size_t parts_bytes(int m, int n, int kbs) {
   const int s = splits_for(m, n, kbs);
   return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
 }
 
-template <int EPI>
-void launch_few(const Args& a, hipStream_t s) {
-  const dim3 grid(cdiv(a.n, EPI == kSwiglu ? 16 : 32));
-  if (a.m <= 16)
-    hipLaunchKernelGGL((few_kernel<kBf16, 2, 1, 2, 16, EPI>), grid, dim3(1024), 0, s, a);
-  else if (a.m <= 32)
-    hipLaunchKernelGGL((few_kernel<kBf16, 2, 2, 2, 8, EPI>), grid, dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((few_kernel<kBf16, 2, 4, 2, 8, EPI>), grid, dim3(512), 0, s, a);
-}
-
-// n: columns of the product (SwiGLU: of h).
 template <int LL, int LR, int EPI>
 void launch_tile(Args a, int splits, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
@@ -187,8 +178,8 @@ extern "C" moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const v
   b.kbs = cdiv(intermediate, 64);
   set_out(b, nullptr, 0, out, out_stride);
   if (m <= kFewTokens) {
-    launch_few<kSwiglu>(a, s);
-    launch_few<kOut>(b, s);
+    launch_few<kBf16, kSwiglu>(a, s);
+    launch_few<kBf16, kOut>(b, s);
   } else {
     float* parts = static_cast<float*>(workspace);
     product<kKin, kSwiglu>(a, 2 * intermediate, parts, s);

@@ -17,24 +17,16 @@ namespace {
 
 using namespace dense;
 
-constexpr int kFewTokens = 64;  // up to here the few-token form
+#ifndef MOE_FEW_MAX
+#define MOE_FEW_MAX 64
+#endif
+constexpr int kFewTokens = MOE_FEW_MAX;  // up to here the few-token form
 constexpr int kFewQuant = 16;   // up to here the shared expert's second product quantises h as it reads it
 
 size_t parts_bytes(int m, int n, int kbs) {
   if (m <= kFewTokens) return 0;
   const int s = splits_for(m, n, kbs);
   return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
-}
-
-template <int L, int RB, int EPI>
-void launch_few(const Args& a, hipStream_t s) {
-  const dim3 grid(cdiv(a.n, EPI == kSwigluF32 ? 16 : 16 * RB));
-  if (a.m <= 16)
-    hipLaunchKernelGGL((few_kernel<L, RB, 1, 2, 16, EPI>), grid, dim3(1024), 0, s, a);
-  else if (a.m <= 32)
-    hipLaunchKernelGGL((few_kernel<L, RB, 2, 2, 8, EPI>), grid, dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((few_kernel<L, RB, 4, 2, 8, EPI>), grid, dim3(512), 0, s, a);
 }
 
 // One product of e4m3 rows, n columns, into `parts` where K is split.
@@ -68,7 +60,7 @@ void launch_big(Args a, hipStream_t s) {
 }
 
 void product(Args a, float* parts, hipStream_t s) {
-  if (a.m <= kFewTokens) return launch_few<kCodes, 2, kOut>(a, s);
+  if (a.m <= kFewTokens) return launch_few<kCodes, kOut>(a, s);
   if (use_big(a.m, a.n)) return launch_big<kOut>(a, s);
   const int splits = splits_for(a.m, a.n, a.kbs);
   if (splits > 1) {
@@ -237,10 +229,10 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
   set_out(b, add_bf16, add_stride, out_bf16, out_stride);
   if (m <= kFewQuant) {
     a.outf = first;
-    launch_few<kCodes, 2, kSwigluF32>(a, s);
+    launch_few<kCodes, kSwigluF32, 1>(a, s);
     b.l = ws;
     b.l_stride = (int64_t)intermediate * 4;
-    hipLaunchKernelGGL((few_kernel<kQuant, 2, 1, 2, 16, kOut>), dim3(cdiv(hidden, 32)), dim3(1024), 0, s, b);
+    launch_few<kQuant, kOut, 1>(b, s);
     return launched("shared expert");
   }
   const int splits = m <= kFewTokens ? 1 : splits_for(m, 2 * intermediate, a.kbs);
@@ -250,7 +242,7 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
     p.outf = first;
     p.vec = 1;
     if (m <= kFewTokens)
-      launch_few<kCodes, 2, kPart>(p, s);
+      launch_few<kCodes, kPart>(p, s);
     else
       tile_parts(p, splits, first, s);
     launch_join<kSwigluQ>(a, first, splits, 2 * intermediate, s);

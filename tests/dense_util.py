@@ -8,7 +8,7 @@ MFMA (rows beyond 64) 2^-10 of its K-block's largest possible product."""
 import torch
 
 HALF_BF16 = 2.0 ** -8
-FEW = 64  # rows up to which e4m3 products are made on the BF16 MFMA
+FEW = 16  # rows up to which e4m3 products are made on the BF16 MFMA
 
 
 def blocks(n):
