@@ -18,10 +18,27 @@ inline size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 inline int splits_for(int m, int n, int kbs) {
   const int64_t tiles = (int64_t)cdiv(m, 128) * cdiv(n, 128);
   if (tiles >= 256) return 1;
-  int s = (int)(512 / tiles);
+#ifndef MOE_SLOTS
+#define MOE_SLOTS 256
+#endif
+  int s = (int)(MOE_SLOTS / tiles);
   if (s > kbs / 4) s = kbs / 4;
   if (s > 16) s = 16;
   return s < 2 ? 1 : cdiv(kbs, cdiv(kbs, s));
+}
+
+// `a` has its tiles.  One workgroup a CU: four stages; more: two.
+template <bool FP8, int LL, int LR, int BM, int BN, int EPI>
+void launch_tile(const Args& a, int splits, hipStream_t s) {
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  const dim3 grid(tile_grid(tiles), splits);
+  if constexpr (BM + BN <= 256) {  // (four stages of larger tiles do not fit)
+    if (tiles * splits <= 256) {
+      hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4>), grid, dim3(256), 0, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <int EPI>

@@ -1,9 +1,9 @@
 // Dense products on 128 x 128 (or 64 x 256) tiles: the simple form, for mid-size
 // batches, and the sums of products split over K.
 //
-// Four waves, 2 (n) x 2 (m); a K-block of 128 bytes is one stage of a ring of
-// two, and two workgroups share a CU, so that one's loads run beside the
-// other's MFMAs.
+// Four waves, 2 (n) x 2 (m); a K-block of 128 bytes is one stage of a ring, of
+// four where a CU has one workgroup, of two where it has two, whose loads then
+// run beside the other's MFMAs.
 #pragma once
 
 #include "moe_dense_dev.h"
@@ -107,15 +107,15 @@ __device__ __forceinline__ void store_dswiglu(const Args& a, int64_t m, int c, c
   *reinterpret_cast<u32x2*>(o + a.n) = pack4(du);
 }
 
-template <bool FP8, int LL, int LR, int BM, int BN, int EPI>
-__global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
+template <bool FP8, int LL, int LR, int BM, int BN, int EPI, int STAGES>
+__global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
   static_assert(!FP8 || (LL == kKin && LR == kKin), "e4m3 has no transposing read here");
   constexpr int NB = BN / 32, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
   constexpr int NP = (BN + BM) / 32;                      // DMA pieces per wave and K-block
-  constexpr int STAGE = (BN + BM) * kLine;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[2 * STAGE];
-  __shared__ uint32_t top_s[EPI == kSwigluQ ? 2 * BM : 1];
+  constexpr int STAGE = (BN + BM) * kLine + (FP8 ? BM * 4 : 0);
+  constexpr int LOADS = NP + (FP8 ? 1 : 0);
+  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[STAGES * STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
   int mt, nt;
@@ -148,8 +148,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
     else
       off[i] = piece_offset<LL>(op[2], p - BN / 8, lane);
   }
+  const uint32_t sx_off = FP8 ? __umul24(min(wave * 64 % BM + lane, op[2].rows - 1), (uint32_t)a.kbs) * 4u : 0;
   auto issue = [&](int kb) {
-    const lds_u8* st = (const lds_u8*)ring_lds + (kb & 1) * STAGE;
+    const lds_u8* st = (const lds_u8*)ring_lds + (kb - kb0) % STAGES * STAGE;
+    if constexpr (FP8)  // the rows' scales (waves 2 and 3 load what 0 and 1 do)
+      dma4(a.ls + (int64_t)m0 * a.kbs + kb, sx_off, st + (BN + BM) * kLine + wave * 64 % BM * 4);
     const int64_t radv = LR == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.r_stride;
     const int64_t ladv = LL == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.l_stride;
     const int kleft = a.k - kb * (kLine / ES);  // values of K from here on
@@ -172,27 +175,14 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
     }
   };
 
-  // e4m3: scales of this lane's tokens and of the two halves' weight blocks
-  const float* sx_p[TB];
-  const float* sw_p[2];
-  float sx[TB], sw[2];
+  // e4m3: scales of the two halves' weight blocks
+  const float* sw_p[2] = {nullptr, nullptr};
   if constexpr (FP8) {
-#pragma unroll
-    for (int t = 0; t < TB; ++t)
-      sx_p[t] = a.ls + (int64_t)min(m0 + wm * (BM / 2) + t * 16 + (lane & 15), a.m - 1) * a.kbs;
     const int blocks = ((kPair ? 2 * a.n : a.n) + 127) / 128;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       sw_p[h] = a.rs + (int64_t)min((kPair ? n0 + h * a.n : n0 + h * HN) / 128, blocks - 1) * a.kbs;
   }
-  auto scales = [&](int kb) {
-    if constexpr (FP8) {
-#pragma unroll
-      for (int t = 0; t < TB; ++t) sx[t] = sx_p[t][kb];
-      sw[0] = sw_p[0][kb];
-      sw[1] = sw_p[1][kb];
-    }
-  };
 
   v4f acc[NB][TB];
 #pragma unroll
@@ -203,57 +193,66 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
   auto r_tile = [&](const lds_u8* st, int i) { return st + (i < NB / 2 ? 0 : HN * kLine); };
   auto r_block = [&](int i) { return wn * (NB / 2) + (i < NB / 2 ? i : i - NB / 2); };
 
-  if (kb0 < kb1) {  // (no tokens: no K-block)
-    scales(kb0);
-    issue(kb0);
-  }
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i)
+    if (kb0 + i < kb1) issue(kb0 + i);  // (no tokens: no K-block)
   for (int kb = kb0; kb < kb1; ++kb) {
-    wait_vm<0>();
+    if (kb + STAGES - 2 < kb1)
+      wait_vm<LOADS * (STAGES - 2)>();
+    else
+      wait_vm<0>();
     wait_lds();
     barrier();
-    const lds_u8* st = (const lds_u8*)ring_lds + (kb & 1) * STAGE;
+    const lds_u8* st = (const lds_u8*)ring_lds + (kb - kb0) % STAGES * STAGE;
     const lds_u8* lt = st + BN * kLine;
-    float f0[TB], f1[TB];
     if constexpr (FP8) {
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        f0[t] = sx[t] * sw[0];
-        f1[t] = sx[t] * sw[1];
-      }
-    }
-    if (kb + 1 < kb1) {
-      scales(kb + 1);
-      issue(kb + 1);
-    }
-    if constexpr (FP8) {
-      v8i rf[NB];
+      const float sw0 = scalar_f32(sw_p[0] + kb), sw1 = scalar_f32(sw_p[1] + kb);
+      const __attribute__((address_space(3))) float* sx =
+          (const __attribute__((address_space(3))) float*)(lt + BM * kLine) + wm * (BM / 2) + (lane & 15);
+      // every fragment at once: the loads are issued while they come
+      v8i rf[NB], lf[TB];
+      float s[TB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) rf[i] = frag_fp8(r_tile(st, i), r_block(i), lane);
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        const v8i lf = frag_fp8(lt, wm * TB + t, lane);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rf[i], lf, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
-                                                                         127, 0, 127);
-          const float f = i < NB / 2 ? f0[t] : f1[t];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(p[e], f, acc[i][t][e]);
-        }
+        lf[t] = frag_fp8(lt, wm * TB + t, lane);
+        s[t] = sx[t * 16];
       }
+      if (kb + STAGES - 1 < kb1) issue(kb + STAGES - 1);
+      // the multiply-adds run two MFMAs behind
+      v4f p[4];
+      auto add = [&](int q) {
+        const int t = q / NB, i = q % NB;
+        const float f = s[t] * (i < NB / 2 ? sw0 : sw1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(p[q & 3][e], f, acc[i][t][e]);
+      };
+#pragma unroll
+      for (int q = 0; q < NB * TB; ++q) {
+        p[q & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rf[q % NB], lf[q / NB], v4f{0.f, 0.f, 0.f, 0.f}, 0,
+                                                                    0, 0, 0, 0, 0);
+        if (q >= 2) add(q - 2);
+      }
+      add(NB * TB - 2);
+      add(NB * TB - 1);
     } else {
+      v8bf rf[2][NB], lf[2][TB];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        v8bf rf[NB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) rf[i] = frag_bf16<LR>(r_tile(st, i), r_block(i), s, lane);
+        for (int i = 0; i < NB; ++i) rf[s][i] = frag_bf16<LR>(r_tile(st, i), r_block(i), s, lane);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          const v8bf lf = frag_bf16<LL>(lt, wm * TB + t, s, lane);
-#pragma unroll
-          for (int i = 0; i < NB; ++i) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rf[i], lf, acc[i][t], 0, 0, 0);
-        }
+        for (int t = 0; t < TB; ++t) lf[s][t] = frag_bf16<LL>(lt, wm * TB + t, s, lane);
       }
+      if (kb + STAGES - 1 < kb1) issue(kb + STAGES - 1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rf[s][i], lf[s][t], acc[i][t], 0, 0, 0);
     }
   }
 
@@ -261,6 +260,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Args a) {
   const int lc = 4 * (lane >> 4);
   if constexpr (EPI == kSwigluQ) {
     static_assert(EPI != kSwigluQ || HN == 128, "one scale block of h per tile");
+    __syncthreads();  // the ring has been read
+    __attribute__((address_space(3))) uint32_t* top_s = (__attribute__((address_space(3))) uint32_t*)ring_lds;
     float h[NB / 2][TB][4];
 #pragma unroll
     for (int t = 0; t < TB; ++t) {

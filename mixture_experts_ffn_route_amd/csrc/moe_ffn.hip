@@ -34,12 +34,11 @@ size_t parts_bytes(int m, int n, int kbs) {
 }
 
 template <int LL, int LR, int EPI>
-void launch_tile(Args a, int splits, hipStream_t s) {
+void tile(Args a, int splits, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, EPI == kSwiglu ? 64 : 128);
   a.kb_per_split = splits > 1 ? cdiv(a.kbs, splits) : a.kbs;
-  hipLaunchKernelGGL((tile_kernel<false, LL, LR, 128, 128, EPI>), dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles), splits),
-                     dim3(256), 0, s, a);
+  launch_tile<false, LL, LR, 128, 128, EPI>(a, splits, s);
 }
 
 template <int LL, int LR, int EPI, int BM, int BN>
@@ -62,12 +61,12 @@ template <int LR, int EPI>
 void product(Args a, int n, float* parts, hipStream_t s) {
   if (use_big(a.m, n)) return launch_big<kKin, LR, EPI, 256, 256>(a, s);
   const int splits = splits_for(a.m, n, a.kbs);
-  if (splits == 1) return launch_tile<kKin, LR, EPI>(a, 1, s);
+  if (splits == 1) return tile<kKin, LR, EPI>(a, 1, s);
   Args p = a;
   p.n = n;
   p.outf = parts;
   p.vec = 1;
-  launch_tile<kKin, LR, kPart>(p, splits, s);
+  tile<kKin, LR, kPart>(p, splits, s);
   launch_join<EPI>(a, parts, splits, n, s);
 }
 
@@ -271,13 +270,13 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
       if (m > 0 && use_big(a.m, a.n))
         launch_big<kKout, kKout, kOutF32, 256, 256>(a, s);
       else
-        launch_tile<kKout, kKout, kOutF32>(a, 1, s);
+        tile<kKout, kKout, kOutF32>(a, 1, s);
     } else {
       set_out(a, nullptr, 0, dw, a.n);
       if (m > 0 && use_big(a.m, a.n))
         launch_big<kKout, kKout, kOut, 256, 256>(a, s);
       else
-        launch_tile<kKout, kKout, kOut>(a, 1, s);
+        tile<kKout, kKout, kOut>(a, 1, s);
     }
   }
   return launched("gated ffn backward");

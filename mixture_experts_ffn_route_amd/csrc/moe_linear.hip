@@ -36,8 +36,7 @@ void tile_parts(Args a, int splits, float* parts, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, 128);
   a.kb_per_split = cdiv(a.kbs, splits);
-  hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 128, 128, kPart>),
-                     dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles), splits), dim3(256), 0, s, a);
+  launch_tile<true, kKin, kKin, 128, 128, kPart>(a, splits, s);
 }
 
 bool use_big(int64_t m, int64_t n) { return (int64_t)cdiv(m, 256) * cdiv(n, 256) >= 96; }
@@ -70,8 +69,7 @@ void product(Args a, float* parts, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, 128);
   a.kb_per_split = a.kbs;
-  hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 128, 128, kOut>), dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles)),
-                     dim3(256), 0, s, a);
+  launch_tile<true, kKin, kKin, 128, 128, kOut>(a, 1, s);
 }
 
 moe_status_t check_rows(const char* name, const void* x, int64_t stride, int64_t rows, int64_t k) {
@@ -252,8 +250,7 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
     a.m_tiles = cdiv(m, 64);
     a.n_tiles = intermediate / 128;
     a.kb_per_split = a.kbs;
-    hipLaunchKernelGGL((tile_kernel<true, kKin, kKin, 64, 256, kSwigluQ>),
-                       dim3(tile_grid((int64_t)a.m_tiles * a.n_tiles)), dim3(256), 0, s, a);
+    launch_tile<true, kKin, kKin, 64, 256, kSwigluQ>(a, 1, s);
   }
   product(b, first, s);
   return launched("shared expert");
