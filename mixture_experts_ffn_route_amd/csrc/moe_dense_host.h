@@ -7,6 +7,10 @@
 #include "moe_dense_tile.h"
 #include "moe_internal.h"
 
+#ifndef MOE_WN
+#define MOE_WN 4
+#define MOE_WN2 4
+#endif
 namespace moe {
 namespace dense {
 
@@ -32,13 +36,12 @@ template <bool FP8, int LL, int LR, int BM, int BN, int EPI>
 void launch_tile(const Args& a, int splits, hipStream_t s) {
   const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
   const dim3 grid(tile_grid(tiles), splits);
-  if constexpr (BM + BN <= 256) {  // (four stages of larger tiles do not fit)
-    if (tiles * splits <= 256) {
-      hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4>), grid, dim3(256), 0, s, a);
-      return;
-    }
-  }
-  hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 2>), grid, dim3(256), 0, s, a);
+  if constexpr (BM + BN > 256)  // one workgroup a CU in any case
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 3, MOE_WN2>), grid, dim3(MOE_WN2 * 128), 0, s, a);
+  else if (tiles * splits <= 256)
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4, MOE_WN>), grid, dim3(MOE_WN * 128), 0, s, a);
+  else
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <int EPI>

@@ -1,7 +1,7 @@
 // Dense products on 128 x 128 (or 64 x 256) tiles: the simple form, for mid-size
 // batches, and the sums of products split over K.
 //
-// Four waves, 2 (n) x 2 (m); a K-block of 128 bytes is one stage of a ring, of
+// WN (n) x 2 (m) waves; a K-block of 128 bytes is one stage of a ring, of
 // four where a CU has one workgroup, of two where it has two, whose loads then
 // run beside the other's MFMAs.
 #pragma once
@@ -107,17 +107,17 @@ __device__ __forceinline__ void store_dswiglu(const Args& a, int64_t m, int c, c
   *reinterpret_cast<u32x2*>(o + a.n) = pack4(du);
 }
 
-template <bool FP8, int LL, int LR, int BM, int BN, int EPI, int STAGES>
-__global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) {
+template <bool FP8, int LL, int LR, int BM, int BN, int EPI, int STAGES, int WN>
+__global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
   static_assert(!FP8 || (LL == kKin && LR == kKin), "e4m3 has no transposing read here");
-  constexpr int NB = BN / 32, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
-  constexpr int NP = (BN + BM) / 32;                      // DMA pieces per wave and K-block
+  constexpr int WAVES = 2 * WN, NB = BN / 16 / WN, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
+  constexpr int NP = (BN + BM) / 8 / WAVES, NPR = BN / 8 / WAVES;  // DMA pieces per wave and K-block, of R
   constexpr int STAGE = (BN + BM) * kLine + (FP8 ? BM * 4 : 0);
   constexpr int LOADS = NP + (FP8 ? 1 : 0);
   __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[STAGES * STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
   int mt, nt;
   if (!tile_of(blockIdx.x, a.m_tiles, a.n_tiles, 8, mt, nt)) return;
   const int m0 = mt * BM, n0 = nt * (kPair ? HN : BN);
@@ -140,10 +140,10 @@ __global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) 
   uint32_t off[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const int p = i * 4 + wave;
-    if (i < HN / 32)
+    const int p = i * WAVES + wave;
+    if (i < NPR / 2)
       off[i] = piece_offset<LR>(op[0], p, lane);
-    else if (i < BN / 32)
+    else if (i < NPR)
       off[i] = piece_offset<LR>(op[1], p - HN / 8, lane);
     else
       off[i] = piece_offset<LL>(op[2], p - BN / 8, lane);
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) 
   const uint32_t sx_off = FP8 ? __umul24(min(wave * 64 % BM + lane, op[2].rows - 1), (uint32_t)a.kbs) * 4u : 0;
   auto issue = [&](int kb) {
     const lds_u8* st = (const lds_u8*)ring_lds + (kb - kb0) % STAGES * STAGE;
-    if constexpr (FP8)  // the rows' scales (waves 2 and 3 load what 0 and 1 do)
+    if constexpr (FP8)  // the rows' scales (the waves behind the first load them again)
       dma4(a.ls + (int64_t)m0 * a.kbs + kb, sx_off, st + (BN + BM) * kLine + wave * 64 % BM * 4);
     const int64_t radv = LR == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.r_stride;
     const int64_t ladv = LL == kKin ? (int64_t)kb * kLine : (int64_t)kb * 64 * a.l_stride;
@@ -159,18 +159,18 @@ __global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) 
     if (kleft >= kLine / ES) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const bool is_r = i < BN / 32;
-        dma16(is_r ? op[i < HN / 32 ? 0 : 1].base + radv : op[2].base + ladv, off[i], st + (i * 4 + wave) * 1024);
+        const bool is_r = i < NPR;
+        dma16(is_r ? op[i < NPR / 2 ? 0 : 1].base + radv : op[2].base + ladv, off[i], st + (i * WAVES + wave) * 1024);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const bool is_r = i < BN / 32;
-        const int p = i * 4 + wave - (is_r ? (i < HN / 32 ? 0 : HN / 8) : BN / 8);
-        const uint8_t* src = (is_r ? op[i < HN / 32 ? 0 : 1].base + radv : op[2].base + ladv) + off[i];
+        const bool is_r = i < NPR;
+        const int p = i * WAVES + wave - (is_r ? (i < NPR / 2 ? 0 : HN / 8) : BN / 8);
+        const uint8_t* src = (is_r ? op[i < NPR / 2 ? 0 : 1].base + radv : op[2].base + ladv) + off[i];
         const bool ok = is_r ? piece_valid<LR>(p, lane, LR == kKin ? kleft * ES : kleft)
                              : piece_valid<LL>(p, lane, LL == kKin ? kleft * ES : kleft);
-        dma16_at(ok ? src : (const uint8_t*)&kZeros, st + (i * 4 + wave) * 1024);
+        dma16_at(ok ? src : (const uint8_t*)&kZeros, st + (i * WAVES + wave) * 1024);
       }
     }
   };
@@ -282,11 +282,14 @@ __global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) 
     for (int t = 0; t < TB; ++t) {
       const int r = wm * (BM / 2) + t * 16 + (lane & 15), m = m0 + r;
       if (m >= a.m) continue;
-      const float s = __uint_as_float(max(top_s[r], top_s[BM + r])) / kE4m3Max;
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) top = max(top, top_s[w * BM + r]);
+      const float s = __uint_as_float(top) / kE4m3Max;
       if (wn == 0 && lane < 16) a.hs[(int64_t)m * (a.n / 128) + nt] = s;
 #pragma unroll
       for (int i = 0; i < NB / 2; ++i)
-        *reinterpret_cast<uint32_t*>(a.hq + (int64_t)m * a.n + n0 + wn * (HN / 2) + i * 16 + lc) = quant4(h[i][t], s);
+        *reinterpret_cast<uint32_t*>(a.hq + (int64_t)m * a.n + n0 + wn * (HN / WN) + i * 16 + lc) = quant4(h[i][t], s);
     }
   } else {
 #pragma unroll
