@@ -1,4 +1,4 @@
-// BF16 products on 256 x 256 (256 x 128, 128 x 256) tiles.
+// BF16 products on tiles of 256 rows of R and BM (256, 128) of L.
 //
 // Four waves, one a SIMD, 2 (n) x 2 (m), each with a quarter of the tile in its
 // accumulators (128 x 128: 256 registers).  A wave that large reads an operand
@@ -20,12 +20,6 @@
 
 #include "moe_dense_tile.h"
 
-#ifndef MOE_RD
-#define MOE_RD 3
-#endif
-#ifndef MOE_FRONT
-#define MOE_FRONT 1
-#endif
 namespace moe {
 namespace dense {
 
@@ -38,7 +32,7 @@ __device__ __forceinline__ void mfma(v4f& acc, const v8bf& r, const v8bf& l) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(r), "v"(l));
 }
 
-// CUT: K is no multiple of 64.
+// CUT: K is no multiple of 64.  blockIdx.y: the part of K (kPart).
 template <int LL, int LR, int BM, int BN, int EPI, bool CUT>
 __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu;
@@ -46,10 +40,12 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   constexpr int NPR = BN / 32, NPL = BM / 32;               // DMA pieces per wave and K-block
   constexpr int R_BYTES = BN * kLine, L_BYTES = BM * kLine;  // a K-block of each
   __shared__ __attribute__((aligned(1024))) uint8_t r_lds[3 * R_BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t l_lds[2 * L_BYTES];
+  constexpr int LST = BM == 256 ? 2 : 3;                     // stages of L
+  __shared__ __attribute__((aligned(1024))) uint8_t l_lds[LST * L_BYTES];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
-  const int total = a.m_tiles * a.n_tiles, kbs = a.kbs;
+  const int total = a.m_tiles * a.n_tiles;
+  const int kb0 = blockIdx.y * a.kb_per_split, kbs = min(a.kb_per_split, a.kbs - kb0);
 
   // The tiles whose loads are being issued, R's and L's: scalars only (a lane's
   // offsets are computed again for each piece, three instructions beside the
@@ -80,7 +76,8 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
   const int out_k = 16 * (2 * (wave & 1) + ((lane >> 3) & 1)) + 4 * (wave >> 1) + ((lane >> 1) & 3);
   const int out_n = 16 * (lane >> 4) + 8 * (lane & 1);
   // Piece i of K-block kb of R or L into a stage of its own.
-  auto issue_piece = [&](bool is_r, int stage, int kb, int i) {
+  auto issue_piece = [&](bool is_r, int stage, int kb_local, int i) {
+    const int kb = kb0 + kb_local;
     const lds_u8* to = (is_r ? (const lds_u8*)r_lds + stage * R_BYTES : (const lds_u8*)l_lds + stage * L_BYTES) +
                        (i * 4 + wave) * 1024;
     const int o = is_r ? (i < HN / 32 ? 0 : 1) : 2, j = is_r ? i - o * (HN / 32) : i;
@@ -143,6 +140,9 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < NPR; ++i) issue_piece(true, pre, cr.kb, i);
     advance_r();
+  }
+#pragma unroll
+  for (int pre = 0; pre < LST; ++pre) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) issue_piece(false, pre, cl.kb, i);
     advance_l();
@@ -175,11 +175,11 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
 #pragma unroll
       for (int q = 0; q < GROUPS; ++q) {
 #pragma unroll
-        for (int f = q * READS * MOE_RD / 2 / GROUPS; f < (q + 1) * READS * MOE_RD / 2 / GROUPS; ++f)
+        for (int f = q * READS * 3 / 2 / GROUPS; f < (q + 1) * READS * 3 / 2 / GROUPS; ++f)
           if (f < READS) read(fr, fl, s ^ 1, f);
 #pragma unroll
-        for (int i = q * NP * MOE_FRONT / GROUPS; i < (q + 1) * NP * MOE_FRONT / GROUPS; ++i)
-          if (i < NP) issue_piece(s == 0, into, s == 0 ? cr.kb : cl.kb, i);
+        for (int i = q * NP / GROUPS; i < (q + 1) * NP / GROUPS; ++i)
+          issue_piece(s == 0, into, s == 0 ? cr.kb : cl.kb, i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (q * 4 + e) % NB, t = (q * 4 + e) / NB;
@@ -192,13 +192,14 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
       half(std::integral_constant<int, 0>{}, sr, sl, after(sr, 2));
       advance_r();
       wait_lds();
-      wait_vm<NPR>();  // all but the pieces just issued: the next K-block is there
+      wait_vm<NPR + (LST - 2) * NPL>();  // the next K-block is there; what was issued after it stays in flight
       barrier();
       __builtin_amdgcn_sched_barrier(0);
-      half(std::integral_constant<int, 1>{}, after(sr, 1), sl ^ 1, sl);
+      const int sn = sl + 1 == LST ? 0 : sl + 1;
+      half(std::integral_constant<int, 1>{}, after(sr, 1), sn, sl);
       advance_l();
       sr = after(sr, 1);
-      sl ^= 1;
+      sl = sn;
     }
     // the MFMAs' results are there 18 wait states after the last
     asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
@@ -221,6 +222,8 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
           const float f[4] = {r[0], r[1], r[2], r[3]};
           if constexpr (EPI == kOut) {
             *reinterpret_cast<u32x2*>(a.out + m * a.out_stride + c) = pack4(f);
+          } else if constexpr (EPI == kPart) {
+            *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
           } else if constexpr (EPI == kOutF32) {
             v4f* o = reinterpret_cast<v4f*>(a.outf + m * a.n + c);
             *o = a.accumulate ? *o + r : r;

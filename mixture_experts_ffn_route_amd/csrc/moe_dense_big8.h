@@ -1,18 +1,19 @@
-// e4m3 products with block scales on 256 x 256 tiles.
+// e4m3 products with block scales on tiles of 256 rows of R and BM (256, 128) of L.
 //
 // Every block's sum P has to leave the MFMA to be multiplied by its own scales:
 // acc += sx sw P, four multiply-adds a lane beside each 16 x 16 x 128 MFMA (16 of
 // its 32 cycles).  Those need the accumulators in ordinary registers, so eight
-// waves share the tile (64 x 128 each, 128 registers), two a SIMD, in two groups
-// of four that own 128 rows of L each and run one slot apart: a K-block of 128
+// waves share the tile (64 x BM / 2 each, 128 registers at 256), two a SIMD, in two groups
+// of four that own half of L's rows each and run one slot apart: a K-block of 128
 // is a load slot (the loads of the next K-block, the fragments of R) and an MFMA
 // slot (32 MFMAs, L's fragments as they come, the multiply-adds of the MFMA
 // before the last), with a barrier behind each, and while one group multiplies
 // the other loads.
 //
-// Two stages of 64 KB.  Group 0 loads R and its rows of L, group 1 its rows, each
-// one K-block ahead; a wave waits for its loads at the end of its MFMA slot,
-// and the barrier there publishes them.
+// Two stages of 64 KB, loaded one K-block ahead, or with 128 rows of L, whose
+// MFMA slots are half as long, three of 48 KB, loaded two ahead.  Group 0 loads R
+// and its rows of L, group 1 its rows; a wave waits for its loads of the next
+// K-block at the end of its MFMA slot, and the barrier there publishes them.
 #pragma once
 
 #include "moe_dense_tile.h"
@@ -21,19 +22,23 @@ namespace moe {
 namespace dense {
 
 // CUT: K is no multiple of 128.  VEC: four columns are stored at once (kOut).
-template <int EPI, bool CUT, bool VEC>
+// blockIdx.y: the part of K (kPart).
+template <int EPI, bool CUT, bool VEC, int BM>
 __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
   constexpr bool kPair = EPI == kSwigluQ;
-  constexpr int BM = 256, BN = 256, HN = BN / 2, NB = 4, TB = 8;
+  constexpr int BN = 256, HN = BN / 2, NB = 4, GM = BM / 2, TB = GM / 16;  // GM: rows of L per group
+  constexpr int STAGES = BM == 256 ? 2 : 3, AHEAD = STAGES - 1, LP = GM / 32;  // LP: pieces of L per wave
+  constexpr int LOADS0 = 8 + LP + 1, LOADS1 = LP + 1;                          // loads of a wave per K-block
   constexpr int R_BYTES = BN * kLine, L_BYTES = BM * kLine;
-  __shared__ __attribute__((aligned(1024))) uint8_t r_lds[2 * R_BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t l_lds[2 * L_BYTES];
-  __shared__ __attribute__((aligned(16))) float sx_lds[2][BM];
+  __shared__ __attribute__((aligned(1024))) uint8_t r_lds[STAGES * R_BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t l_lds[STAGES * L_BYTES];
+  __shared__ __attribute__((aligned(16))) float sx_lds[STAGES][BM];
   __shared__ uint32_t top_s[kPair ? 4 * BM : 1];
   typedef __attribute__((address_space(3))) const float lds_f32;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, grp = wave >> 2;
-  const int total = a.m_tiles * a.n_tiles, kbs = a.kbs;
+  const int total = a.m_tiles * a.n_tiles;
+  const int kb0 = blockIdx.y * a.kb_per_split, kbs = min(a.kb_per_split, a.kbs - kb0);
   const int blocks = ((kPair ? 2 * a.n : a.n) + 127) / 128;
 
   // the tile whose loads are being issued
@@ -55,12 +60,12 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     }
     lb = a.l + m0 * a.l_stride;
     lrows = min(a.m - m0, BM);
-    sxb = a.ls + (int64_t)m0 * kbs;
+    sxb = a.ls + (int64_t)m0 * a.kbs;
   };
-  // Pieces: wave w of a group takes pieces 4 i + w of 8 rows; in a half of R
-  // (16 pieces) i = 0..3, in the group's rows of L (16 pieces) i = 0..3.
+  // Pieces: wave w of a group takes pieces 4 i + w of 8 rows: of a half of R
+  // (16 pieces) i = 0..3, of the group's rows of L i = 0..LP-1.
   const int in_row = 8 * wn + (lane >> 3), in_c = ((lane & 7) ^ swz(in_row & 15)) * 16;
-  const int sx_row = 128 * grp + (wn & 1) * 64 + lane;  // of waves 0 and 1
+  const int sx_row = GM * grp + wn * 64 % GM;  // 64 scales a wave; the waves past the group's rows load them again
   auto piece = [&](const uint8_t* from, int64_t stride, int row, int rows, int kb, const lds_u8* to) {
     const uint32_t off = __umul24(min(row, rows - 1), (uint32_t)stride) + in_c;
     if constexpr (!CUT)
@@ -68,7 +73,8 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     else
       dma16_at(in_c < a.k - kb * kLine ? from + (int64_t)kb * kLine + off : (const uint8_t*)&kZeros, to);
   };
-  auto issue = [&](int stage, int kb) {
+  auto issue = [&](int stage, int kb_local) {
+    const int kb = kb0 + kb_local;
     if (grp == 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -76,12 +82,10 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
               (const lds_u8*)r_lds + stage * R_BYTES + (i * 4 + wn) * 1024);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      piece(lb, a.l_stride, 128 * grp + 32 * i + in_row, lrows, kb,
-            (const lds_u8*)l_lds + stage * L_BYTES + (16 * grp + i * 4 + wn) * 1024);
-    if (wn < 2)
-      dma4(sxb + kb, __umul24(min(sx_row, lrows - 1), (uint32_t)kbs) * 4u,
-           (const lds_u8*)&sx_lds[stage][128 * grp + (wn & 1) * 64]);
+    for (int i = 0; i < LP; ++i)
+      piece(lb, a.l_stride, GM * grp + 32 * i + in_row, lrows, kb,
+            (const lds_u8*)l_lds + stage * L_BYTES + (4 * LP * grp + i * 4 + wn) * 1024);
+    dma4(sxb + kb, __umul24(min(sx_row + lane, lrows - 1), (uint32_t)a.kbs) * 4u, (const lds_u8*)&sx_lds[stage][sx_row]);
   };
 
   // The K-block to load next is kb_in of tile v_in; after the last tile its last
@@ -98,8 +102,8 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
   setup(mt, nt);
   const float *sw0, *sw1;  // the current tile's weight scales
   auto tile_scales = [&]() {
-    sw0 = a.rs + (int64_t)sblk[0] * kbs;
-    sw1 = a.rs + (int64_t)sblk[1] * kbs;
+    sw0 = a.rs + (int64_t)sblk[0] * a.kbs + kb0;
+    sw1 = a.rs + (int64_t)sblk[1] * a.kbs + kb0;
   };
   tile_scales();
   auto advance = [&]() {
@@ -108,8 +112,11 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     kb_in = v_in < ids ? 0 : kbs - 1;
     if (v_in < ids) setup(mt, nt);
   };
-  issue(0, 0);
-  advance();
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    issue(i, kb_in);
+    advance();
+  }
   wait_vm<0>();
   __syncthreads();
 
@@ -129,11 +136,11 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     if (grp == 1) barrier();  // one slot behind
     for (int kb = 0; kb < kbs; ++kb) {
       // load slot
-      issue(stage ^ 1, kb_in);
+      issue(stage + AHEAD >= STAGES ? stage + AHEAD - STAGES : stage + AHEAD, kb_in);
       const float w0 = scalar_f32(sw0 + kb), w1 = scalar_f32(sw1 + kb);
       const lds_u8* rt = (const lds_u8*)r_lds + stage * R_BYTES;
       const lds_u8* lt = (const lds_u8*)l_lds + stage * L_BYTES + grp * TB * 2048;
-      lds_f32* st = (lds_f32*)&sx_lds[stage][128 * grp + tl];
+      lds_f32* st = (lds_f32*)&sx_lds[stage][GM * grp + tl];
       v8i rf[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) rf[i] = frag(rt + (i < 2 ? 0 : HN * kLine) + (wn * 2 + (i & 1)) * 2048);
@@ -187,16 +194,20 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int t = 0; t < TB; ++t) asm volatile("" : "+v"(acc[i][t]));  // issued before the slot ends
-      wait_vm<0>();
+      // the next K-block is there; the loads behind it stay in flight
+      if (grp == 0)
+        wait_vm<LOADS0 * (AHEAD - 1)>();
+      else
+        wait_vm<LOADS1 * (AHEAD - 1)>();
       wait_lds();
       barrier();
       __builtin_amdgcn_sched_barrier(0);
-      stage ^= 1;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     if (grp == 0) barrier();  // the groups side by side again
 
     const int m0 = mt_cur * BM, n0 = nt_cur * (kPair ? HN : BN);
-    const int lm = m0 + 128 * grp + tl, lc = n0 + wn * 32 + 4 * g;
+    const int lm = m0 + GM * grp + tl, lc = n0 + wn * 32 + 4 * g;
     if constexpr (kPair) {
       float h[2][TB][4];
 #pragma unroll
@@ -211,13 +222,13 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
           }
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (lane < 16) top_s[wn * BM + 128 * grp + t * 16 + tl] = top;
+        if (lane < 16) top_s[wn * BM + GM * grp + t * 16 + tl] = top;
       }
       wait_lds();
       barrier();
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        const int r = 128 * grp + t * 16 + tl;
+        const int r = GM * grp + t * 16 + tl;
         const int64_t m = m0 + r;
         const uint32_t top = max(max(top_s[r], top_s[BM + r]), max(top_s[2 * BM + r], top_s[3 * BM + r]));
         const float sc = __uint_as_float(top) / kE4m3Max;
@@ -240,7 +251,9 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
             const int c = lc + (i < 2 ? i * 16 : HN + (i - 2) * 16);
             const v4f r = acc[i][t];
             float f[4] = {r[0], r[1], r[2], r[3]};
-            if constexpr (VEC) {
+            if constexpr (EPI == kPart) {
+              if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
+            } else if constexpr (VEC) {
               if (c >= a.n) continue;
               if (a.add) {
                 float d[4];
@@ -268,8 +281,8 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     {  // the weight scales of the tile that follows
       const int n1 = nt * (kPair ? HN : BN);
       const int r1 = kPair ? n1 + a.n : (a.n - n1 > HN ? n1 + HN : n1);
-      sw0 = a.rs + (int64_t)min(n1 / 128, blocks - 1) * kbs;
-      sw1 = a.rs + (int64_t)min(r1 / 128, blocks - 1) * kbs;
+      sw0 = a.rs + (int64_t)min(n1 / 128, blocks - 1) * a.kbs + kb0;
+      sw1 = a.rs + (int64_t)min(r1 / 128, blocks - 1) * a.kbs + kb0;
     }
   }
   wait_vm<0>();  // no load into LDS outlives the workgroup

@@ -7,28 +7,66 @@
 #include "moe_dense_tile.h"
 #include "moe_internal.h"
 
-#ifndef MOE_WN
-#define MOE_WN 4
-#define MOE_WN2 4
-#endif
 namespace moe {
 namespace dense {
 
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 inline size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Parts of K for a product whose 128 x 128 tiles would leave CUs idle (two
-// tiles a CU): at least 4 K-blocks each.
-inline int splits_for(int m, int n, int kbs) {
-  const int64_t tiles = (int64_t)cdiv(m, 128) * cdiv(n, 128);
-  if (tiles >= 256) return 1;
-#ifndef MOE_SLOTS
-#define MOE_SLOTS 256
-#endif
-  int s = (int)(MOE_SLOTS / tiles);
-  if (s > kbs / 4) s = kbs / 4;
-  if (s > 16) s = 16;
-  return s < 2 ? 1 : cdiv(kbs, cdiv(kbs, s));
+inline int pitch_of(int n) { return (n + 3) / 4 * 4; }
+
+// How a product is made: by few_kernel, or on tiles of tm rows of L and tn of R (128
+// x 128: tile_kernel, else the large tiles' kernel), K in `splits` parts that
+// join_kernel sums.
+struct Plan {
+  int tm, tn, splits;  // tm 0: few_kernel
+};
+
+// us a K-block (128 bytes of K) takes in a workgroup of each form, as measured:
+// few_kernel with 1..4 blocks of L rows and 32 columns, and its part of that with
+// 16; 128 x 128 tiles, one and two workgroups a CU; 128 x 256; 256 x 256.
+struct Rates {
+  double few[4], narrow, tile, tile2, wide, large;
+};
+
+// The form that is estimated to be fastest, from the sizes alone: rounds of
+// workgroups over the CUs (tiles: over the 32 of the XCD with the most), each as many K-blocks long as a part of K has, 4
+// us around them (few_kernel 2.8), and with parts of K a join of 3 us and their
+// bytes at 6.5 TB/s.  Measured over 32 <= m <= 4096 and the products of H=7168
+// I=2048, H=2048 I=768, N=1003 K=2000 and N=576 K=7168, each form for each m, the
+// choice takes at most 1.22 times the time of the fastest of them, and not more in
+// the mean.
+// few: whether few_kernel can make it; split: whether K may be split; joined: a
+// join follows in any case but that of one part on tiles of 256 rows of R.
+inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, bool joined) {
+  auto rounds = [](int64_t groups, int64_t slots) { return (double)((groups + slots - 1) / slots); };
+  auto join = [&](int parts) { return 3.0 + (double)parts * m * n * 8e-6 / 6.5; };
+  Plan best{128, 128, 1};
+  double least = 1e30;
+  auto offer = [&](double us, const Plan& p) {
+    if (us < least) {
+      least = us;
+      best = p;
+    }
+  };
+  if (few) {
+    const int blocks = cdiv(m, 16), parts = cdiv(blocks, 4), mt = cdiv(blocks, parts);
+    const int64_t groups = (int64_t)cdiv(n, 32) * parts;
+    const double us = groups < 200 ? 2.8 + rounds(2 * groups, 256) * (kbs * r.few[mt - 1] * r.narrow + 0.4)
+                                   : 2.8 + rounds(groups, 256) * (kbs * r.few[mt - 1] + 0.4);
+    offer(us + (joined ? join(1) : 0.0), Plan{0, 0, 1});
+  }
+  for (int s = 1; s <= 16 && (s == 1 || (split && kbs >= 2 * s)); ++s) {
+    const int kb = cdiv(kbs, s);
+    if (cdiv(kbs, kb) != s) continue;  // fewer parts of the same length
+    auto per_xcd = [&](int tm, int tn) { return cdiv((int64_t)cdiv(m, tm) * cdiv(n, tn), 8) * (int64_t)s; };
+    const int64_t t = per_xcd(128, 128);
+    const double tail = s > 1 ? join(s) : 0.0, fused = joined && s == 1 ? join(1) : 0.0;
+    offer(4.0 + (t <= 32 ? kb * r.tile : rounds(t, 64) * kb * r.tile2) + tail + fused, Plan{128, 128, s});
+    offer(4.0 + rounds(per_xcd(128, 256), 32) * kb * r.wide + tail, Plan{128, 256, s});
+    offer(4.0 + rounds(per_xcd(256, 256), 32) * kb * r.large + tail, Plan{256, 256, s});
+  }
+  return best;
 }
 
 // `a` has its tiles.  One workgroup a CU: four stages; more: two.
@@ -37,17 +75,17 @@ void launch_tile(const Args& a, int splits, hipStream_t s) {
   const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
   const dim3 grid(tile_grid(tiles), splits);
   if constexpr (BM + BN > 256)  // one workgroup a CU in any case
-    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 3, MOE_WN2>), grid, dim3(MOE_WN2 * 128), 0, s, a);
-  else if (tiles * splits <= 256)
-    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4, MOE_WN>), grid, dim3(MOE_WN * 128), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 3, 4>), grid, dim3(512), 0, s, a);
+  else if ((tiles + 7) / 8 * splits <= 32)
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4, 4>), grid, dim3(512), 0, s, a);
   else
     hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <int EPI>
-void launch_join(const Args& a, const float* part, int splits, int cols, hipStream_t s) {
+void launch_join(const Args& a, const float* part, int splits, int pitch, hipStream_t s) {
   const int64_t threads = (int64_t)a.m * ((a.n + 3) / 4);
-  hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, part, splits, cols);
+  hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, part, splits, pitch);
 }
 
 // Whether two strided areas of rows share memory, by their first and last byte.

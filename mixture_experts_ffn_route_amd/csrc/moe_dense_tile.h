@@ -36,7 +36,8 @@ struct Args {
   int64_t out_stride;  // values
   const uint16_t* add;  // null: none
   int64_t add_stride;
-  float* outf;  // kOutF32: [m, n]; kPart: [splits, m, n]; kSwigluF32: [m, n]
+  float* outf;  // kOutF32: [m, n]; kPart: [splits, m, pitch]; kSwigluF32: [m, n]
+  int32_t pitch;  // kPart: n up to whole 16 bytes
   int32_t accumulate;
   int32_t vec;  // results of 4 columns may be stored at once
   float* gu;  // [m, 2 n]
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Arg
         } else if constexpr (EPI == kOutF32) {
           store_f32(a.outf + m * a.n + c, c, a.n, a.vec, a.accumulate, f);
         } else if constexpr (EPI == kPart) {
-          store_f32(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.n + c, c, a.n, a.vec, false, f);
+          if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = v;
         } else if constexpr (EPI == kSwiglu) {
           const v4f w = acc[NB / 2 + i][t];
           const float u[4] = {w[0], w[1], w[2], w[3]};
@@ -321,31 +322,25 @@ __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Arg
 
 // Sums of kPart results over the splits, in ascending order, and what becomes
 // of them; a thread takes 4 columns of one row.  kSwigluQ: 32 lanes hold a scale
-// block.  part: [splits, a.m, cols].
+// block.  part: [splits, a.m, pitch].
 template <int EPI>
-__global__ __launch_bounds__(256) void join_kernel(Args a, const float* part, int splits, int cols) {
+__global__ __launch_bounds__(256) void join_kernel(Args a, const float* part, int splits, int pitch) {
   constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
   const int quads = (a.n + 3) / 4;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = at / quads;
   const int c = (int)(at - m * quads) * 4;
   if (m >= a.m) return;  // kSwigluQ: whole groups of 32 lanes
-  const int64_t plane = (int64_t)a.m * cols;
-  const bool whole = cols % 4 == 0;
+  const int64_t plane = (int64_t)a.m * pitch;
   float v[kPair ? 2 : 1][4] = {};
 #pragma unroll
   for (int h = 0; h < (kPair ? 2 : 1); ++h) {
-    const float* p = part + m * cols + c + h * a.n;
-    for (int s = 0; s < splits; ++s, p += plane) {
-      if (whole) {
-        const v4f w = *reinterpret_cast<const v4f*>(p);
+    const float* p = part + m * pitch + c + h * a.n;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const v4f w = *reinterpret_cast<const v4f*>(p + s * plane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[h][i] += w[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < cols) v[h][i] += p[i];
-      }
+      for (int i = 0; i < 4; ++i) v[h][i] += w[i];
     }
   }
   if constexpr (EPI == kOut) {

@@ -12,6 +12,8 @@
 // place of 0.0024 of their root mean square, of which that rounding is 0.0017).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "moe_dense_big.h"
 #include "moe_dense_few.h"
 #include "moe_dense_host.h"
@@ -23,51 +25,59 @@ namespace {
 
 using namespace dense;
 
-#ifndef MOE_FEW_MAX
-#define MOE_FEW_MAX 64
-#endif
-constexpr int kFewTokens = MOE_FEW_MAX;  // up to here the few-token form
+constexpr Rates kRates = {{0.075, 0.12, 0.14, 0.17}, 0.8, 0.52, 1.05, 0.88, 1.55};
 
-size_t parts_bytes(int m, int n, int kbs) {
-  const int s = splits_for(m, n, kbs);
-  return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
+Plan plan_for(int m, int n, int kbs, bool k_inside) { return choose(m, n, kbs, kRates, k_inside, true, false); }
+
+size_t parts_bytes(int m, int n, int kbs, bool k_inside) {
+  const Plan p = plan_for(m, n, kbs, k_inside);
+  return p.splits > 1 ? pad256((size_t)p.splits * m * n * 4) : 0;
 }
 
+// a.n: columns of the product (SwiGLU: of h).
+template <int LL, int LR, int EPI, int BM>
+void launch_big(Args a, int splits, hipStream_t s) {
+  a.m_tiles = cdiv(a.m, BM);
+  a.n_tiles = cdiv(a.n, EPI == kSwiglu ? 128 : 256);
+  a.kb_per_split = cdiv(a.kbs, splits);
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256, splits);
+  if (a.k % 64 == 0)
+    hipLaunchKernelGGL((big_kernel<LL, LR, BM, 256, EPI, false>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((big_kernel<LL, LR, BM, 256, EPI, true>), grid, dim3(256), 0, s, a);
+}
 template <int LL, int LR, int EPI>
-void tile(Args a, int splits, hipStream_t s) {
+void launch_plan(Args a, const Plan& p, hipStream_t s) {
+  if (p.tn == 256)
+    return p.tm == 256 ? launch_big<LL, LR, EPI, 256>(a, p.splits, s) : launch_big<LL, LR, EPI, 128>(a, p.splits, s);
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, EPI == kSwiglu ? 64 : 128);
-  a.kb_per_split = splits > 1 ? cdiv(a.kbs, splits) : a.kbs;
-  launch_tile<false, LL, LR, 128, 128, EPI>(a, splits, s);
+  a.kb_per_split = p.splits > 1 ? cdiv(a.kbs, p.splits) : a.kbs;
+  launch_tile<false, LL, LR, 128, 128, EPI>(a, p.splits, s);
 }
 
-template <int LL, int LR, int EPI, int BM, int BN>
-void launch_big(Args a, hipStream_t s) {
-  a.m_tiles = cdiv(a.m, BM);
-  a.n_tiles = cdiv(a.n, EPI == kSwiglu ? BN / 2 : BN);
-  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256);
-  if (a.k % 64 == 0)
-    hipLaunchKernelGGL((big_kernel<LL, LR, BM, BN, EPI, false>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((big_kernel<LL, LR, BM, BN, EPI, true>), grid, dim3(256), 0, s, a);
-}
-
-bool use_big(int64_t m, int64_t n) { return (int64_t)cdiv(m, 256) * cdiv(n, 256) >= 96; }
-
-// A product whose result has n columns, of L (K inside) and R, into EPI; with
-// SwiGLU h has half of the columns.
+// A product of L (K inside) and R, whose result has n columns, into EPI (SwiGLU:
+// h has half of them).
 template <int LR, int EPI>
 void product(Args a, int n, float* parts, hipStream_t s) {
-  if (use_big(a.m, n)) return launch_big<kKin, LR, EPI, 256, 256>(a, s);
-  const int splits = splits_for(a.m, n, a.kbs);
-  if (splits == 1) return tile<kKin, LR, EPI>(a, 1, s);
-  Args p = a;
-  p.n = n;
-  p.outf = parts;
-  p.vec = 1;
-  tile<kKin, LR, kPart>(p, splits, s);
-  launch_join<EPI>(a, parts, splits, n, s);
+  const Plan p = plan_for(a.m, n, a.kbs, LR == kKin);
+  if constexpr (LR == kKin) {
+    if (p.tm == 0) return launch_few<kBf16, EPI>(a, s);
+  }
+  if (p.splits == 1) return launch_plan<kKin, LR, EPI>(a, p, s);
+  Args b = a;
+  b.n = b.pitch = n;
+  b.outf = parts;
+  launch_plan<kKin, LR, kPart>(b, p, s);
+  launch_join<EPI>(a, parts, p.splits, n, s);
+}
+
+// A weight gradient: K (the tokens) outside both operands; without tokens zero.
+template <int EPI>
+void gradient(const Args& a, hipStream_t s) {
+  const Plan p = a.kbs == 0 ? Plan{128, 128, 1} : choose(a.m, a.n, a.kbs, kRates, false, false, false);
+  launch_plan<kKout, kKout, EPI>(a, p, s);
 }
 
 moe_status_t check_sizes(int32_t m, int32_t hidden, int32_t inter) {
@@ -105,15 +115,13 @@ moe_status_t check_apart(const Area* outs, int n_outs, const Area* ins, int n_in
 }
 
 size_t forward_bytes(int m, int hidden, int inter) {
-  if (m <= kFewTokens) return 0;
-  const size_t a = parts_bytes(m, 2 * inter, cdiv(hidden, 64)), b = parts_bytes(m, hidden, cdiv(inter, 64));
-  return a > b ? a : b;
+  return std::max(parts_bytes(m, 2 * inter, cdiv(hidden, 64), true), parts_bytes(m, hidden, cdiv(inter, 64), true));
 }
 // dg | du, then parts
 size_t backward_bytes(int m, int hidden, int inter, size_t* first) {
   *first = pad256((size_t)m * 2 * inter * 2);
-  const size_t a = parts_bytes(m, inter, cdiv(hidden, 64)), b = parts_bytes(m, hidden, cdiv(2 * inter, 64));
-  return *first + (a > b ? a : b);
+  return *first +
+         std::max(parts_bytes(m, inter, cdiv(hidden, 64), false), parts_bytes(m, hidden, cdiv(2 * inter, 64), false));
 }
 
 }  // namespace
@@ -176,14 +184,9 @@ extern "C" moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const v
   b.k = intermediate;
   b.kbs = cdiv(intermediate, 64);
   set_out(b, nullptr, 0, out, out_stride);
-  if (m <= kFewTokens) {
-    launch_few<kBf16, kSwiglu>(a, s);
-    launch_few<kBf16, kOut>(b, s);
-  } else {
-    float* parts = static_cast<float*>(workspace);
-    product<kKin, kSwiglu>(a, 2 * intermediate, parts, s);
-    product<kKin, kOut>(b, hidden, parts, s);
-  }
+  float* parts = static_cast<float*>(workspace);
+  product<kKin, kSwiglu>(a, 2 * intermediate, parts, s);
+  product<kKin, kOut>(b, hidden, parts, s);
   return launched("gated ffn");
 }
 
@@ -267,16 +270,10 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
     if (dw_type == MOE_TYPE_F32) {
       a.outf = static_cast<float*>(dw);
       a.vec = 1;
-      if (m > 0 && use_big(a.m, a.n))
-        launch_big<kKout, kKout, kOutF32, 256, 256>(a, s);
-      else
-        tile<kKout, kKout, kOutF32>(a, 1, s);
+      gradient<kOutF32>(a, s);
     } else {
       set_out(a, nullptr, 0, dw, a.n);
-      if (m > 0 && use_big(a.m, a.n))
-        launch_big<kKout, kKout, kOut, 256, 256>(a, s);
-      else
-        tile<kKout, kKout, kOut>(a, 1, s);
+      gradient<kOut>(a, s);
     }
   }
   return launched("gated ffn backward");

@@ -17,59 +17,79 @@ namespace {
 
 using namespace dense;
 
-#ifndef MOE_FEW_MAX
-#define MOE_FEW_MAX 64
-#endif
-constexpr int kFewTokens = MOE_FEW_MAX;  // up to here the few-token form
-constexpr int kFewQuant = 16;   // up to here the shared expert's second product quantises h as it reads it
+constexpr int kFewQuant = 16;  // up to here the shared expert's second product quantises h as it reads it
+
+constexpr Rates kRates = {{0.13, 0.17, 0.19, 0.21}, 0.6, 0.80, 1.10, 1.00, 1.75};
+
+// Up to 16 rows sums are float32's in any case: few_kernel.
+Plan plan_for(int m, int n, int kbs, bool joined = false) {
+  if (m <= 16) return Plan{0, 0, 1};
+  return choose(m, n, kbs, kRates, true, true, joined);
+}
 
 size_t parts_bytes(int m, int n, int kbs) {
-  if (m <= kFewTokens) return 0;
-  const int s = splits_for(m, n, kbs);
-  return s > 1 ? pad256((size_t)s * m * n * 4) : 0;
+  const Plan p = plan_for(m, n, kbs);
+  return p.splits > 1 ? pad256((size_t)p.splits * m * pitch_of(n) * 4) : 0;
 }
 
-// One product of e4m3 rows, n columns, into `parts` where K is split.
-void tile_parts(Args a, int splits, float* parts, hipStream_t s) {
-  a.outf = parts;
-  a.vec = a.n % 4 == 0;
-  a.m_tiles = cdiv(a.m, 128);
-  a.n_tiles = cdiv(a.n, 128);
+template <int EPI, int BM>
+void launch_big(Args a, int splits, hipStream_t s) {
+  a.m_tiles = cdiv(a.m, BM);
+  a.n_tiles = cdiv(a.n, EPI == kSwigluQ ? 128 : 256);
   a.kb_per_split = cdiv(a.kbs, splits);
-  launch_tile<true, kKin, kKin, 128, 128, kPart>(a, splits, s);
+  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256, splits), block(512);
+  const bool cut = a.k % 128 != 0;
+  if constexpr (EPI == kSwigluQ) {
+    hipLaunchKernelGGL((big8_kernel<EPI, false, true, BM>), grid, block, 0, s, a);
+  } else if (EPI == kPart || (a.vec && a.n % 4 == 0)) {
+    if (cut)
+      hipLaunchKernelGGL((big8_kernel<EPI, true, true, BM>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((big8_kernel<EPI, false, true, BM>), grid, block, 0, s, a);
+  } else {
+    if (cut)
+      hipLaunchKernelGGL((big8_kernel<kOut, true, false, BM>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((big8_kernel<kOut, false, false, BM>), grid, block, 0, s, a);
+  }
 }
-
-bool use_big(int64_t m, int64_t n) { return (int64_t)cdiv(m, 256) * cdiv(n, 256) >= 96; }
 
 template <int EPI>
-void launch_big(Args a, hipStream_t s) {
-  a.m_tiles = cdiv(a.m, 256);
-  a.n_tiles = cdiv(a.n, EPI == kSwigluQ ? 128 : 256);
-  const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-  const dim3 grid(tiles < 256 ? tile_grid(tiles) : 256), block(512);
-  const bool cut = a.k % 128 != 0, vec = EPI == kSwigluQ || (a.vec && a.n % 4 == 0);
-  if (EPI == kSwigluQ || (!cut && vec))
-    hipLaunchKernelGGL((big8_kernel<EPI, false, true>), grid, block, 0, s, a);
-  else if (vec)
-    hipLaunchKernelGGL((big8_kernel<kOut, true, true>), grid, block, 0, s, a);
-  else if (cut)
-    hipLaunchKernelGGL((big8_kernel<kOut, true, false>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((big8_kernel<kOut, false, false>), grid, block, 0, s, a);
+void launch_plan(Args a, const Plan& p, hipStream_t s) {
+  if (p.tn == 256) return p.tm == 256 ? launch_big<EPI, 256>(a, p.splits, s) : launch_big<EPI, 128>(a, p.splits, s);
+  a.m_tiles = cdiv(a.m, 128);
+  a.n_tiles = cdiv(a.n, 128);
+  a.kb_per_split = cdiv(a.kbs, p.splits);
+  launch_tile<true, kKin, kKin, 128, 128, EPI>(a, p.splits, s);
 }
 
 void product(Args a, float* parts, hipStream_t s) {
-  if (a.m <= kFewTokens) return launch_few<kCodes, kOut>(a, s);
-  if (use_big(a.m, a.n)) return launch_big<kOut>(a, s);
-  const int splits = splits_for(a.m, a.n, a.kbs);
-  if (splits > 1) {
-    tile_parts(a, splits, parts, s);
-    return launch_join<kOut>(a, parts, splits, a.n, s);
-  }
-  a.m_tiles = cdiv(a.m, 128);
-  a.n_tiles = cdiv(a.n, 128);
-  a.kb_per_split = a.kbs;
-  launch_tile<true, kKin, kKin, 128, 128, kOut>(a, 1, s);
+  const Plan p = plan_for(a.m, a.n, a.kbs);
+  if (p.tm == 0) return launch_few<kCodes, kOut>(a, s);
+  if (p.splits == 1) return launch_plan<kOut>(a, p, s);
+  Args b = a;
+  b.outf = parts;
+  b.pitch = pitch_of(a.n);
+  launch_plan<kPart>(b, p, s);
+  launch_join<kOut>(a, parts, p.splits, b.pitch, s);
+}
+
+// h of the shared expert: gate | up of `a` (a.n columns of h), quantised.  Where
+// the 2 n columns of gate | up are no plan of one part on tiles of 256 rows of R
+// they go through `first`, 2 n float32 a row and part.
+bool fused_h(const Plan& p) { return p.tn == 256 && p.splits == 1; }
+void product_h(Args a, float* first, hipStream_t s) {
+  const Plan p = plan_for(a.m, 2 * a.n, a.kbs, true);
+  if (fused_h(p)) return p.tm == 256 ? launch_big<kSwigluQ, 256>(a, 1, s) : launch_big<kSwigluQ, 128>(a, 1, s);
+  Args b = a;
+  b.n = b.pitch = 2 * a.n;
+  b.outf = first;
+  if (p.tm == 0)
+    launch_few<kCodes, kPart>(b, s);
+  else
+    launch_plan<kPart>(b, p, s);
+  launch_join<kSwigluQ>(a, first, p.splits, b.pitch, s);
 }
 
 moe_status_t check_rows(const char* name, const void* x, int64_t stride, int64_t rows, int64_t k) {
@@ -108,7 +128,8 @@ FfnLayout ffn_layout(int32_t m, int32_t hidden, int32_t inter) {
     l.first = pad256((size_t)m * inter * 4);
     return l;
   }
-  l.first = m <= kFewTokens ? pad256((size_t)m * 2 * inter * 4) : parts_bytes(m, 2 * inter, hidden / 128);
+  const Plan p = plan_for(m, 2 * inter, hidden / 128, true);
+  l.first = fused_h(p) ? 0 : pad256((size_t)p.splits * m * 2 * inter * 4);
   const size_t second = parts_bytes(m, hidden, inter / 128);
   if (second > l.first) l.first = second;
   l.codes = pad256((size_t)m * inter);
@@ -233,25 +254,7 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
     launch_few<kQuant, kOut, 1>(b, s);
     return launched("shared expert");
   }
-  const int splits = m <= kFewTokens ? 1 : splits_for(m, 2 * intermediate, a.kbs);
-  if (m <= kFewTokens || splits > 1) {
-    Args p = a;
-    p.n = 2 * intermediate;
-    p.outf = first;
-    p.vec = 1;
-    if (m <= kFewTokens)
-      launch_few<kCodes, kPart>(p, s);
-    else
-      tile_parts(p, splits, first, s);
-    launch_join<kSwigluQ>(a, first, splits, 2 * intermediate, s);
-  } else if (use_big(m, 2 * (int64_t)intermediate)) {
-    launch_big<kSwigluQ>(a, s);
-  } else {
-    a.m_tiles = cdiv(m, 64);
-    a.n_tiles = intermediate / 128;
-    a.kb_per_split = a.kbs;
-    launch_tile<true, kKin, kKin, 64, 256, kSwigluQ>(a, 1, s);
-  }
+  product_h(a, first, s);
   product(b, first, s);
   return launched("shared expert");
 }
