@@ -31,6 +31,30 @@ def _sizes(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor):
     return T, H, I
 
 
+def _forward(x, w13, w2, out, gate_up: bool):
+    """moe_ffn_forward of checked tensors on the current device."""
+    (T, H), I, dev = x.shape, w2.shape[1], x.device
+    if out is None:
+        out = empty_rows(T, H, torch.bfloat16, dev)
+    gu = empty_rows(T, 2 * I, torch.float32, dev) if gate_up else None
+    h = empty_rows(T, I, torch.bfloat16, dev)
+    ws_bytes = L.moe_ffn_workspace_query(T, H, I)[0]
+    ws = _workspace(ws_bytes, dev)
+    L.moe_ffn_forward(x.data_ptr(), x.stride(0), w13.data_ptr(), w2.data_ptr(), T, H, I, ptr(gu), h.data_ptr(),
+                      out.data_ptr(), out.stride(0), ptr(ws), ws_bytes, current_raw_stream(dev.index))
+    return out, gu, h
+
+
+def _backward(dy, x, w13, w2, gu, h, dx, dw13, dw2, dw_type: int, accumulate: int) -> None:
+    """moe_ffn_backward of checked tensors on the current device."""
+    (T, H), I, dev = x.shape, w2.shape[1], x.device
+    ws_bytes = L.moe_ffn_workspace_query(T, H, I)[1]
+    ws = _workspace(ws_bytes, dev)
+    L.moe_ffn_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), w13.data_ptr(), w2.data_ptr(), ptr(gu),
+                       ptr(h), T, H, I, ptr(dx), 0 if dx is None else dx.stride(0), ptr(dw13), ptr(dw2), dw_type,
+                       accumulate, ptr(ws), ws_bytes, current_raw_stream(dev.index))
+
+
 def gated_ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, *, gate_up: bool = True,
                       out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor], torch.Tensor]:
     """``(silu(x Wg^T) * (x Wu^T)) w2^T`` without autograd (moe_ffn_forward):
@@ -40,18 +64,9 @@ def gated_ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, *, g
         with torch.cuda.device(x.device):
             return gated_ffn_forward(x, w13, w2, gate_up=gate_up, out=out)
     T, H, I = _sizes(x, w13, w2)
-    dev = x.device
-    if out is None:
-        out = empty_rows(T, H, torch.bfloat16, dev)
-    else:
-        check(out, "out", (T, H), _BF16, dev, True)
-    gu = empty_rows(T, 2 * I, torch.float32, dev) if gate_up else None
-    h = empty_rows(T, I, torch.bfloat16, dev)
-    ws_bytes = L.moe_ffn_workspace_query(T, H, I)[0]
-    ws = _workspace(ws_bytes, dev)
-    L.moe_ffn_forward(x.data_ptr(), x.stride(0), w13.data_ptr(), w2.data_ptr(), T, H, I, ptr(gu), h.data_ptr(),
-                      out.data_ptr(), out.stride(0), ptr(ws), ws_bytes, current_raw_stream(dev.index))
-    return out, gu, h
+    if out is not None:
+        check(out, "out", (T, H), _BF16, x.device, True)
+    return _forward(x, w13, w2, out, gate_up)
 
 
 def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
@@ -86,19 +101,19 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2:
         check(dw13, "dw13", (2 * I, H), _GRADS, dev)
     if dw2 is not None:
         check(dw2, "dw2", (H, I), _GRADS, dev)
-    ws_bytes = L.moe_ffn_workspace_query(T, H, I)[1]
-    ws = _workspace(ws_bytes, dev)
-    L.moe_ffn_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), w13.data_ptr(), w2.data_ptr(),
-                       ptr(gate_up), ptr(h), T, H, I, ptr(dx), 0 if dx is None else dx.stride(0), ptr(dw13), ptr(dw2),
-                       _GRADS[kinds.pop()] if kinds else L.MOE_TYPE_BF16, int(accumulate), ptr(ws), ws_bytes,
-                       current_raw_stream(dev.index))
+    _backward(dy, x, w13, w2, gate_up, h, dx, dw13, dw2, _GRADS[kinds.pop()] if kinds else L.MOE_TYPE_BF16,
+              int(accumulate))
+
+
+# Mark on a leaf's gradient node: an eager graph of the default stream holds it.
+_EAGER = "moe_gated_ffn_eager"
 
 
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2):
         need_x, need_w13, need_w2 = ctx.needs_input_grad
-        out, gu, h = gated_ffn_forward(x, w13, w2, gate_up=need_x or need_w13)
+        out, gu, h = _forward(x, w13, w2, None, need_x or need_w13)
         ctx.save_for_backward(x, w13, w2, gu, h if need_w2 else None)
         return out
 
@@ -107,34 +122,18 @@ class _GatedFFN(torch.autograd.Function):
     def backward(ctx, dy):
         x, w13, w2, gu, h = ctx.saved_tensors
         need_x, need_w13, need_w2 = ctx.needs_input_grad
-        if dy.stride(-1) != 1 or (dy.shape[0] > 1 and (dy.stride(0) < dy.shape[1] or dy.stride(0) % 8)) or \
-                dy.data_ptr() % 16:
+        T, H = x.shape
+        if dy.stride(1) != 1 or dy.data_ptr() % 16 or (T > 1 and (dy.stride(0) < H or dy.stride(0) % 8)):
             dy = dy.clone(memory_format=torch.contiguous_format)  # broadcast, or a view that the kernels do not read
-        dx = empty_rows(*x.shape, torch.bfloat16, x.device) if need_x else None
-        dw13 = torch.empty_like(w13) if need_w13 else None
-        dw2 = torch.empty_like(w2) if need_w2 else None
-        gated_ffn_backward(dy, x, w13, w2, gu, h, dx=dx, dw13=dw13, dw2=dw2)
+        dx = empty_rows(T, H, torch.bfloat16, x.device) if need_x else None
+        dw13 = empty_rows(w13.shape[0], H, torch.bfloat16, x.device) if need_w13 else None
+        dw2 = empty_rows(H, w2.shape[1], torch.bfloat16, x.device) if need_w2 else None
+        if x.device.index != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                _backward(dy, x, w13, w2, gu, h, dx, dw13, dw2, L.MOE_TYPE_BF16, 0)
+        else:
+            _backward(dy, x, w13, w2, gu, h, dx, dw13, dw2, L.MOE_TYPE_BF16, 0)
         return dx, dw13, dw2
-
-
-_BORN = "moe_gated_ffn_stream"  # mark on a leaf's gradient node: the stream of the graph that it was met in
-
-
-def _leaf_nodes(leaves, dev) -> list:
-    """The leaves' gradient nodes, marked; to be held until the new graph holds
-    them.  Refuses a capture with leaves whose gradient nodes an eager graph of the
-    default stream keeps alive: the captured backward would make that stream wait
-    within the capture, which it cannot be part of, and ends the process."""
-    stream = current_raw_stream(dev.index)
-    capturing = torch.cuda.is_current_stream_capturing()
-    nodes = []
-    for t in leaves:
-        if t.requires_grad and t.is_leaf:
-            nodes.append(get_gradient_edge(t).node)
-            if nodes[-1].metadata.setdefault(_BORN, stream) == 0 and capturing:
-                raise RuntimeError("gated_ffn is being captured while an eager graph of one of its leaves lives: "
-                                   "release that graph first, or capture gated_ffn_forward and gated_ffn_backward")
-    return nodes
 
 
 def gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
@@ -147,7 +146,24 @@ def gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Ten
     float32 weight gradients.  As with any backward pass, a capture into a graph
     must not meet leaves of an eager graph that is still alive; that is refused
     where this function made the eager graph."""
-    if torch.is_grad_enabled() and (x.requires_grad or w13.requires_grad or w2.requires_grad):
-        nodes = _leaf_nodes((x, w13, w2), x.device) if x.is_cuda else None  # noqa: F841 (held over the call)
+    if not (torch.is_grad_enabled() and (x.requires_grad or w13.requires_grad or w2.requires_grad)):
+        return gated_ffn_forward(x, w13, w2, gate_up=False)[0]
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        with torch.cuda.device(x.device):
+            return gated_ffn(x, w13, w2)
+    _sizes(x, w13, w2)
+    if torch.cuda.is_current_stream_capturing():
+        # The captured backward would make the default stream, on which an eager
+        # graph's nodes were born, wait within the capture; it cannot be part of
+        # one, and the process ends.
+        for t in (x, w13, w2):
+            if t.requires_grad and t.is_leaf and _EAGER in get_gradient_edge(t).node.metadata:
+                raise RuntimeError("gated_ffn is being captured while an eager graph of one of its leaves lives: "
+                                   "release that graph first, or capture gated_ffn_forward and gated_ffn_backward")
         return _GatedFFN.apply(x, w13, w2)
-    return gated_ffn_forward(x, w13, w2, gate_up=False)[0]
+    y = _GatedFFN.apply(x, w13, w2)
+    if current_raw_stream(x.device.index) == 0:
+        for node, _ in y.grad_fn.next_functions:
+            if node is not None and node.name() == "torch::autograd::AccumulateGrad":
+                node.metadata[_EAGER] = True
+    return y
