@@ -3,7 +3,9 @@
     block = MoEBlock(norm_weight, router, layer)
     out, residual = block.forward(attention_out, residual)
 
-``out`` is what the next layer adds to ``residual``.
+``out`` is what the next layer adds to ``residual``.  With a shared expert,
+``MoEBlock(norm_weight, router, layer, shared=MoESharedExpert(...))``, it is the
+sum of the routed experts' and the shared one's.
 """
 
 from __future__ import annotations
@@ -15,6 +17,7 @@ import torch
 from . import _lib as L
 from ._args import check
 from .layer import MoELayer
+from .linear import MoESharedExpert
 from .norm import rms_norm_quant
 from .router import MoERouter
 
@@ -39,10 +42,13 @@ FEW_TOKENS_MX, FEW_ROUTES_MX = 12, 40
 
 class MoEBlock:
     """``router`` has to give local expert ids of ``layer`` (its
-    local_experts are the layer's).  FP8 layers take the norm's e4m3 rows,
-    MXFP8 layers its BF16 rows, which the router reads in both cases."""
+    local_experts are the layer's).  FP8 layers and the shared expert take the
+    norm's e4m3 rows, MXFP8 layers its BF16 rows, which the router reads in all
+    cases.  Where a token's experts lie on several GPUs, the block of one of them
+    has the shared expert."""
 
-    def __init__(self, norm_weight: torch.Tensor, router: MoERouter, layer: MoELayer, *, eps: float = 1e-6):
+    def __init__(self, norm_weight: torch.Tensor, router: MoERouter, layer: MoELayer, *, eps: float = 1e-6,
+                 shared: Optional[MoESharedExpert] = None):
         if router.hidden != layer.hidden or router.top_k != layer.top_k:
             raise ValueError(f"router (hidden {router.hidden}, top_k {router.top_k}) and layer (hidden "
                              f"{layer.hidden}, top_k {layer.top_k}) do not fit")
@@ -51,7 +57,10 @@ class MoEBlock:
                              f"{layer.cfg.num_experts}")
         if router.device != layer.workspace.device:
             raise ValueError(f"router on device {router.device}, layer on {layer.workspace.device}")
-        self.norm_weight, self.router, self.layer, self.eps = norm_weight, router, layer, eps
+        if shared is not None and (shared.hidden != layer.hidden or shared.device != router.device):
+            raise ValueError(f"shared expert (hidden {shared.hidden}, device {shared.device}) and layer (hidden "
+                             f"{layer.hidden}, device {router.device}) do not fit")
+        self.norm_weight, self.router, self.layer, self.eps, self.shared = norm_weight, router, layer, eps, shared
         self.fp8 = layer.cfg.act_format == L.MOE_ACT_E4M3_1X128
         tokens, routes = FEW_TOKENS_MX, FEW_ROUTES_MX
         if self.fp8:
@@ -64,12 +73,13 @@ class MoEBlock:
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """x: bfloat16 [T, H]; residual: [T, H] or None.  Returns the experts'
-        output (bfloat16 [T, H]) and x + residual.  The optional int32
+        output (bfloat16 [T, H], the shared expert's added to the routed ones'
+        rounded sum) and x + residual.  The optional int32
         ``status`` word ([1]) receives the call's MOE_DEV_* bits
         (``layer.status()`` has those of stage + forward only)."""
         if status is not None:
             check(status, "status", (1,), (torch.int32,), self.router.device)
-        n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8, bf16=True)
+        n = rms_norm_quant(x, self.norm_weight, residual, eps=self.eps, codes=self.fp8 or self.shared is not None, bf16=True)
         idx, w = self.router.route(n.y)
         rows, scale = (n.codes, n.scale) if self.fp8 else (n.y, None)
         if x.shape[0] <= self.few:
@@ -79,4 +89,6 @@ class MoEBlock:
             self.layer.forward()
             if status is not None:
                 status.copy_(self.layer.region("status", torch.int32)[:1])
+        if self.shared is not None:
+            out = self.shared.forward(n.codes, n.scale, add=out, out=out)
         return out, n.residual
