@@ -40,13 +40,14 @@ def test_matmul_without_rows_launches_nothing():
 
 
 def test_workspace_has_to_be_large_enough_and_aligned():
-    m_, n, k = 100, 200, 4096
+    m_, n, k = 300, 7168, 7168  # K in parts
     need = L.moe_fp8_matmul_workspace_query(m_, n, k)
     assert need > 0
-    call = dict(MATMUL, m=m_, n=n, k=k, x_stride=k, w_stride=k, w=32 << 20, add=0)
-    for kw, status in ((dict(ws_bytes=need - 1, workspace=64 << 20), L.MOE_ERR_WORKSPACE_TOO_SMALL),
+    call = dict(MATMUL, m=m_, n=n, k=k, x_stride=k, w_stride=k, w=32 << 20, add=0, w_scale=128 << 20, x_scale=129 << 20,
+                out=130 << 20, out_stride=n)
+    for kw, status in ((dict(ws_bytes=need - 1, workspace=256 << 20), L.MOE_ERR_WORKSPACE_TOO_SMALL),
                        (dict(ws_bytes=need, workspace=0), INVALID),
-                       (dict(ws_bytes=need, workspace=(64 << 20) + 16), INVALID)):
+                       (dict(ws_bytes=need, workspace=(256 << 20) + 16), INVALID)):
         with pytest.raises(L.MoEError) as e:
             L.moe_fp8_matmul(**{**call, **kw})
         assert e.value.status == status
