@@ -276,7 +276,7 @@ void launch_few(const Args& a, hipStream_t s) {
   if constexpr (MAX_MT > 1) {
     if (mt == 2) return narrow ? launch_few_as<L, EPI, 1, 2, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 2, 8, 2>(a, s);
     if (mt == 3) return narrow ? launch_few_as<L, EPI, 1, 3, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 3, 4, 3>(a, s);
-    if (mt == 4) return narrow ? launch_few_as<L, EPI, 1, 4, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 4, 4, 3>(a, s);
+    if (mt == 4) return narrow ? launch_few_as<L, EPI, 1, 4, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 4, 6, 2>(a, s);
   }
   return narrow ? launch_few_as<L, EPI, 1, 1, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 1, 8, 2>(a, s);
 }
