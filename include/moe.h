@@ -477,7 +477,7 @@ moe_status_t moe_router_destroy(moe_router_t* router);
  *  workspace  device, 256-byte aligned, at least the query's bytes (0 for many
  *             sizes: then it may be NULL), of this call alone until it is done.
  * k is a multiple of 16 and at most 65536, n at most 262144; the rows of x and
- * w are 16-byte aligned, with strides of whole 16 bytes below 2^21.  m 0
+ * w are 16-byte aligned, with strides of whole 16 bytes up to 2^21.  m 0
  * launches nothing.
  *
  * Sums over blocks are FP32, rounded once.  Up to 16 rows a block's sum is FP32
@@ -520,7 +520,7 @@ moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const float* x_scal
  *  h          device bfloat16 [T, I]: scratch, and for moe_ffn_backward.
  *  out        device bfloat16 [T, H], rows out_stride apart.
  * H and I are multiples of 8, at most 65536; pointers are 16-byte aligned and
- * strides whole 16 bytes, below 2^20; outputs share memory with nothing else.
+ * strides whole 16 bytes, up to 2^20; outputs share memory with nothing else.
  * Sums are FP32; h is rounded to bfloat16 between the products.  num_tokens 0
  * launches nothing. */
 moe_status_t moe_ffn_workspace_query(int32_t num_tokens, int32_t hidden, int32_t intermediate,

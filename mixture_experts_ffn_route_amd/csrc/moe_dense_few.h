@@ -10,7 +10,7 @@
 namespace moe {
 namespace dense {
 
-enum { kBf16 = 0, kCodes = 1, kQuant = 2 };  // L: bfloat16; e4m3 codes; float32 rows, quantised as they are read
+enum { kBf16 = 0, kCodes = 1, kQuant = 2 };  // L: bfloat16; e4m3 codes; float32 rows, quantised as they are read (up to 16)
 
 // 8 codes -> 8 bfloat16, exact
 __device__ __forceinline__ v8bf widen_fp8(uint32_t lo, uint32_t hi) {
@@ -20,32 +20,6 @@ __device__ __forceinline__ v8bf widen_fp8(uint32_t lo, uint32_t hi) {
   const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, false);
   const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, true);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-struct Line {
-  u32x4 c[2];
-};
-// e4m3 codes and scale of 32 float32 values of a row, the other 96 of whose block
-// the lanes l ^ 16, l ^ 32 and l ^ 48 hold.
-__device__ __forceinline__ Line quant_line(const float* row, float& scale) {
-  float v[32];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const v4f f = reinterpret_cast<const v4f*>(row)[i];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[4 * i + e] = f[e];
-      top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
-    }
-  }
-  top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-  scale = __uint_as_float(top) / kE4m3Max;
-  Line r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r.c[i >> 2][i & 3] = quant4(v + 4 * i, scale);
-  return r;
 }
 
 // RB: blocks of 16 rows of R (SwiGLU: 2, gate rows and up rows, or 1, 8 of each);
@@ -60,8 +34,8 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluF32, kFp8 = L != kBf16, kHalves = kPair && RB == 1;
   static_assert(!kPair || RB <= 2, "gate and up rows");
   constexpr int COLS = kHalves ? 8 : kPair ? 16 : 16 * RB;  // of the result, per workgroup
-  constexpr int LT = L == kQuant ? 0 : MT;                  // blocks of L in a slot
-  constexpr int SLOT = (RB + LT) * 2048 + (L == kCodes ? 256 : 0);
+  constexpr int SLOT = (RB + MT) * 2048 + (kFp8 ? 256 : 0);
+  constexpr int LT = L == kQuant ? 0 : MT;                  // blocks of L that DMA fetches
   constexpr int LOADS = 2 * (RB + LT) + (L == kCodes ? 1 : 0);
   constexpr int RING = WAVES * DEPTH * SLOT, PART = WAVES * RB * MT * 1024;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[RING > PART ? RING : PART];
@@ -128,7 +102,7 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) dma16_at(from(lbase, loff[t][h], h), to + (RB + t) * 2048 + h * 1024);
     }
-    if constexpr (L == kCodes) dma4(a.ls + (int64_t)m0 * a.kbs + kb, soff, to + (RB + LT) * 2048);
+    if constexpr (L == kCodes) dma4(a.ls + (int64_t)m0 * a.kbs + kb, soff, to + (RB + MT) * 2048);
   };
 
   // The weight scales of each block of R, which lies in one scale block (kHalves:
@@ -153,11 +127,24 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
   int slot = 0;
   for (int i = 0; i < count; ++i) {
     const int kb = wave + i * WAVES;
-    Line xq;
-    float xs = 0.f;
     if constexpr (L == kQuant) {
-      const int m = min(m0 + (lane & 15), a.m - 1);
-      xq = quant_line(reinterpret_cast<const float*>(a.l + m * a.l_stride) + kb * kLine + 32 * g, xs);
+      // this K-block of L's rows as codes and scales into the slot: four rows at a
+      // time, 16 lanes and 8 columns a lane each
+      lds_u8* to = ring + slot * SLOT + RB * 2048;
+      const int c = lane & 15;
+      for (int r0 = 0; r0 < rows; r0 += 4) {
+        const int r = r0 + (lane >> 4);
+        const float* p = reinterpret_cast<const float*>(a.l + min(m0 + r, a.m - 1) * a.l_stride) + kb * kLine + 8 * c;
+        const v4f lo = reinterpret_cast<const v4f*>(p)[0], hi = reinterpret_cast<const v4f*>(p)[1];
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        uint32_t top = 0;  // max |v| as bits: a NaN is larger than every number
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        const float scale = __uint_as_float(row16_max(top)) / kE4m3Max;
+        *reinterpret_cast<__attribute__((address_space(3))) q_u32x2*>(to + chunk_at(r, c >> 1) + 8 * (c & 1)) =
+            quant8(v, scale);
+        if (c == 0) *reinterpret_cast<__attribute__((address_space(3))) float*>(to + MT * 2048 + 4 * r) = scale;
+      }
     }
     if (i + DEPTH <= count)
       wait_vm<LOADS * (DEPTH - 1)>();
@@ -177,15 +164,8 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
       for (int b = 0; b < RB; ++b) w[b] = frag_fp8(st, b, lane);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        v8i x;
-        float fx;
-        if constexpr (L == kQuant) {
-          x = __builtin_bit_cast(v8i, xq);
-          fx = xs;
-        } else {
-          x = frag_fp8(st, RB + t, lane);
-          fx = ((const __attribute__((address_space(3))) float*)(st + (RB + LT) * 2048))[16 * t + (lane & 15)];
-        }
+        const v8i x = frag_fp8(st, RB + t, lane);
+        const float fx = ((const __attribute__((address_space(3))) float*)(st + (RB + MT) * 2048))[16 * t + (lane & 15)];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           v4f p = {0.f, 0.f, 0.f, 0.f};
@@ -278,7 +258,12 @@ void launch_few(const Args& a, hipStream_t s) {
     if (mt == 3) return narrow ? launch_few_as<L, EPI, 1, 3, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 3, 4, 3>(a, s);
     if (mt == 4) return narrow ? launch_few_as<L, EPI, 1, 4, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 4, 6, 2>(a, s);
   }
-  return narrow ? launch_few_as<L, EPI, 1, 1, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 1, 8, 2>(a, s);
+  // what is quantised first hides behind more waves (shared expert T=1 H=4096 I=8192
+  // 23.3 us with 16 waves, 25.6 with 8)
+  if constexpr (L == kQuant)
+    return narrow ? launch_few_as<L, EPI, 1, 1, 16, 1>(a, s) : launch_few_as<L, EPI, 2, 1, 16, 1>(a, s);
+  else
+    return narrow ? launch_few_as<L, EPI, 1, 1, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 1, 8, 2>(a, s);
 }
 
 }  // namespace dense

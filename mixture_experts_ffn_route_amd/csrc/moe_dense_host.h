@@ -54,7 +54,8 @@ inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, 
     const int64_t groups = (int64_t)cdiv(n, 32) * parts;
     const double us = groups < 200 ? 2.8 + rounds(2 * groups, 256) * (kbs * r.few[mt - 1] * r.narrow + 0.4)
                                    : 2.8 + rounds(groups, 256) * (kbs * r.few[mt - 1] + 0.4);
-    offer(us + (joined ? join(1) : 0.0), Plan{0, 0, 1});
+    if (parts <= 65535)  // the grid's second dimension
+      offer(us + (joined ? join(1) : 0.0), Plan{0, 0, 1});
   }
   for (int s = 1; s <= 16 && (s == 1 || (split && kbs >= 2 * s)); ++s) {
     const int kb = cdiv(kbs, s);

@@ -225,3 +225,25 @@ def test_in_place_change_of_a_saved_weight_is_refused(m):
     w13.add_(1.0)
     with pytest.raises(RuntimeError, match="inplace"):
         y.backward(dy)
+
+
+def test_offsets_beyond_32_bits(m):
+    """2.5 GB of rows, of which a few are not zero: their outputs and the
+    gradients are those of these rows by themselves."""
+    t, h, i = 160000, 8192, 136
+    few, w13, w2, dy_few = D.ffn_inputs(70, h, i, 31)
+    x = torch.zeros(t, h, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(t, h, dtype=torch.bfloat16, device="cuda")
+    at = torch.cat((torch.arange(35), t - 35 + torch.arange(35))).cuda()
+    x[at], dy[at] = few, dy_few
+    want = D.ffn64(few, w13, w2, dy_few)
+    leaves = [v.requires_grad_(True) for v in (x, w13, w2)]
+    y = m.gated_ffn(*leaves)
+    dx, dw13, dw2 = torch.autograd.grad(y, leaves, dy)
+    D.assert_within(y.detach()[at], *want["y"], "y")
+    D.assert_within(dx[at], *want["dx"], "dx")
+    D.assert_within(dw13, *D.rounded(*want["dw13"]), "dw13")
+    D.assert_within(dw2, *D.rounded(*want["dw2"]), "dw2")
+    rest = torch.ones(t, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert not y.detach()[rest].any() and not dx[rest].any()

@@ -177,3 +177,18 @@ def test_two_streams_at_once(m):
                 outs.append(m.fp8_matmul(x, xs, w, ws))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_offsets_beyond_32_bits(m):
+    """5 GB of rows: the last ones equal the same rows by themselves, which take
+    the few-row form, within both forms' bounds."""
+    rows, n, k = 300000, 64, 16384
+    x = torch.randint(0, 120, (rows, k), dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    xs = torch.rand(rows, k // 128, generator=gen, device="cuda")
+    _, _, w, ws = D.fp8_inputs(1, n, k, 2)
+    got = m.fp8_matmul(x, xs, w, ws)
+    for at in (0, rows // 2, rows - 70):
+        sl = slice(at, at + 70)
+        want, bound = D.rounded(*D.product64(x[sl].contiguous(), xs[sl].contiguous(), w, ws))
+        D.assert_within(got[sl], want, bound, f"rows from {at}")
