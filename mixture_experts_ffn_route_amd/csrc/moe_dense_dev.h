@@ -92,7 +92,7 @@ __device__ __forceinline__ float scalar_f32(const float* p) {
 // 16 bytes of zeros that lanes past the end of K read instead
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
-// MOE_DENSE_* layouts
+// how an operand lies in memory
 enum { kKin = 0, kKout = 1 };
 
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }

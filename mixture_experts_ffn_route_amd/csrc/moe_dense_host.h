@@ -71,16 +71,14 @@ inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, 
 }
 
 // `a` has its tiles.  One workgroup a CU: four stages; more: two.
-template <bool FP8, int LL, int LR, int BM, int BN, int EPI>
+template <bool FP8, int LL, int LR, int EPI>
 void launch_tile(const Args& a, int splits, hipStream_t s) {
   const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
   const dim3 grid(tile_grid(tiles), splits);
-  if constexpr (BM + BN > 256)  // one workgroup a CU in any case
-    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 3, 4>), grid, dim3(512), 0, s, a);
-  else if ((tiles + 7) / 8 * splits <= 32)
-    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 4, 4>), grid, dim3(512), 0, s, a);
+  if ((tiles + 7) / 8 * splits <= 32)
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, EPI, 4, 4>), grid, dim3(512), 0, s, a);
   else
-    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, BM, BN, EPI, 2, 2>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<FP8, LL, LR, EPI, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <int EPI>
@@ -89,13 +87,26 @@ void launch_join(const Args& a, const float* part, int splits, int pitch, hipStr
   hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, part, splits, pitch);
 }
 
-// Whether two strided areas of rows share memory, by their first and last byte.
-inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+// Rows of `width` bytes, `stride` bytes apart.
+struct Area {
+  const void* p;
+  int64_t rows, stride, width;
+};
+inline Area area(const void* p, int64_t rows, int64_t stride, int64_t cols, int size) {
+  return Area{p, rows, rows > 1 ? stride * size : cols * size, cols * size};
 }
-inline int64_t span(int64_t rows, int64_t stride, int64_t cols, int size) {
-  return rows > 0 ? ((rows - 1) * stride + cols) * size : 0;
+// Whether two areas may share memory: by their first and last bytes, but not
+// columns of one buffer beside each other.
+inline bool overlap(const Area& a, const Area& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  if (x >= y + (uintptr_t)((b.rows - 1) * b.stride + b.width) || y >= x + (uintptr_t)((a.rows - 1) * a.stride + a.width))
+    return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
+    const int64_t s = a.stride, d = (((int64_t)(y - x)) % s + s) % s;  // b's columns from a's first
+    return !(d >= a.width && d + b.width <= s);
+  }
+  return true;
 }
 
 // Bytes from one memory line of an operand to the next: offsets in a tile stay
@@ -109,7 +120,7 @@ inline moe_status_t check_out(int32_t m, int64_t n, const void* add, int64_t add
     return fail(MOE_ERR_INVALID_ARG, "out_stride %lld or add_stride %lld below %lld", (long long)out_stride,
                 (long long)add_stride, (long long)n);
   if (add && !(add == out && (m == 1 || add_stride == out_stride)) &&
-      overlap(add, span(m, add_stride, n, 2), out, span(m, out_stride, n, 2)))
+      overlap(area(add, m, add_stride, n, 2), area(out, m, out_stride, n, 2)))
     return fail(MOE_ERR_INVALID_ARG, "add and out overlap without being the same rows");
   return MOE_OK;
 }

@@ -1,5 +1,5 @@
-// Dense products on 128 x 128 (or 64 x 256) tiles: the simple form, for mid-size
-// batches, and the sums of products split over K.
+// Dense products on 128 x 128 tiles, for mid-size batches, and the sums of products
+// split over K.
 //
 // WN (n) x 2 (m) waves; a K-block of 128 bytes is one stage of a ring, of
 // four where a CU has one workgroup, of two where it has two, whose loads then
@@ -108,11 +108,11 @@ __device__ __forceinline__ void store_dswiglu(const Args& a, int64_t m, int c, c
   *reinterpret_cast<u32x2*>(o + a.n) = pack4(du);
 }
 
-template <bool FP8, int LL, int LR, int BM, int BN, int EPI, int STAGES, int WN>
+template <bool FP8, int LL, int LR, int EPI, int STAGES, int WN>
 __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) {
-  constexpr bool kPair = EPI == kSwiglu || EPI == kSwigluQ;
+  constexpr bool kPair = EPI == kSwiglu;
   static_assert(!FP8 || (LL == kKin && LR == kKin), "e4m3 has no transposing read here");
-  constexpr int WAVES = 2 * WN, NB = BN / 16 / WN, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
+  constexpr int BM = 128, BN = 128, WAVES = 2 * WN, NB = BN / 16 / WN, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
   constexpr int NP = (BN + BM) / 8 / WAVES, NPR = BN / 8 / WAVES;  // DMA pieces per wave and K-block, of R
   constexpr int STAGE = (BN + BM) * kLine + (FP8 ? BM * 4 : 0);
   constexpr int LOADS = NP + (FP8 ? 1 : 0);
@@ -259,62 +259,27 @@ __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Arg
 
   const int lm = m0 + wm * (BM / 2) + (lane & 15);  // this lane's row of block t: + 16 t
   const int lc = 4 * (lane >> 4);
-  if constexpr (EPI == kSwigluQ) {
-    static_assert(EPI != kSwigluQ || HN == 128, "one scale block of h per tile");
-    __syncthreads();  // the ring has been read
-    __attribute__((address_space(3))) uint32_t* top_s = (__attribute__((address_space(3))) uint32_t*)ring_lds;
-    float h[NB / 2][TB][4];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      uint32_t top = 0;  // max |h| as bits: a NaN is larger than every number
+  for (int t = 0; t < TB; ++t) {
+    const int64_t m = lm + t * 16;
+    if (m >= a.m) continue;
 #pragma unroll
-      for (int i = 0; i < NB / 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[i][t][e] = swiglu(acc[i][t][e], acc[NB / 2 + i][t][e]);
-          top = max(top, __float_as_uint(h[i][t][e]) & 0x7fffffffu);
-        }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-      if (lane < 16) top_s[wn * BM + wm * (BM / 2) + t * 16 + lane] = top;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const int r = wm * (BM / 2) + t * 16 + (lane & 15), m = m0 + r;
-      if (m >= a.m) continue;
-      uint32_t top = 0;
-#pragma unroll
-      for (int w = 0; w < WN; ++w) top = max(top, top_s[w * BM + r]);
-      const float s = __uint_as_float(top) / kE4m3Max;
-      if (wn == 0 && lane < 16) a.hs[(int64_t)m * (a.n / 128) + nt] = s;
-#pragma unroll
-      for (int i = 0; i < NB / 2; ++i)
-        *reinterpret_cast<uint32_t*>(a.hq + (int64_t)m * a.n + n0 + wn * (HN / WN) + i * 16 + lc) = quant4(h[i][t], s);
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const int64_t m = lm + t * 16;
-      if (m >= a.m) continue;
-#pragma unroll
-      for (int i = 0; i < (kPair ? NB / 2 : NB); ++i) {
-        const int c = n0 + (i < NB / 2 ? 0 : HN) + r_block(i) * 16 + lc;
-        const v4f v = acc[i][t];
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        if constexpr (EPI == kOut) {
-          store_out(a, m, c, f);
-        } else if constexpr (EPI == kOutF32) {
-          store_f32(a.outf + m * a.n + c, c, a.n, a.vec, a.accumulate, f);
-        } else if constexpr (EPI == kPart) {
-          if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = v;
-        } else if constexpr (EPI == kSwiglu) {
-          const v4f w = acc[NB / 2 + i][t];
-          const float u[4] = {w[0], w[1], w[2], w[3]};
-          store_swiglu(a, m, c, f, u);
-        } else {
-          store_dswiglu(a, m, c, f);
-        }
+    for (int i = 0; i < (kPair ? NB / 2 : NB); ++i) {
+      const int c = n0 + (i < NB / 2 ? 0 : HN) + r_block(i) * 16 + lc;
+      const v4f v = acc[i][t];
+      const float f[4] = {v[0], v[1], v[2], v[3]};
+      if constexpr (EPI == kOut) {
+        store_out(a, m, c, f);
+      } else if constexpr (EPI == kOutF32) {
+        store_f32(a.outf + m * a.n + c, c, a.n, a.vec, a.accumulate, f);
+      } else if constexpr (EPI == kPart) {
+        if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = v;
+      } else if constexpr (EPI == kSwiglu) {
+        const v4f w = acc[NB / 2 + i][t];
+        const float u[4] = {w[0], w[1], w[2], w[3]};
+        store_swiglu(a, m, c, f, u);
+      } else {
+        store_dswiglu(a, m, c, f);
       }
     }
   }

@@ -54,7 +54,7 @@ void launch_plan(Args a, const Plan& p, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, EPI == kSwiglu ? 64 : 128);
   a.kb_per_split = p.splits > 1 ? cdiv(a.kbs, p.splits) : a.kbs;
-  launch_tile<false, LL, LR, 128, 128, EPI>(a, p.splits, s);
+  launch_tile<false, LL, LR, EPI>(a, p.splits, s);
 }
 
 // A product of L (K inside) and R, whose result has n columns, into EPI (SwiGLU:
@@ -97,18 +97,14 @@ moe_status_t check_rows(const char* name, const void* p, int64_t stride, int64_t
   return MOE_OK;
 }
 
-struct Area {
-  const void* p;
-  int64_t bytes;
-};
 // Outputs share memory with no other area.
 moe_status_t check_apart(const Area* outs, int n_outs, const Area* ins, int n_ins) {
   for (int i = 0; i < n_outs; ++i) {
     for (int j = 0; j < n_ins; ++j)
-      if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+      if (overlap(outs[i], ins[j]))
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input");
     for (int j = 0; j < i; ++j)
-      if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+      if (overlap(outs[i], outs[j]))
         return fail(MOE_ERR_INVALID_ARG, "two outputs overlap");
   }
   return MOE_OK;
@@ -156,9 +152,9 @@ extern "C" moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const v
   if ((st = check_rows("w2", w2, intermediate, 1, intermediate)) != MOE_OK) return st;
   if ((st = check_rows("h", h, intermediate, 1, intermediate)) != MOE_OK) return st;
   if ((uintptr_t)gate_up & 15) return fail(MOE_ERR_INVALID_ARG, "gate_up must be 16-byte aligned");
-  const int64_t weights = (int64_t)hidden * intermediate * 2, rows = (int64_t)m * intermediate * 2;
-  const Area outs[] = {{out, span(m, out_stride, hidden, 2)}, {h, rows}, {gate_up, 4 * rows}};
-  const Area ins[] = {{x, span(m, x_stride, hidden, 2)}, {w13, 2 * weights}, {w2, weights}};
+  const int64_t weights = (int64_t)hidden * intermediate, rows = (int64_t)m * intermediate;
+  const Area outs[] = {area(out, m, out_stride, hidden, 2), area(h, 1, 0, rows, 2), area(gate_up, 1, 0, 2 * rows, 4)};
+  const Area ins[] = {area(x, m, x_stride, hidden, 2), area(w13, 1, 0, 2 * weights, 2), area(w2, 1, 0, weights, 2)};
   if ((st = check_apart(outs, 3, ins, 3)) != MOE_OK) return st;
   if ((st = check_workspace(workspace, ws_bytes, forward_bytes(m, hidden, intermediate))) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -216,11 +212,12 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
     if (dw2 && (st = check_rows("h", h, intermediate, 1, intermediate)) != MOE_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, backward_bytes(m, hidden, intermediate, &first))) != MOE_OK) return st;
   }
-  const int64_t weights = (int64_t)hidden * intermediate, rows = (int64_t)m * intermediate * 2;
+  const int64_t weights = (int64_t)hidden * intermediate, rows = (int64_t)m * intermediate;
   const int size = dw_type == MOE_TYPE_F32 ? 4 : 2;
-  const Area outs[] = {{dx, span(m, dx_stride, hidden, 2)}, {dw13, 2 * weights * size}, {dw2, weights * size}};
-  const Area ins[] = {{dy, span(m, dy_stride, hidden, 2)}, {x, span(m, x_stride, hidden, 2)}, {w13, 4 * weights},
-                      {w2, 2 * weights}, {gate_up, 4 * rows}, {h, rows}};
+  const Area outs[] = {area(dx, m, dx_stride, hidden, 2), area(dw13, 1, 0, 2 * weights, size),
+                       area(dw2, 1, 0, weights, size)};
+  const Area ins[] = {area(dy, m, dy_stride, hidden, 2),  area(x, m, x_stride, hidden, 2), area(w13, 1, 0, 2 * weights, 2),
+                      area(w2, 1, 0, weights, 2), area(gate_up, 1, 0, 2 * rows, 4), area(h, 1, 0, rows, 2)};
   if ((st = check_apart(outs, 3, ins, 6)) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* dgu = static_cast<uint8_t*>(workspace);

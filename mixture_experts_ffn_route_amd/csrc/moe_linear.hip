@@ -61,7 +61,7 @@ void launch_plan(Args a, const Plan& p, hipStream_t s) {
   a.m_tiles = cdiv(a.m, 128);
   a.n_tiles = cdiv(a.n, 128);
   a.kb_per_split = cdiv(a.kbs, p.splits);
-  launch_tile<true, kKin, kKin, 128, 128, EPI>(a, p.splits, s);
+  launch_tile<true, kKin, kKin, EPI>(a, p.splits, s);
 }
 
 void product(Args a, float* parts, hipStream_t s) {
@@ -163,9 +163,10 @@ extern "C" moe_status_t moe_fp8_matmul(const uint8_t* x, int64_t x_stride, const
   if (!x_scale || !w_scale || (((uintptr_t)x_scale | (uintptr_t)w_scale) & 3))
     return fail(MOE_ERR_INVALID_ARG, "x_scale and w_scale must be non-NULL and 4-byte aligned");
   if ((st = check_out(m, n, add_bf16, add_stride, out_bf16, out_stride)) != MOE_OK) return st;
-  const int64_t out_bytes = span(m, out_stride, n, 2), kbs = cdiv(k, 128);
-  if (overlap(x, span(m, x_stride, k, 1), out_bf16, out_bytes) || overlap(w, span(n, w_stride, k, 1), out_bf16, out_bytes) ||
-      overlap(x_scale, m * kbs * 4, out_bf16, out_bytes) || overlap(w_scale, cdiv(n, 128) * kbs * 4, out_bf16, out_bytes))
+  const int64_t kbs = cdiv(k, 128);
+  const Area to = area(out_bf16, m, out_stride, n, 2);
+  if (overlap(to, area(x, m, x_stride, k, 1)) || overlap(to, area(w, n, w_stride, k, 1)) ||
+      overlap(to, area(x_scale, 1, 0, m * kbs, 4)) || overlap(to, area(w_scale, 1, 0, cdiv(n, 128) * kbs, 4)))
     return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
   if ((st = check_workspace(workspace, ws_bytes, parts_bytes(m, n, (int)kbs))) != MOE_OK) return st;
   Args a = {};
@@ -211,11 +212,11 @@ extern "C" moe_status_t moe_ffn_fp8(const uint8_t* x, int64_t x_stride, const fl
   if (!x_scale || !w13_scale || !w2_scale || (((uintptr_t)x_scale | (uintptr_t)w13_scale | (uintptr_t)w2_scale) & 3))
     return fail(MOE_ERR_INVALID_ARG, "the scales must be non-NULL and 4-byte aligned");
   if ((st = check_out(m, hidden, add_bf16, add_stride, out_bf16, out_stride)) != MOE_OK) return st;
-  const int64_t out_bytes = span(m, out_stride, hidden, 2), weights = (int64_t)hidden * intermediate;
-  if (overlap(x, span(m, x_stride, hidden, 1), out_bf16, out_bytes) || overlap(w13, 2 * weights, out_bf16, out_bytes) ||
-      overlap(w2, weights, out_bf16, out_bytes) || overlap(x_scale, (int64_t)m * (hidden / 128) * 4, out_bf16, out_bytes) ||
-      overlap(w13_scale, weights / 8192 * 4, out_bf16, out_bytes) ||
-      overlap(w2_scale, weights / 16384 * 4, out_bf16, out_bytes))
+  const int64_t weights = (int64_t)hidden * intermediate;
+  const Area to = area(out_bf16, m, out_stride, hidden, 2);
+  if (overlap(to, area(x, m, x_stride, hidden, 1)) || overlap(to, area(w13, 1, 0, 2 * weights, 1)) ||
+      overlap(to, area(w2, 1, 0, weights, 1)) || overlap(to, area(x_scale, 1, 0, (int64_t)m * (hidden / 128), 4)) ||
+      overlap(to, area(w13_scale, 1, 0, weights / 8192, 4)) || overlap(to, area(w2_scale, 1, 0, weights / 16384, 4)))
     return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
   const FfnLayout lay = ffn_layout(m, hidden, intermediate);
   if ((st = check_workspace(workspace, ws_bytes, lay.total())) != MOE_OK) return st;

@@ -24,6 +24,7 @@ MATMUL = dict(x=1 << 20, x_stride=256, x_scale=2 << 20, w=3 << 20, w_stride=256,
     (dict(x_stride=240), INVALID), (dict(x_stride=264), INVALID), (dict(w_stride=0), INVALID),
     (dict(w_stride=1 << 22), INVALID), (dict(out_stride=199), INVALID), (dict(add_stride=0), INVALID),
     (dict(add=6 << 20, add_stride=208), INVALID),        # over out with another stride
+    (dict(add=(6 << 20) + 200, add_stride=400, out_stride=400), INVALID),  # half over out's columns
     (dict(add=(6 << 20) + 400), INVALID),                # a row further
     (dict(out=(1 << 20) + 512), INVALID),                # over x
     (dict(out=(3 << 20) + 2), INVALID),                  # over w

@@ -124,6 +124,17 @@ def test_strided_rows(m, t):
     assert torch.equal(a, b)
 
 
+def test_rows_and_output_beside_each_other(m):
+    """Columns of one buffer that do not overlap."""
+    x, w13, w2, _ = D.ffn_inputs(70, 72, 40, 9)
+    wide = torch.zeros(70, 160, device="cuda").bfloat16()
+    wide[:, 8:80] = x
+    y, _, _ = m.gated_ffn_forward(wide[:, 8:80], w13, w2, out=wide[:, 80:152])
+    assert torch.equal(y, m.gated_ffn(x, w13, w2))
+    with pytest.raises(m.MoEError):
+        m.gated_ffn_forward(wide[:, 8:80], w13, w2, out=wide[:, 72:144])
+
+
 def test_no_tokens(m):
     x, w13, w2, dy = D.ffn_inputs(1, 72, 40, 8)
     leaves = [x[:0].clone().requires_grad_(True), w13.requires_grad_(True), w2.requires_grad_(True)]
