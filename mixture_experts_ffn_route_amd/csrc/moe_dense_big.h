@@ -13,7 +13,18 @@
 // its halves: there every wave holds the second half's fragments, so the stage
 // can take the next K-block but one, and the next K-block has landed.
 //
+// R has three stages of 32 KB and L two (with 128 rows of L three of 16 KB): the
+// loads of a K-block are issued over all of the one before, half of them two ahead.
+// All in the half behind the barrier, they hold up the MFMAs (T=16384 H=7168 I=2048
+// FC1 792 us against 776; in the first half of that 822).
+//
 // Workgroups stay: a tile's last K-blocks already load the next tile's first.
+//
+// The card's power bounds it in long runs: FC1 of T=16384 H=7168 I=2048 takes 705 us
+// at first (1.36 PFLOP/s) and 770 when the clock has come down to 1.8 GHz, where the
+// MFMAs are busy 72 % of the cycles.  Products with K outside run at the same rate
+// (dw13 of T=4096 2 I=4096 H=7168 256 us in 1.75 rounds of tiles): their LDS reads
+// have no conflicts either.
 #pragma once
 
 #include <type_traits>

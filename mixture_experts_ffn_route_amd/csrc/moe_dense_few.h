@@ -3,6 +3,15 @@
 // turn, each through a ring of its own in LDS, filled by DMA (no two waves share a
 // weight, so they never wait for each other), and their sums are joined through
 // LDS.
+//
+// Memory bounds it for one row: N=K=7168 (51 MB of e4m3 weights) 10.2 us with the
+// weights in no cache, 5.0 TB/s (a 2 GiB copy: 4.8); the BF16 block T=1 H=7168
+// I=2048 (88 MB) 17.9 us in two launches.  Those are with non-temporal loads of
+// the weights; with plain ones 11.7 and 19.3, though weights that stay in the last
+// cache then come faster (N=7168 K=2048 3.9 us against 4.5).  With 64 rows, whose
+// 12 KB a K-block the CUs load at 17 bytes a clock, 18 us.  Fragments loaded
+// straight into registers, 16 bytes of each of 16 rows four times a line, took
+// 14.5 us for one row and 47.8 for 64: the DMA asks for whole lines.
 #pragma once
 
 #include "moe_dense_tile.h"

@@ -4,6 +4,12 @@
 // WN (n) x 2 (m) waves; a K-block of 128 bytes is one stage of a ring, of
 // four where a CU has one workgroup, of two where it has two, whose loads then
 // run beside the other's MFMAs.
+//
+// Latency bounds it: a K-block takes 0.75 us with one workgroup a CU (LDS reads 0.35,
+// MFMAs 0.25, and a barrier between), 1.1 for two.  N=7168 K=2048 M=512 16.4 us;
+// with four waves in place of eight 18.6, with two stages in parts of K 25.
+// Fragments read one K-block ahead, between the MFMAs, were slower (24 us): with
+// branches around the loads the compiler no longer overlaps anything.
 #pragma once
 
 #include "moe_dense_dev.h"
