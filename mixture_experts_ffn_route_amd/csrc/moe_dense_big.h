@@ -220,30 +220,54 @@ __global__ __launch_bounds__(256, 1) void big_kernel(Args a) {
       for (int t = 0; t < TB; ++t) asm volatile("" : "+a"(acc[i][t]));
 
     const int m0 = mt_cur * BM, n0 = nt_cur * (kPair ? HN : BN);
-    const int lm = m0 + wm * (BM / 2) + (lane & 15), lc = n0 + wn * (HN / 2) + 4 * (lane >> 4);
+    const int g = lane >> 4, lm = m0 + wm * (BM / 2) + (lane & 15), lc = n0 + wn * (HN / 2) + 4 * g;
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
       const int64_t m = lm + t * 16;
       if (m < a.m) {
 #pragma unroll
         for (int i = 0; i < (kPair ? NB / 2 : NB); ++i) {
-          const int c = lc + (i < NB / 2 ? i * 16 : HN + (i - NB / 2) * 16);
-          if (c >= a.n) continue;
+          const int at = i < NB / 2 ? i * 16 : HN + (i - NB / 2) * 16;
+          const int c = lc + at;
           const v4f r = acc[i][t];
-          const float f[4] = {r[0], r[1], r[2], r[3]};
-          if constexpr (EPI == kOut) {
-            *reinterpret_cast<u32x2*>(a.out + m * a.out_stride + c) = pack4(f);
-          } else if constexpr (EPI == kPart) {
-            *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
+          if constexpr (EPI == kPart) {
+            if (c < a.n) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
           } else if constexpr (EPI == kOutF32) {
             v4f* o = reinterpret_cast<v4f*>(a.outf + m * a.n + c);
-            *o = a.accumulate ? *o + r : r;
-          } else if constexpr (EPI == kSwiglu) {
-            const v4f w = acc[NB / 2 + i][t];
-            const float u[4] = {w[0], w[1], w[2], w[3]};
-            store_swiglu(a, m, c, f, u);
-          } else {
-            store_dswiglu(a, m, c, f);
+            if (c < a.n) *o = a.accumulate ? *o + r : r;
+          } else if (i % 2 == 0) {  // two blocks: 8 columns a lane (n is a multiple of 8)
+            const int c16 = n0 + wn * (HN / 2) + at + 16 * (g & 1) + 8 * (g >> 1);
+            uint16_t* o = a.out + m * a.out_stride + c16;
+            u32x2 x[2], y[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const v4f q = acc[i + k][t];
+              float f[4] = {q[0], q[1], q[2], q[3]};
+              if constexpr (EPI == kSwiglu) {
+                const v4f w = acc[NB / 2 + i + k][t];
+                if (a.gu && c + 16 * k < a.n) {
+                  float* p = a.gu + m * 2 * (int64_t)a.n + c + 16 * k;
+                  *reinterpret_cast<v4f*>(p) = q;
+                  *reinterpret_cast<v4f*>(p + a.n) = w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = swiglu(q[e], w[e]);
+              } else if constexpr (EPI == kDswiglu) {
+                const float* p = a.gu + m * 2 * (int64_t)a.n + min(c + 16 * k, a.n - 4);
+                const v4f gate = *reinterpret_cast<const v4f*>(p), up = *reinterpret_cast<const v4f*>(p + a.n);
+                float du[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dswiglu(gate[e], up[e], q[e], f[e], du[e]);
+                y[k] = pack4(du);
+              }
+              x[k] = pack4(f);
+            }
+            const u32x4 first = join16(x[0], x[1]);
+            if (c16 < a.n) *reinterpret_cast<u32x4*>(o) = first;
+            if constexpr (EPI == kDswiglu) {
+              const u32x4 second = join16(y[0], y[1]);
+              if (c16 < a.n) *reinterpret_cast<u32x4*>(o + a.n) = second;
+            }
           }
         }
       }

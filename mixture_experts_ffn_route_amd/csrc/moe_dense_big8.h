@@ -26,7 +26,7 @@
 namespace moe {
 namespace dense {
 
-// CUT: K is no multiple of 128.  VEC: four columns are stored at once (kOut).
+// CUT: K is no multiple of 128.  VEC: eight columns are stored at once (kOut).
 // blockIdx.y: the part of K (kPart).
 template <int EPI, bool CUT, bool VEC, int BM>
 __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
@@ -247,36 +247,58 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
       wait_lds();
       barrier();  // top_s is read before the next tile's
     } else {
+      if constexpr (EPI == kOut && VEC) {
+        const int c16 = n0 + wn * 32 + 16 * (g & 1) + 8 * (g >> 1);  // this lane's 8 columns of a pair of blocks
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const int64_t m = lm + t * 16;
-        if (m < a.m) {
+        for (int t = 0; t < TB; ++t) {
+          const int64_t m = lm + t * 16;  // the lanes that exchange have one row: all or none store
+          if (m < a.m) {
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const int c = lc + (i < 2 ? i * 16 : HN + (i - 2) * 16);
-            const v4f r = acc[i][t];
-            float f[4] = {r[0], r[1], r[2], r[3]};
-            if constexpr (EPI == kPart) {
-              if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
-            } else if constexpr (VEC) {
-              if (c >= a.n) continue;
+            for (int h = 0; h < 2; ++h) {
+              const int c = c16 + h * HN;
+              v4f x = acc[2 * h][t], y = acc[2 * h + 1][t];
               if (a.add) {
-                float d[4];
-                unpack4(*reinterpret_cast<const u32x2*>(a.add + m * a.add_stride + c), d);
+                u32x2 dx, dy;
+                part16(*reinterpret_cast<const u32x4*>(a.add + m * a.add_stride + min(c, a.n - 8)), dx, dy);
+                float e[4], f[4];
+                unpack4(dx, e);
+                unpack4(dy, f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] += d[e];
+                for (int k = 0; k < 4; ++k) {
+                  x[k] += e[k];
+                  y[k] += f[k];
+                }
               }
-              *reinterpret_cast<u32x2*>(a.out + m * a.out_stride + c) = pack4(f);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (c + e < a.n)
-                  a.out[m * a.out_stride + c + e] = (uint16_t)f32_to_bf16_rne(
-                      a.add ? f[e] + bf16_to_f32(a.add[m * a.add_stride + c + e]) : f[e]);
+              const float p[4] = {x[0], x[1], x[2], x[3]}, q[4] = {y[0], y[1], y[2], y[3]};
+              const u32x4 o = join16(pack4(p), pack4(q));
+              if (c < a.n) *reinterpret_cast<u32x4*>(a.out + m * a.out_stride + c) = o;
             }
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+      } else {
+  #pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const int64_t m = lm + t * 16;
+          if (m < a.m) {
+  #pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const int c = lc + (i < 2 ? i * 16 : HN + (i - 2) * 16);
+              const v4f r = acc[i][t];
+              float f[4] = {r[0], r[1], r[2], r[3]};
+              if constexpr (EPI == kPart) {
+                if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
+              } else {
+  #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (c + e < a.n)
+                    a.out[m * a.out_stride + c + e] = (uint16_t)f32_to_bf16_rne(
+                        a.add ? f[e] + bf16_to_f32(a.add[m * a.add_stride + c + e]) : f[e]);
+              }
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     v = next(v + gridDim.x);

@@ -140,8 +140,11 @@ inline void set_out(Args& a, const void* add, int64_t add_stride, void* out, int
   a.out_stride = out_stride;
   a.add = static_cast<const uint16_t*>(add);
   a.add_stride = add_stride;
-  const bool strides = a.m == 1 || (out_stride % 4 == 0 && (!add || add_stride % 4 == 0));
-  a.vec = strides && !(((uintptr_t)out | (uintptr_t)add) & 7);
+  auto pieces = [&](int values) {
+    const bool strides = a.m == 1 || (out_stride % values == 0 && (!add || add_stride % values == 0));
+    return strides && !(((uintptr_t)out | (uintptr_t)add) & (2 * values - 1));
+  };
+  a.vec = pieces(8) && a.n % 8 == 0 ? 2 : pieces(4) ? 1 : 0;
 }
 
 }  // namespace dense

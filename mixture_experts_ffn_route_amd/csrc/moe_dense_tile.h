@@ -45,7 +45,7 @@ struct Args {
   float* outf;  // kOutF32: [m, n]; kPart: [splits, m, pitch]; kSwigluF32: [m, n]
   int32_t pitch;  // kPart: n up to whole 16 bytes
   int32_t accumulate;
-  int32_t vec;  // results of 4 columns may be stored at once
+  int32_t vec;  // results of 4 columns may be stored at once; 2: of 8, and n is a multiple of 8
   float* gu;  // [m, 2 n]
   uint8_t* hq;
   float* hs;
@@ -58,6 +58,28 @@ __device__ __forceinline__ void unpack4(u32x2 v, float f[4]) {
   f[3] = bf16_to_f32(v[1] >> 16);
 }
 __device__ __forceinline__ u32x2 pack4(const float f[4]) { return u32x2{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])}; }
+
+// Results of two neighbouring blocks of 16 columns as 16 bytes a lane: lane group g
+// of 16 lanes holds columns 4 g + [0, 4) of both, and after the exchange of rows
+// of lanes columns 8 (g / 2) + [0, 8) of block g % 2; and back.
+__device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ u32x4 join16(u32x2 a, u32x2 b) {
+  uint32_t a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
+  swap_rows(a0, b0);
+  swap_rows(a1, b1);
+  return u32x4{a0, a1, b0, b1};
+}
+__device__ __forceinline__ void part16(u32x4 v, u32x2& a, u32x2& b) {
+  uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3];
+  swap_rows(a0, b0);
+  swap_rows(a1, b1);
+  a = u32x2{a0, a1};
+  b = u32x2{b0, b1};
+}
 
 // Four results of row m, columns [c, c + 4) (those below n exist).
 __device__ __forceinline__ void store_out(const Args& a, int64_t m, int c, const float v[4]) {

@@ -42,7 +42,7 @@ void launch_big(Args a, int splits, hipStream_t s) {
   const bool cut = a.k % 128 != 0;
   if constexpr (EPI == kSwigluQ) {
     hipLaunchKernelGGL((big8_kernel<EPI, false, true, BM>), grid, block, 0, s, a);
-  } else if (EPI == kPart || (a.vec && a.n % 4 == 0)) {
+  } else if (EPI == kPart || a.vec == 2) {
     if (cut)
       hipLaunchKernelGGL((big8_kernel<EPI, true, true, BM>), grid, block, 0, s, a);
     else
