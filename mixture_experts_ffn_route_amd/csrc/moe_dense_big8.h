@@ -239,9 +239,9 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
         const float sc = __uint_as_float(top) / kE4m3Max;
         if (m < a.m) {
           if (wn == 0 && lane < 16) a.hs[m * (a.n / 128) + nt_cur] = sc;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<uint32_t*>(a.hq + m * a.n + lc + i * 16) = quant4(h[i][t], sc);
+          uint32_t q0 = quant4(h[0][t], sc), q1 = quant4(h[1][t], sc);
+          swap_rows(q0, q1);  // 8 columns of one of the two blocks
+          *reinterpret_cast<u32x2*>(a.hq + m * a.n + n0 + wn * 32 + 16 * (g & 1) + 8 * (g >> 1)) = u32x2{q0, q1};
         }
       }
       wait_lds();
