@@ -52,7 +52,7 @@ inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, 
   if (few) {
     const int blocks = cdiv(m, 16), parts = cdiv(blocks, 4), mt = cdiv(blocks, parts);
     const int64_t groups = (int64_t)cdiv(n, 32) * parts;
-    const double us = groups < 200 ? 2.8 + rounds(2 * groups, 256) * (kbs * r.few[mt - 1] * r.narrow + 0.4)
+    const double us = few_narrow(groups, mt) ? 2.8 + rounds(2 * groups, 256) * (kbs * r.few[mt - 1] * r.narrow + 0.4)
                                    : 2.8 + rounds(groups, 256) * (kbs * r.few[mt - 1] + 0.4);
     if (parts <= 65535)  // the grid's second dimension
       offer(us + (joined ? join(1) : 0.0), Plan{0, 0, 1});

@@ -51,6 +51,13 @@ struct Args {
   float* hs;
 };
 
+// Whether few_kernel takes half of its columns a workgroup: where the whole would
+// be `groups` workgroups, too few for the CUs, and twice as many run at once (two
+// a CU with one block of L rows, else one). N=K=5120, 160 groups of whole width:
+// M=24 9.7 us with half, 7.0 with whole; M=64 17.1 and 11.2; N=4160 K=2048 M=17 4.9
+// and 3.8. With one block of L rows half gains up to 200 groups.
+inline bool few_narrow(int64_t groups, int mt) { return mt == 1 ? groups < 200 : groups <= 128; }
+
 __device__ __forceinline__ void unpack4(u32x2 v, float f[4]) {
   f[0] = bf16_to_f32(v[0] & 0xffffu);
   f[1] = bf16_to_f32(v[0] >> 16);
