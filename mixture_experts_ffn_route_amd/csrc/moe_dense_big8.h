@@ -15,8 +15,8 @@
 // and its rows of L, group 1 its rows; a wave waits for its loads of the next
 // K-block at the end of its MFMA slot, and the barrier there publishes them.
 //
-// M=16384 N=K=7168: 745 us, 2.26 PFLOP/s.  The card's power bounds it in long runs
-// (750 us at first, 900 behind others of its kind at 1.6 GHz, the MFMAs busy 58 %
+// M=16384 N=K=7168: 727 us, 2.32 PFLOP/s.  The card's power bounds it in long runs
+// (740 us at first, 840 behind others of its kind at 1.6 GHz, the MFMAs busy 62 %
 // of the cycles); what the multiply-adds and LDS reads cost is seen without them:
 // 543 and 606 us in place of 895, without the DMA 757.
 #pragma once
