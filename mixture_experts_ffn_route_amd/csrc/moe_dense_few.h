@@ -257,11 +257,12 @@ void launch_few_as(const Args& a, hipStream_t s) {
 // MAX_MT 1: one block of L rows only (a.m <= 16).
 template <int L, int EPI, int MAX_MT = 4>
 void launch_few(const Args& a, hipStream_t s) {
-  const int blocks = (a.m + 15) / 16, parts = (blocks + 3) / 4, mt = (blocks + parts - 1) / parts;
   // 16 columns a workgroup, 8 with SwiGLU, where twice as many would leave CUs idle
   // (M=64 K=7168: N=7168 18 us with 32, 26 with 16; N=4096 T=1 7.1 with 16)
-  const int wide = EPI == kSwiglu || EPI == kSwigluF32 ? 16 : 32;
-  const bool narrow = few_narrow((int64_t)((a.n + wide - 1) / wide) * parts, mt);
+  const int wide = EPI == kSwiglu || EPI == kSwigluF32 ? 16 : 32, blocks = (a.m + 15) / 16;
+  const int64_t cols = (a.n + wide - 1) / wide;
+  const int mt = few_blocks(blocks, cols);
+  const bool narrow = few_narrow(cols * ((blocks + mt - 1) / mt), mt);
   if constexpr (MAX_MT > 1) {
     if (mt == 2) return narrow ? launch_few_as<L, EPI, 1, 2, 8, 2>(a, s) : launch_few_as<L, EPI, 2, 2, 8, 2>(a, s);
     if (mt == 3) return narrow ? launch_few_as<L, EPI, 1, 3, 4, 3>(a, s) : launch_few_as<L, EPI, 2, 3, 4, 3>(a, s);

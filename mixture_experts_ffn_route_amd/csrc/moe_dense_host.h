@@ -50,7 +50,7 @@ inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, 
     }
   };
   if (few) {
-    const int blocks = cdiv(m, 16), parts = cdiv(blocks, 4), mt = cdiv(blocks, parts);
+    const int blocks = cdiv(m, 16), mt = few_blocks(blocks, cdiv(n, 32)), parts = cdiv(blocks, mt);
     const int64_t groups = (int64_t)cdiv(n, 32) * parts;
     const double us = few_narrow(groups, mt) ? 2.8 + rounds(2 * groups, 256) * (kbs * r.few[mt - 1] * r.narrow + 0.4)
                                    : 2.8 + rounds(groups, 256) * (kbs * r.few[mt - 1] + 0.4);

@@ -57,6 +57,16 @@ struct Args {
 // M=24 9.7 us with half, 7.0 with whole; M=64 17.1 and 11.2; N=4160 K=2048 M=17 4.9
 // and 3.8. With one block of L rows half gains up to 200 groups.
 inline bool few_narrow(int64_t groups, int mt) { return mt == 1 ? groups < 200 : groups <= 128; }
+// Blocks of 16 L rows a workgroup of few_kernel takes, at most 4: fewer where the
+// workgroups of half width still run at once, `cols` of whole width for each part of L
+// (N=576 K=7168: M=64 11.5 us with 4, 5.3 with 1, M=128 9.2 and 5.6; BF16 block H=2048
+// I=768 T=64 11.3 and 7.3).
+inline int few_blocks(int blocks, int64_t cols) {
+  const int parts = (blocks + 3) / 4;
+  int mt = (blocks + parts - 1) / parts;
+  while (mt > 1 && 2 * cols * ((blocks + mt - 2) / (mt - 1)) <= 256) --mt;
+  return mt;
+}
 
 __device__ __forceinline__ void unpack4(u32x2 v, float f[4]) {
   f[0] = bf16_to_f32(v[0] & 0xffffu);
