@@ -481,7 +481,7 @@ moe_status_t moe_router_destroy(moe_router_t* router);
  * launches nothing.
  *
  * Sums over blocks are FP32, rounded once.  Up to 16 rows a block's sum is FP32
- * too; above, it is one FP8 MFMA's, whose error is at most 2^-10 of the block's
+ * too; above, it can be one FP8 MFMA's, whose error is at most 2^-10 of the block's
  * largest product.  A NaN code or scale makes its own row's (or weight's) results
  * NaN.  A scale product outside of float32's normal range loses bits as such a
  * number does. */
