@@ -9,6 +9,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 from torch.autograd.graph import get_gradient_edge
 
@@ -145,7 +146,11 @@ def gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Ten
     8.  Gradients are bfloat16; gated_ffn_backward also gives and accumulates
     float32 weight gradients.  As with any backward pass, a capture into a graph
     must not meet leaves of an eager graph that is still alive; that is refused
-    where this function made the eager graph."""
+    where this function made the eager graph.  Derivatives are those of reverse
+    mode: a tangent of forward mode on an input is refused."""
+    # The level by itself first: unpack_dual takes 0.5 us a tensor.
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w13, w2)):
+        raise NotImplementedError("gated_ffn has no forward-mode derivative")
     if not (torch.is_grad_enabled() and (x.requires_grad or w13.requires_grad or w2.requires_grad)):
         return gated_ffn_forward(x, w13, w2, gate_up=False)[0]
     if x.is_cuda and x.device.index != torch.cuda.current_device():
