@@ -106,6 +106,19 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2:
               int(accumulate))
 
 
+_MAX_STRIDE = 1 << 20  # of rows that the kernels read, in values
+
+
+def _readable_rows(dy: torch.Tensor) -> torch.Tensor:
+    """dy, or a copy of one that is broadcast or a view that the kernels do not
+    read."""
+    T, H = dy.shape
+    row = dy.stride(0)
+    if dy.stride(1) != 1 or dy.data_ptr() % 16 or (T > 1 and (row < H or row % 8 or row > _MAX_STRIDE)):
+        return dy.clone(memory_format=torch.contiguous_format)
+    return dy
+
+
 # Mark on a leaf's gradient node: an eager graph of the default stream holds it.
 _EAGER = "moe_gated_ffn_eager"
 
@@ -124,8 +137,7 @@ class _GatedFFN(torch.autograd.Function):
         x, w13, w2, gu, h = ctx.saved_tensors
         need_x, need_w13, need_w2 = ctx.needs_input_grad
         T, H = x.shape
-        if dy.stride(1) != 1 or dy.data_ptr() % 16 or (T > 1 and (dy.stride(0) < H or dy.stride(0) % 8)):
-            dy = dy.clone(memory_format=torch.contiguous_format)  # broadcast, or a view that the kernels do not read
+        dy = _readable_rows(dy)
         dx = empty_rows(T, H, torch.bfloat16, x.device) if need_x else None
         dw13 = empty_rows(w13.shape[0], H, torch.bfloat16, x.device) if need_w13 else None
         dw2 = empty_rows(H, w2.shape[1], torch.bfloat16, x.device) if need_w2 else None
