@@ -537,7 +537,8 @@ moe_status_t moe_ffn_forward(const void* x, int64_t x_stride, const void* w13, c
  *  dw13, dw2   device [2 I, H] and [H, I] of dw_type (MOE_TYPE_*), each or NULL.
  *              accumulate 1 (float32 only): they are added to what is there.
  * Inputs that the wanted gradients do not need may be NULL (x without dw13, w13
- * without dx, h without dw2, w2 and gate_up with dw2 alone).  dg and du are
+ * without dx, h without dw2, w2, gate_up and the workspace with dw2 alone, which
+ * takes 0 bytes of it).  dg and du are
  * rounded to bfloat16 between the products; sums are FP32, in an order that
  * depends on the sizes alone.  With no tokens the weight gradients are zero. */
 moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* w13,

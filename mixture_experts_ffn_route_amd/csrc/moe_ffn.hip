@@ -210,7 +210,8 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
     if ((dx || dw13) && (st = check_rows("w2", w2, intermediate, 1, intermediate)) != MOE_OK) return st;
     if ((dx || dw13) && (st = check_rows("gate_up", gate_up, intermediate, 1, intermediate)) != MOE_OK) return st;
     if (dw2 && (st = check_rows("h", h, intermediate, 1, intermediate)) != MOE_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, backward_bytes(m, hidden, intermediate, &first))) != MOE_OK) return st;
+    const size_t need = dx || dw13 ? backward_bytes(m, hidden, intermediate, &first) : 0;
+    if ((st = check_workspace(workspace, ws_bytes, need)) != MOE_OK) return st;
   }
   const int64_t weights = (int64_t)hidden * intermediate, rows = (int64_t)m * intermediate;
   const int size = dw_type == MOE_TYPE_F32 ? 4 : 2;

@@ -49,7 +49,7 @@ def _forward(x, w13, w2, out, gate_up: bool):
 def _backward(dy, x, w13, w2, gu, h, dx, dw13, dw2, dw_type: int, accumulate: int) -> None:
     """moe_ffn_backward of checked tensors on the current device."""
     (T, H), I, dev = x.shape, w2.shape[1], x.device
-    ws_bytes = L.moe_ffn_workspace_query(T, H, I)[1]
+    ws_bytes = 0 if dx is None and dw13 is None else L.moe_ffn_workspace_query(T, H, I)[1]
     ws = _workspace(ws_bytes, dev)
     L.moe_ffn_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), w13.data_ptr(), w2.data_ptr(), ptr(gu),
                        ptr(h), T, H, I, ptr(dx), 0 if dx is None else dx.stride(0), ptr(dw13), ptr(dw2), dw_type,

@@ -1,10 +1,12 @@
-"""Derivatives that the gated block cannot give are refused, not left out."""
+"""Edges of the gated block's derivatives: what it cannot give is refused, which
+gradients of the output it copies, what dw2 alone takes."""
 
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
 
 import mixture_experts_ffn_route_amd as m
+from mixture_experts_ffn_route_amd import _lib as L
 from mixture_experts_ffn_route_amd import ffn
 from tests import dense_util as D
 
@@ -70,4 +72,33 @@ def test_backward_takes_any_view(k):
     dy, _ = _views("cuda")[k]
     (want,) = torch.autograd.grad(m.gated_ffn(x, w13, w2), (x,), dy.clone(memory_format=torch.contiguous_format))
     (got,) = torch.autograd.grad(m.gated_ffn(x, w13, w2), (x,), dy)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("which", range(1, 8))
+def test_workspace_of_the_wanted_gradients(which, monkeypatch):
+    """dg | du and parts of K are dx's and dw13's; dw2 alone takes nothing."""
+    t, h, i = 40, 64, 48
+    x, w13, w2, dy = D.ffn_inputs(t, h, i, 0, device="cpu")
+    calls = []
+    monkeypatch.setattr(L, "moe_ffn_backward", lambda *args: calls.append(args))
+    monkeypatch.setattr(ffn, "current_raw_stream", lambda index: 0)
+    dx, dw13, dw2 = (v if which >> k & 1 else None for k, v in enumerate((x, w13, w2)))
+    ffn._backward(dy, x, w13, w2, None, None, dx, dw13, dw2, L.MOE_TYPE_BF16, 0)
+    workspace, ws_bytes = calls[0][-3:-1]
+    assert ws_bytes == (0 if which == 4 else L.moe_ffn_workspace_query(t, h, i)[1]) and bool(workspace) == bool(ws_bytes)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,h,i", [(3, 72, 40), (1000, 128, 2048)])
+def test_dw2_alone_without_a_workspace(t, h, i):
+    x, w13, w2, dy = D.ffn_inputs(t, h, i, 2)
+    _, gu, hid = m.gated_ffn_forward(x, w13, w2)
+    want, got = torch.empty_like(w2), torch.empty_like(w2)
+    m.gated_ffn_backward(dy, x, w13, w2, gu, hid, dx=torch.empty_like(x), dw2=want)
+    L.moe_ffn_backward(dy.data_ptr(), dy.stride(0), 0, 0, 0, 0, 0, hid.data_ptr(), t, h, i, 0, 0, 0, got.data_ptr(),
+                       L.MOE_TYPE_BF16, 0, 0, 0, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(got, want)
+    got.zero_()
+    m.gated_ffn_backward(dy, x, w13, w2, None, hid, dw2=got)
     assert torch.equal(got, want)
