@@ -49,7 +49,7 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
   // the tile whose loads are being issued
   const uint8_t *rb[2], *lb;
   const float* sxb;
-  int rrows[2], lrows, sblk[2];
+  int rrows[2], lrows;
   auto setup = [&](int mt, int nt) {
     const int m0 = mt * BM, n0 = nt * (kPair ? HN : BN);
 #pragma unroll
@@ -61,7 +61,6 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
       }
       rb[h] = a.r + row * a.r_stride;
       rrows[h] = min(left, HN);
-      sblk[h] = min(row / 128, blocks - 1);
     }
     lb = a.l + m0 * a.l_stride;
     lrows = min(a.m - m0, BM);
@@ -107,8 +106,10 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
   setup(mt, nt);
   const float *sw0, *sw1;  // the current tile's weight scales
   auto tile_scales = [&]() {
-    sw0 = a.rs + (int64_t)sblk[0] * a.kbs + kb0;
-    sw1 = a.rs + (int64_t)sblk[1] * a.kbs + kb0;
+    const int n0 = nt_cur * (kPair ? HN : BN);
+    const int n1 = kPair ? n0 + a.n : (a.n - n0 > HN ? n0 + HN : n0);
+    sw0 = a.rs + (int64_t)min(n0 / 128, blocks - 1) * a.kbs + kb0;
+    sw1 = a.rs + (int64_t)min(n1 / 128, blocks - 1) * a.kbs + kb0;
   };
   tile_scales();
   auto advance = [&]() {
@@ -277,11 +278,11 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-  #pragma unroll
+#pragma unroll
         for (int t = 0; t < TB; ++t) {
           const int64_t m = lm + t * 16;
           if (m < a.m) {
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < NB; ++i) {
               const int c = lc + (i < 2 ? i * 16 : HN + (i - 2) * 16);
               const v4f r = acc[i][t];
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
               if constexpr (EPI == kPart) {
                 if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = r;
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 4; ++e)
                   if (c + e < a.n)
                     a.out[m * a.out_stride + c + e] = (uint16_t)f32_to_bf16_rne(
@@ -305,12 +306,7 @@ __global__ __launch_bounds__(512, 1) void big8_kernel(Args a) {
     if (v >= ids) break;
     mt_cur = mt;
     nt_cur = nt;
-    {  // the weight scales of the tile that follows
-      const int n1 = nt * (kPair ? HN : BN);
-      const int r1 = kPair ? n1 + a.n : (a.n - n1 > HN ? n1 + HN : n1);
-      sw0 = a.rs + (int64_t)min(n1 / 128, blocks - 1) * a.kbs + kb0;
-      sw1 = a.rs + (int64_t)min(r1 / 128, blocks - 1) * a.kbs + kb0;
-    }
+    tile_scales();
   }
   wait_vm<0>();  // no load into LDS outlives the workgroup
 }

@@ -243,7 +243,7 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args a) {
       float h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e] = swiglu(v[0][e], v[1][e]);
-      store_f32(a.outf + (int64_t)m * a.n + c, c, a.n, 1, false, h);
+      store_f32(a.outf + (int64_t)m * a.n + c, c, a.n, false, h);
     }
   }
 }

@@ -117,18 +117,14 @@ __device__ __forceinline__ void store_out(const Args& a, int64_t m, int c, const
       if (c + i < a.n) o[i] = (uint16_t)f32_to_bf16_rne(d ? v[i] + bf16_to_f32(d[i]) : v[i]);
   }
 }
-__device__ __forceinline__ void store_f32(float* o, int c, int n, int vec, bool accumulate, const float v[4]) {
-  if (vec && c + 4 <= n) {
-    v4f f = {v[0], v[1], v[2], v[3]};
-    if (accumulate) f += *reinterpret_cast<const v4f*>(o);
-    *reinterpret_cast<v4f*>(o) = f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < n) o[i] = accumulate ? o[i] + v[i] : v[i];
-  }
+// n is a multiple of 4, and o aligned, in these
+__device__ __forceinline__ void store_f32(float* o, int c, int n, bool accumulate, const float v[4]) {
+  if (c >= n) return;
+  v4f f = {v[0], v[1], v[2], v[3]};
+  if (accumulate) f += *reinterpret_cast<const v4f*>(o);
+  *reinterpret_cast<v4f*>(o) = f;
 }
-// h, and g | u where wanted; n is a multiple of 4
+// h, and g | u where wanted
 __device__ __forceinline__ void store_swiglu(const Args& a, int64_t m, int c, const float g[4], const float u[4]) {
   if (c >= a.n) return;
   float h[4];
@@ -156,7 +152,7 @@ __device__ __forceinline__ void store_dswiglu(const Args& a, int64_t m, int c, c
 template <bool FP8, int LL, int LR, int EPI, int STAGES, int WN>
 __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Args a) {
   constexpr bool kPair = EPI == kSwiglu;
-  static_assert(!FP8 || (LL == kKin && LR == kKin), "e4m3 has no transposing read here");
+  static_assert(!FP8 || (LL == kKin && LR == kKin && !kPair), "e4m3: no transposing read here, gate | up through kPart");
   constexpr int BM = 128, BN = 128, WAVES = 2 * WN, NB = BN / 16 / WN, TB = BM / 32, HN = BN / 2;  // blocks of 16 per wave; rows of R in half a tile
   constexpr int NP = (BN + BM) / 8 / WAVES, NPR = BN / 8 / WAVES;  // DMA pieces per wave and K-block, of R
   constexpr int STAGE = (BN + BM) * kLine + (FP8 ? BM * 4 : 0);
@@ -224,10 +220,9 @@ __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Arg
   // e4m3: scales of the two halves' weight blocks
   const float* sw_p[2] = {nullptr, nullptr};
   if constexpr (FP8) {
-    const int blocks = ((kPair ? 2 * a.n : a.n) + 127) / 128;
+    const int blocks = (a.n + 127) / 128;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      sw_p[h] = a.rs + (int64_t)min((kPair ? n0 + h * a.n : n0 + h * HN) / 128, blocks - 1) * a.kbs;
+    for (int h = 0; h < 2; ++h) sw_p[h] = a.rs + (int64_t)min((n0 + h * HN) / 128, blocks - 1) * a.kbs;
   }
 
   v4f acc[NB][TB];
@@ -316,7 +311,7 @@ __global__ __launch_bounds__(WN * 128, STAGES == 2 ? 2 : 1) void tile_kernel(Arg
       if constexpr (EPI == kOut) {
         store_out(a, m, c, f);
       } else if constexpr (EPI == kOutF32) {
-        store_f32(a.outf + m * a.n + c, c, a.n, a.vec, a.accumulate, f);
+        store_f32(a.outf + m * a.n + c, c, a.n, a.accumulate, f);
       } else if constexpr (EPI == kPart) {
         if (c < a.pitch) *reinterpret_cast<v4f*>(a.outf + ((int64_t)blockIdx.y * a.m + m) * a.pitch + c) = v;
       } else if constexpr (EPI == kSwiglu) {

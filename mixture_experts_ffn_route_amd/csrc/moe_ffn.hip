@@ -267,7 +267,6 @@ extern "C" moe_status_t moe_ffn_backward(const void* dy, int64_t dy_stride, cons
     a.accumulate = accumulate;
     if (dw_type == MOE_TYPE_F32) {
       a.outf = static_cast<float*>(dw);
-      a.vec = 1;
       gradient<kOutF32>(a, s);
     } else {
       set_out(a, nullptr, 0, dw, a.n);
