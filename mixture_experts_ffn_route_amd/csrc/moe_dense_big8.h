@@ -15,7 +15,7 @@
 // and its rows of L, group 1 its rows; a wave waits for its loads of the next
 // K-block at the end of its MFMA slot, and the barrier there publishes them.
 //
-// M=16384 N=K=7168: 727 us, 2.32 PFLOP/s.  The card's power bounds it in long runs
+// M=16384 N=K=7168: 727 to 743 us, 2.27 to 2.32 PFLOP/s.  The card's power bounds it in long runs
 // (740 us at first, 840 behind others of its kind at 1.6 GHz, the MFMAs busy 62 %
 // of the cycles); what the multiply-adds and LDS reads cost is seen without them:
 // 543 and 606 us in place of 895, without the DMA 757.

@@ -32,10 +32,11 @@ struct Rates {
 // The form that is estimated to be fastest, from the sizes alone: rounds of
 // workgroups over the CUs (tiles: over the 32 of the XCD with the most), each as many K-blocks long as a part of K has, 4
 // us around them (few_kernel 2.8), and with parts of K a join of 3 us and their
-// bytes at 6.5 TB/s.  Measured over 32 <= m <= 4096 and the products of H=7168
-// I=2048, H=2048 I=768, N=1003 K=2000 and N=576 K=7168, each form for each m, the
-// choice takes at most 1.22 times the time of the fastest of them, and not more in
-// the mean.
+// bytes at 6.5 TB/s.  Measured at 16 m from 17 to 4096 for 8 products from N=576
+// K=7168 to N=K=7168 and the blocks of H=7168 I=2048 and H=2048 I=768, with few_kernel
+// and each tile with K in 1, 2, 4 and 8 parts forced in turn, the choice takes at most
+// 1.20 times the fastest form's time (shared expert H=2048 I=768 T=512 24.1 us, 20.0
+// with few_kernel), 1.007 times in the mean.
 // few: whether few_kernel can make it; split: whether K may be split; joined: a
 // join follows in any case but that of one part on tiles of 256 rows of R.
 inline Plan choose(int m, int n, int kbs, const Rates& r, bool few, bool split, bool joined) {

@@ -7,7 +7,7 @@
 //
 // Sums are FP32.  Rounded to bfloat16 between the products are h and dg | du,
 // which the MFMA takes.  g | u stay float32 for the gradients: as bfloat16 they
-// would save 16 T I bytes of traffic (1.5 % of a step at T=4096 H=7168 I=2048) and
+// would save 8 T I bytes of traffic (1.5 % of a step at T=4096 H=7168 I=2048) and
 // double the error that dx and dw13 have beside their own rounding (0.0030 in
 // place of 0.0024 of their root mean square, of which that rounding is 0.0017).
 #include <hip/hip_runtime.h>

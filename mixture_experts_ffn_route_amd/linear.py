@@ -49,7 +49,7 @@ def fp8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     x: e4m3 codes [M, K] (uint8 or float8_e4m3fn) with x_scale, float32
     [M, ceil(K/128)]; w: codes [N, K] with w_scale, float32 [ceil(N/128),
     ceil(K/128)].  K is a multiple of 16.  x, w, add and out may have a row
-    stride; out may be add."""
+    stride; out may be add.  For serving: no derivative, add's either."""
     if x.dim() != 2 or w.dim() != 2 or not x.is_cuda:
         raise ValueError("x and w must be 2-D device tensors")
     dev = x.device
@@ -95,7 +95,7 @@ class MoESharedExpert:
         """x: e4m3 codes [T, H] with x_scale, float32 [T, H/128], as
         rms_norm_quant gives them.  Returns the expert's output (``+ add``) in
         bfloat16 [T, H]; x, add and out may have a row stride, out may be
-        add."""
+        add.  For serving: no derivative, add's either."""
         dev, H = self.device, self.hidden
         index = dev.index
         if index != torch.cuda.current_device():
